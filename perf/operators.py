@@ -88,8 +88,9 @@ def draw(rng):
                     lens=lens)
     if op == "append":
         seqs = _log(rng, 1, 256)
-        return dict(op="append", tokens=_log(rng, seqs, 131072), seqs=seqs,
-                    ratio=rng.choice([1, 4, 128]), page_rows=page_rows, gap=rng.choice([0, 0, 8, 64]),
+        ratio = rng.choice([1, 4, 128])
+        return dict(op="append", tokens=_log(rng, seqs, 65536 if ratio == 1 else 131072),
+                    seqs=seqs, ratio=ratio, page_rows=page_rows, gap=rng.choice([0, 0, 8, 64]),
                     swa_cap=rng.choice([128, 160, 1000, 8192]), lens=lens)
     heads = rng.choice([1, 8, 16, 24, 32, 40, 64, 64, 64, 96, 128])
     seqs, new = _log(rng, 1, 256), rng.choice([1, 1, 1, 2, 4])
