@@ -366,6 +366,170 @@ csa_status_t csa_topk_noalloc(const csa_layout_t *layout, const csa_params_t *pa
                               const float *scores, int64_t ld_scores, int32_t *idx,
                               int32_t *n_sel, int32_t *dev_status, void *stream);
 
+/* Paged caches.  The calls above read one packed buffer per cache, where a
+ * sequence cannot grow without moving its neighbours.  A server keeps the
+ * same rows in pages of `page_rows` rows instead: a cache is a pool of
+ * num_pages pages, row r of page p at row p * page_stride + r of the pool
+ * (page_stride >= page_rows rows: the pages of several layers may be
+ * interleaved), and a block table names each sequence's pages in order, so
+ * that compressed block g of sequence b is row g % page_rows of page
+ * table[b, g / page_rows].  A slot is that place as one number,
+ * page * page_rows + g % page_rows (without the stride, so one slot map
+ * serves every cache of the same page_rows, whatever its stride and row
+ * width).  One serving step:
+ *   1. csa_page_plan: from each request's length and its new tokens, the new
+ *      pages, the block table, and where every new token and block goes;
+ *   2. csa_paged_append: the step's new rows into the pages and the window
+ *      rings;
+ *   3. csa_paged_attention: each new token over its sequence's pages and
+ *      window.
+ * The window ring is a cache of the same form: page b is the ring of sequence
+ * b, page_rows = page_stride = swa_cap.  All three calls follow the
+ * conventions above; none needs a value on the host that the device made, so
+ * a decode loop is captured into a graph once and replayed. */
+
+/* csa_page_plan: what one step does to the tables.  A request b holds
+ * seq_len[b] tokens and brings new_len[b] more (0: none this step; -1: it is
+ * over, and its pages go back).  It then holds floor(tokens / ratio)
+ * compressed blocks in ceil(blocks / page_rows) pages.  Pages come from the
+ * front of a ring of free pages and go back to its end: entries
+ * free_pos[0] .. free_pos[1] - 1 (modulo num_pages) of free_ring are free, in
+ * the order in which they will be taken.  Requests take pages in the order of
+ * b; pages given back in this step are behind every page taken in it.
+ *   table, free_ring: read and written in place.  Entries of the table that
+ *     hold a request's old pages and ring entries that are free stay as they
+ *     are, so a step planned twice from the same inputs gives the same
+ *     result.  The table row of a request that is over is left as it was.
+ *   tok_seq, tok_pos, swa_slot [tok_cap]: the step's T tokens in the order of
+ *     b, then position; the rest -1.  swa_slot is the token's place in the
+ *     window ring, b * swa_cap + pos % swa_cap, or -1 for a token that newer
+ *     ones of this step push out of the ring again.
+ *   row_slot [row_cap]: the slots of the step's R new blocks, in the same
+ *     order; the rest -1.
+ *   tok_off, row_off [B + 1]: request b's tokens are tok_off[b] ..
+ *     tok_off[b + 1] - 1, its new blocks row_off[b] .. row_off[b + 1] - 1
+ *     (the first of them is block floor(seq_len[b] / ratio)).
+ *   seq_len_out, row_len, swa_first_pos [B], free_pos_out [2]: after the
+ *     step.  They are separate from the inputs (a loop swaps the two).
+ * A step that cannot be done is refused as a whole: too few free pages, a
+ * request with more than max_pages pages, more than tok_cap tokens or
+ * row_cap blocks set CSA_DEV_CAPACITY; a negative or absurd (2^48) length
+ * sets CSA_DEV_BAD_LENGTH; ring positions that do not fit the pool set
+ * CSA_DEV_BAD_LAYOUT.  table and free_ring then stay as they were, the maps
+ * are all -1, the offsets 0 and the lengths those from before the step.
+ * Pages, window and lengths are counted per (ratio, page_rows): layers of
+ * another ratio have a table and a plan of their own.  num_seqs <= 8192,
+ * num_pages * page_rows, tok_cap and row_cap below 2^31, else
+ * CSA_ERR_UNSUPPORTED.  tok_cap or row_cap may be 0 (its arrays NULL).
+ * The plan depends on lengths alone; it is exact. */
+typedef struct {
+    int32_t num_seqs;        /* (host) B >= 1 */
+    int32_t ratio;           /* (host) tokens per compressed block */
+    int32_t page_rows;       /* (host) rows per page >= 1 */
+    int32_t max_pages;       /* (host) entries per sequence of the table >= 1 */
+    int64_t num_pages;       /* (host) pages in the pool = entries of free_ring */
+    int64_t tok_cap;         /* (host) entries of tok_seq, tok_pos, swa_slot */
+    int64_t row_cap;         /* (host) entries of row_slot */
+    int32_t swa_cap;         /* (host) slots of a window ring >= 1 */
+    const int64_t *seq_len;  /* [B] */
+    const int32_t *new_len;  /* [B] */
+    int32_t *table;          /* [B, max_pages] in, out */
+    int32_t *free_ring;      /* [num_pages] in, out */
+    const int64_t *free_pos; /* [2] */
+    int64_t *seq_len_out;    /* [B] out, and all below */
+    int64_t *row_len;        /* [B] blocks held */
+    int64_t *swa_first_pos;  /* [B] */
+    int64_t *free_pos_out;   /* [2] */
+    int64_t *tok_off;        /* [B + 1] */
+    int64_t *row_off;        /* [B + 1] */
+    int32_t *tok_seq;        /* [tok_cap] */
+    int64_t *tok_pos;        /* [tok_cap] */
+    int64_t *swa_slot;       /* [tok_cap] */
+    int64_t *row_slot;       /* [row_cap] */
+} csa_page_plan_t;
+
+csa_status_t csa_page_plan(const csa_page_plan_t *plan, int32_t *dev_status, void *stream);
+
+/* csa_paged_append: copies row i of `rows` to slot slots[i] of a cache, for
+ * up to four (rows, cache) pairs in one launch (a layer's compressed rows,
+ * its indexer keys, its window rows).  Rows are bytes: bf16 rows, MXFP4 rows
+ * (80 bytes) or any other multiple of 16.  A negative slot skips its row; a
+ * slot at or above num_pages * page_rows sets CSA_DEV_BAD_INDEX and skips
+ * it.  Everything else in the cache stays as it was.  Slots of one call must
+ * differ (those of a plan do): where two rows have the same slot, each 16
+ * bytes of it come from one of them.  rows and cache must not overlap.
+ * num_pages * page_rows < 2^31, row_bytes <= 65536, else
+ * CSA_ERR_UNSUPPORTED. */
+typedef struct {
+    const void *rows;        /* [num_rows, row_bytes], row i at i * row_pitch */
+    const int64_t *slots;    /* [num_rows] */
+    int64_t num_rows;        /* (host) >= 0 */
+    int64_t row_pitch;       /* (host) bytes, >= row_bytes, a multiple of 16 */
+    int32_t row_bytes;       /* (host) > 0, a multiple of 16 */
+    int32_t page_rows;       /* (host) rows per page of the cache */
+    int64_t num_pages;       /* (host) pages of the cache */
+    int64_t page_stride;     /* (host) rows from a page to the next, >= page_rows */
+    void *cache;             /* row r of page p at (p * page_stride + r) * row_bytes */
+} csa_append_job_t;
+
+#define CSA_MAX_APPEND_JOBS 4
+
+csa_status_t csa_paged_append(const csa_append_job_t *jobs /* (host) */, int32_t num_jobs,
+                              int32_t *dev_status, void *stream);
+
+/* csa_paged_attention: csa_hca_decode over a paged cache, dense attention of
+ * every query token over the visible compressed rows of its sequence and its
+ * window (any ratio).
+ *   n_vis(t) = min(row_len[b], floor(tok_pos[t] / ratio)),  b = tok_seq[t];
+ *   rows table[b, g / page_rows], g < n_vis(t), then the window rows
+ *   max(0, p - window + 1) .. p from the ring (params->window = 0: none, and
+ *   swa_kv / swa_first_pos may be NULL).
+ * The layout's arrays have the meaning that csa_page_plan gives them; a
+ * token with tok_seq = -1 is padding and its output is left as it was.  A
+ * token without any row gets zeros, with or without a sink.
+ *   cache bf16, num_pages pages of page_rows rows of hd values, page_stride
+ *     rows apart; only the rows named above are read into the result: the
+ *     rest of the pool may hold anything, NaN included.
+ *   q bf16 [T, n_heads, hd], sinks f32 [n_heads] (nullable), out f32 or bf16
+ *     [T, n_heads, hd] by out_type.
+ * n_heads is any number from 1 to 128, page_rows any number from 1 (pages of
+ * a multiple of 8 rows are copied 8 rows at a time, others row by row);
+ * n_ih, ihd and top_k of params are not used.  Rows times weights are summed
+ * in f32; for an f32 output the weights enter as two bf16 terms (relative
+ * 2^-16), for a bf16 output as one (2^-8, as the output itself is rounded).
+ * A table entry outside the pool sets CSA_DEV_BAD_INDEX and its rows are
+ * skipped; row_len above max_pages * page_rows sets CSA_DEV_CAPACITY and is
+ * cut there; a negative one sets CSA_DEV_BAD_LENGTH (read as 0).
+ * num_tokens <= 8192; num_pages * page_stride, max_pages * page_rows and
+ * num_seqs * swa_cap below 2^31, else CSA_ERR_UNSUPPORTED.
+ * Workspace: csa_paged_workspace_size bytes, 256-byte aligned; it needs no
+ * zeroing, and calls that may run at the same time need separate ones (two
+ * captured graphs too, unless one stream replays them). */
+typedef enum { CSA_F32 = 0, CSA_BF16 = 1 } csa_type_t;
+
+typedef struct {
+    int32_t num_seqs;             /* (host) B >= 1 */
+    int32_t num_tokens;           /* (host) T >= 0, padding included */
+    int32_t page_rows;            /* (host) rows per page >= 1 */
+    int32_t max_pages;            /* (host) entries per sequence of the table >= 1 */
+    const int32_t *tok_seq;       /* [T] sequence of each token; -1: padding */
+    const int64_t *tok_pos;       /* [T] */
+    const int64_t *row_len;       /* [B] compressed rows held */
+    const int32_t *table;         /* [B, max_pages] */
+    const void *swa_kv;           /* bf16 [B, swa_cap, hd] */
+    int32_t swa_cap;              /* (host) >= window */
+    const int64_t *swa_first_pos; /* [B] */
+} csa_paged_layout_t;
+
+csa_status_t csa_paged_workspace_size(const csa_paged_layout_t *layout,
+                                      const csa_params_t *params,
+                                      size_t *bytes /* (host) out */);
+
+csa_status_t csa_paged_attention(const csa_paged_layout_t *layout, const csa_params_t *params,
+                                 const void *cache, int64_t num_pages, int64_t page_stride,
+                                 const void *q, const float *sinks, csa_type_t out_type, void *out,
+                                 int32_t *dev_status, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,7 +34,9 @@ EXPORTS = ("csa_status_string", "csa_abi_version", "csa_workspace_size", "csa_in
            "csa_hca_workspace_size", "csa_hca_decode", "csa_fp4_quantize_keys",
            "csa_indexer_scores_fp4", "csa_decode_fp4", "csa_shard_workspace_size",
            "csa_shard_candidates", "csa_shard_merge", "csa_shard_attention", "csa_window_attention",
-           "csa_shard_combine")
+           "csa_shard_combine", "csa_page_plan", "csa_paged_append", "csa_paged_workspace_size",
+           "csa_paged_attention")
+MAX_APPEND_JOBS = 4  # csa_paged_append's limit (include/csa.h)
 MAX_SHARDS = 8  # csa_shard_merge's limit (include/csa.h)
 FP4_ROW = 80  # bytes per MXFP4 key row (include/csa.h)
 
@@ -60,6 +62,34 @@ class csa_params_t(ctypes.Structure):
         ("n_ih", ctypes.c_int32), ("ihd", ctypes.c_int32), ("hd", ctypes.c_int32),
         ("n_heads", ctypes.c_int32), ("top_k", ctypes.c_int32), ("window", ctypes.c_int32),
         ("ratio", ctypes.c_int32), ("scale", ctypes.c_float),
+    ]
+
+
+class csa_page_plan_t(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int32), ("ratio", ctypes.c_int32), ("page_rows", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32), ("num_pages", ctypes.c_int64), ("tok_cap", ctypes.c_int64),
+        ("row_cap", ctypes.c_int64), ("swa_cap", ctypes.c_int32),
+    ] + [(name, ctypes.c_void_p) for name in (
+        "seq_len", "new_len", "table", "free_ring", "free_pos", "seq_len_out", "row_len",
+        "swa_first_pos", "free_pos_out", "tok_off", "row_off", "tok_seq", "tok_pos", "swa_slot",
+        "row_slot")]
+
+
+class csa_append_job_t(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("num_rows", ctypes.c_int64),
+        ("row_pitch", ctypes.c_int64), ("row_bytes", ctypes.c_int32), ("page_rows", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("cache", ctypes.c_void_p),
+    ]
+
+
+class csa_paged_layout_t(ctypes.Structure):
+    _fields_ = [
+        ("num_seqs", ctypes.c_int32), ("num_tokens", ctypes.c_int32), ("page_rows", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32), ("tok_seq", ctypes.c_void_p), ("tok_pos", ctypes.c_void_p),
+        ("row_len", ctypes.c_void_p), ("table", ctypes.c_void_p), ("swa_kv", ctypes.c_void_p),
+        ("swa_cap", ctypes.c_int32), ("swa_first_pos", ctypes.c_void_p),
     ]
 
 
@@ -101,6 +131,11 @@ def load() -> ctypes.CDLL:
     lib.csa_shard_attention.argtypes = [L, Pm, i64, i64, P, P, P, P, P, P, P, P, sz, P]
     lib.csa_window_attention.argtypes = [L, Pm, P, P, P, P, P, sz, P]
     lib.csa_shard_combine.argtypes = [i32, i32, i32, P, P, P, P, P, P]
+    lib.csa_page_plan.argtypes = [ctypes.POINTER(csa_page_plan_t), P, P]
+    lib.csa_paged_append.argtypes = [ctypes.POINTER(csa_append_job_t), i32, P, P]
+    Lp = ctypes.POINTER(csa_paged_layout_t)
+    lib.csa_paged_workspace_size.argtypes = [Lp, Pm, ctypes.POINTER(sz)]
+    lib.csa_paged_attention.argtypes = [Lp, Pm, P, i64, i64, P, P, ctypes.c_int, P, P, P, sz, P]
     for fn in EXPORTS[2:]:
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
@@ -324,3 +359,158 @@ def csa_shard_combine(part_o, part_ml, out, dev_status, sinks=None, stream=None)
     P, T, H, _ = (int(x) for x in part_o.shape)
     _check("csa_shard_combine", load().csa_shard_combine(
         P, T, H, _p(part_o), _p(part_ml), _p(sinks), _p(out), _p(dev_status), _stream(stream)))
+
+
+# ---------------------------------------------------------------- paged caches
+
+def _arg(name: str, t, dtype, shape=None, contiguous=True) -> int:
+    """A tensor argument's address, its type, shape and device checked."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} lives on {t.device}, not on the current device")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _same_device(fn: str, index: int):
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: tensors live on cuda:{index}, not on the current device")
+
+
+class PagePlan:
+    """csa_page_plan's arguments: the sizes are taken from the tensors, which
+    the object keeps alive (it is made once and used every step)."""
+
+    def __init__(self, *, ratio: int, page_rows: int, swa_cap: int, seq_len, new_len, table,
+                 free_ring, free_pos, seq_len_out, row_len, swa_first_pos, free_pos_out, tok_off,
+                 row_off, tok_seq, tok_pos, swa_slot, row_slot):
+        i32, i64 = torch.int32, torch.int64
+        B, (tok_cap,), (row_cap,) = int(seq_len.shape[0]), tok_seq.shape, row_slot.shape
+        if table.dim() != 2 or table.shape[0] != B:
+            raise ValueError(f"table must have shape ({B}, max_pages), got {tuple(table.shape)}")
+        if free_ring.dim() != 1:
+            raise ValueError("free_ring must have one dimension")
+        want = dict(seq_len=(i64, (B,)), new_len=(i32, (B,)), table=(i32, None),
+                    free_ring=(i32, None), free_pos=(i64, (2,)), seq_len_out=(i64, (B,)),
+                    row_len=(i64, (B,)), swa_first_pos=(i64, (B,)), free_pos_out=(i64, (2,)),
+                    tok_off=(i64, (B + 1,)), row_off=(i64, (B + 1,)), tok_seq=(i32, None),
+                    tok_pos=(i64, (tok_cap,)), swa_slot=(i64, (tok_cap,)), row_slot=(i64, None))
+        given = dict(seq_len=seq_len, new_len=new_len, table=table, free_ring=free_ring,
+                     free_pos=free_pos, seq_len_out=seq_len_out, row_len=row_len,
+                     swa_first_pos=swa_first_pos, free_pos_out=free_pos_out, tok_off=tok_off,
+                     row_off=row_off, tok_seq=tok_seq, tok_pos=tok_pos, swa_slot=swa_slot,
+                     row_slot=row_slot)
+        at = {k: _arg(k, given[k], *want[k]) for k in want}
+        self.tensors, self.device = given, seq_len.device.index
+        self.c = csa_page_plan_t(num_seqs=B, ratio=ratio, page_rows=page_rows,
+                                 max_pages=int(table.shape[1]), num_pages=int(free_ring.shape[0]),
+                                 tok_cap=tok_cap, row_cap=row_cap, swa_cap=swa_cap, **at)
+
+
+def csa_page_plan(plan: PagePlan, dev_status, stream=None):
+    _same_device("csa_page_plan", plan.device)
+    _check("csa_page_plan", load().csa_page_plan(ctypes.byref(plan.c), _p(dev_status),
+                                                 _stream(stream)))
+
+
+class AppendJob:
+    """Rows [n, ...] (dense within a row, any pitch) to slots [n] of a cache
+    [num_pages, page_stride, ...] whose rows have the same bytes."""
+
+    def __init__(self, rows, slots, cache, page_rows: int):
+        n = int(rows.shape[0])
+        if cache.dim() < 2 or cache.dtype != rows.dtype or cache.shape[2:] != rows.shape[1:]:
+            raise ValueError(f"cache must be {rows.dtype} [num_pages, page_stride, "
+                             f"*{tuple(rows.shape[1:])}], got {cache.dtype} {tuple(cache.shape)}")
+        if n and not rows[0].is_contiguous():
+            raise ValueError("a row must be contiguous")
+        size = rows.element_size()
+        width = size * (rows[0].numel() if n else cache[0, 0].numel())
+        pitch = rows.stride(0) * size if n > 1 else width
+        self.tensors, self.device = (rows, slots, cache), cache.device.index
+        self.c = csa_append_job_t(
+            rows=_arg("rows", rows, rows.dtype, contiguous=False),
+            slots=_arg("slots", slots, torch.int64, (n,)), num_rows=n, row_pitch=pitch,
+            row_bytes=width, page_rows=page_rows, num_pages=int(cache.shape[0]),
+            page_stride=int(cache.shape[1]), cache=_arg("cache", cache, cache.dtype))
+
+
+class AppendJobs:
+    """Up to four AppendJob for one launch."""
+
+    def __init__(self, jobs):
+        self.jobs, self.device = list(jobs), jobs[0].device
+        self.c = (csa_append_job_t * len(self.jobs))(*[j.c for j in self.jobs])
+
+
+def csa_paged_append(jobs: AppendJobs, dev_status, stream=None):
+    _same_device("csa_paged_append", jobs.device)
+    _check("csa_paged_append", load().csa_paged_append(jobs.c, len(jobs.jobs), _p(dev_status),
+                                                       _stream(stream)))
+
+
+class PagedLayout:
+    """csa_paged_attention's layout: tokens [T] of sequences [B], the block
+    table [B, max_pages], the window ring [B, swa_cap, 512] (None without a
+    window).  Keeps its tensors alive; made once for buffers that stay."""
+
+    def __init__(self, tok_seq, tok_pos, row_len, table, page_rows: int, swa_kv=None,
+                 swa_first_pos=None):
+        T, B = int(tok_seq.shape[0]), int(row_len.shape[0])
+        if table.dim() != 2 or table.shape[0] != B:
+            raise ValueError(f"table must have shape ({B}, max_pages), got {tuple(table.shape)}")
+        ring = {}
+        if swa_kv is not None:
+            if swa_kv.dim() != 3 or swa_kv.shape[0] != B or swa_kv.shape[2] != 512:
+                raise ValueError(f"swa_kv must have shape ({B}, swa_cap, 512), "
+                                 f"got {tuple(swa_kv.shape)}")
+            ring = dict(swa_kv=_arg("swa_kv", swa_kv, torch.bfloat16), swa_cap=int(swa_kv.shape[1]),
+                        swa_first_pos=_arg("swa_first_pos", swa_first_pos, torch.int64, (B,)))
+        self.tensors = (tok_seq, tok_pos, row_len, table, swa_kv, swa_first_pos)
+        self.device, self.num_tokens = row_len.device.index, T
+        self.c = csa_paged_layout_t(
+            num_seqs=B, num_tokens=T, page_rows=page_rows, max_pages=int(table.shape[1]),
+            tok_seq=_arg("tok_seq", tok_seq, torch.int32, (T,)),
+            tok_pos=_arg("tok_pos", tok_pos, torch.int64, (T,)),
+            row_len=_arg("row_len", row_len, torch.int64, (B,)),
+            table=_arg("table", table, torch.int32), **ring)
+
+
+def csa_paged_workspace_size(layout: PagedLayout, prm: csa_params_t) -> int:
+    n = ctypes.c_size_t(0)
+    _check("csa_paged_workspace_size", load().csa_paged_workspace_size(
+        ctypes.byref(layout.c), ctypes.byref(prm), ctypes.byref(n)))
+    return int(n.value)
+
+
+def paged_workspace(layout: PagedLayout, prm: csa_params_t, device=None) -> torch.Tensor:
+    return torch.empty(csa_paged_workspace_size(layout, prm), dtype=torch.uint8,
+                       device=device or torch.device("cuda", layout.device))
+
+
+def csa_paged_attention(layout: PagedLayout, prm: csa_params_t, cache, q, out, dev_status, ws,
+                        sinks=None, stream=None):
+    """cache bf16 [num_pages, page_stride, 512], q bf16 [T, H, 512], out f32 or
+    bf16 [T, H, 512]."""
+    _same_device("csa_paged_attention", layout.device)
+    if cache.dtype != torch.bfloat16 or q.dtype != torch.bfloat16:
+        raise ValueError("cache and q must be bfloat16")
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out must be float32 or bfloat16")
+    shape = (layout.num_tokens, prm.n_heads, prm.hd)
+    if tuple(q.shape) != shape or tuple(out.shape) != shape:
+        raise ValueError(f"q and out must have shape {shape}")
+    if cache.dim() != 3 or cache.shape[2] != prm.hd:
+        raise ValueError(f"cache must have shape (num_pages, page_stride, {prm.hd})")
+    if sinks is not None and (sinks.dtype != torch.float32 or tuple(sinks.shape) != (prm.n_heads,)):
+        raise ValueError(f"sinks must be float32 [{prm.n_heads}]")
+    _check("csa_paged_attention", load().csa_paged_attention(
+        ctypes.byref(layout.c), ctypes.byref(prm), _p(cache), int(cache.shape[0]),
+        int(cache.shape[1]), _p(q), _p(sinks), 1 if out.dtype == torch.bfloat16 else 0, _p(out),
+        _p(dev_status), _p(ws), int(ws.numel()), _stream(stream)))

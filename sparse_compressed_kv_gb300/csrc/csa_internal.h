@@ -187,6 +187,14 @@ cudaError_t launch_partials_combine(const Launch &lc, int32_t P, int32_t T, int3
                                     const float *part_o, const float *part_ml, const float *sinks,
                                     float *out, int32_t *status);
 
+// Attention over a paged cache (csa_paged_attention.cu).
+constexpr int kPagedMaxTokens = 8192;
+size_t paged_attention_workspace(const csa_paged_layout_t &L, const csa_params_t &p);
+cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L,
+                                   const csa_params_t &p, const void *cache, int64_t num_pages,
+                                   int64_t page_stride, const void *q, const float *sinks,
+                                   csa_type_t out_type, void *out, int32_t *status, void *ws);
+
 // Launch helper: programmatic dependent launch on, so each kernel's prologue
 // may overlap the previous kernel's tail (kernels wait with griddepcontrol).
 template <typename... KArgs, typename... Args>
