@@ -108,6 +108,23 @@ CUresult encode_tensor_map_2d_bf16(CUtensorMap *map, const void *base, uint64_t 
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+CUresult encode_tensor_map_bf16(CUtensorMap *map, const void *base, uint32_t rank,
+                                const uint64_t *dims, const uint64_t *strides, const uint32_t *box) {
+    resolve_encode();
+    if (!g_encode) return CUDA_ERROR_NOT_SUPPORTED;
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5], e[5];
+    for (uint32_t i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        e[i] = 1;
+        if (i + 1 < rank) s[i] = strides[i];
+    }
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, s, b, e,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 CUresult encode_tensor_map_2d_u8(CUtensorMap *map, const void *base, uint64_t inner_bytes,
                                  uint64_t outer, uint32_t box_inner, uint32_t box_outer) {
     resolve_encode();

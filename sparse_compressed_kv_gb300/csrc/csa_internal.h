@@ -231,6 +231,10 @@ cudaError_t set_kernel_smem(K kernel, size_t dyn_bytes) {
 CUresult encode_tensor_map_2d_bf16(CUtensorMap *map, const void *base, uint64_t inner,
                                    uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
                                    uint32_t box_outer);
+// The same with any rank up to 5: dims and box in elements, strides (of dims
+// 1 ..) in bytes; 128-byte swizzle, zeros out of bounds.
+CUresult encode_tensor_map_bf16(CUtensorMap *map, const void *base, uint32_t rank,
+                                const uint64_t *dims, const uint64_t *strides, const uint32_t *box);
 // Dense byte rows of inner_bytes each, no swizzle.
 CUresult encode_tensor_map_2d_u8(CUtensorMap *map, const void *base, uint64_t inner_bytes,
                                  uint64_t outer, uint32_t box_inner, uint32_t box_outer);

@@ -1,8 +1,32 @@
 // csa_paged_attention.cu -- shared-KV attention of new tokens over a paged
-// cache and the window ring:
+// cache and the window ring, on the 5th-generation tensor cores:
 //   l_j = scale q_h . row_j,   out_h = sum_j softmax_j(l [, sink]) row_j.
-// One CTA per (token, head) walks the token's rows: each warp takes a row's
-// logit, then every thread accumulates two of the 512 output columns.
+//
+// A token's row slots are its visible compressed rows, padded to a multiple of
+// 8, then its window rows; 64 slots are a chunk.  One kernel of one CTA per SM
+// (per 64 heads) divides the chunks of all tokens: each CTA counts every
+// token's chunks for itself (the lengths are on the device only), takes an
+// equal range of them, and walks it as segments, one per token, through one
+// pipeline that does not drain between tokens:
+//   warps 0, 6..8  fetch a chunk's rows, 16 each: a group of 8 rows that lies
+//                  in one page is one TMA box (64 columns x 8 rows x 8 column
+//                  groups: 8 KiB whatever the page size), other groups
+//                  (page ends, the last rows, the window) go row by row with
+//                  16-byte cp.async, rows that do not exist as zeros
+//   warp 1         issues  S = Q . rows^T        (M = 64 heads, N = 64 rows)
+//                          O^T += rows^T . P^T   (M = 128 columns, N = 64 heads)
+//                  whichever is ready, Q^T of the next segment included
+//   warps 2..5     softmax with a lazily raised maximum; a segment's epilogue
+// A group's 8 KiB hold 8 column groups of 8 rows x 128 bytes (the swizzle
+// atom), so the same bytes are the K-major operand of S (row groups 8 KiB
+// apart) and the MN-major operand of O^T (column groups 1 KiB apart, row
+// groups 8 KiB).
+//
+// A segment that is a whole token writes the output; the parts of a token cut
+// between CTAs go to the workspace as (O, m, l) and a second kernel joins
+// them.  The accumulator of tcgen05 drops bits below its last place, so
+// sums of thousands of rows drift; every kFlush chunks O^T is added, rounded,
+// into the CTA's own f32 partial and starts again from zero.
 #include <math.h>
 
 #include "csa_device.cuh"
@@ -11,128 +35,957 @@
 namespace csa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 32;   // rows per softmax step
+constexpr int kThreads = 288;
+constexpr int kSmThreads = 128;                 // warps 2..5
+constexpr int kBarSm = 1;
+constexpr int kHG = 64;                         // heads per CTA
+constexpr int kChunk = 64;
+constexpr int kQBytes = kHG * kHD * 2;          // 64 KiB
+constexpr int kGroupBytes = 8 * kHD * 2;        // 8 rows: 8 KiB
+constexpr int kStageBytes = 8 * kGroupBytes;    // 64 KiB
+constexpr int kStages = 2;
+constexpr int kPBytes = kHG * kChunk * 2;       // one bf16 term of P: 8 KiB
+constexpr int kSCol = 0;                        // two S buffers of 64 columns
+constexpr int kOCol = 128;                      // O^T: 4 tiles x 64 heads
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleAbove = 8.f;            // log2 units
+constexpr int kMaxRec = 128;                    // segments a CTA lists at a time
+constexpr int kMaxCtas = 152;                   // CTAs of the grid at most (sizes the workspace)
+constexpr int kSegCost = 2;                     // a segment's epilogue, in chunks
+constexpr int kCutAbove = 4;                    // chunks a token may exceed the mean before tokens are cut
+constexpr int kFlushF32 = 32, kFlushBf16 = 512; // chunks between roundings of the accumulator
 
 struct PagedArgs {
     csa_paged_layout_t L;
-    int32_t H, window, ratio;
-    float scale;
-    const __nv_bfloat16 *cache;
+    int32_t H, window, ratio, bf16_out;
+    float scale_log2;
+    int32_t total_rows;       // rows of the pool: the coordinate that reads as zeros
     int64_t num_pages, page_stride;
-    const __nv_bfloat16 *q;
+    const __nv_bfloat16 *cache;
     const float *sinks;
     void *out;
-    int32_t bf16_out;
+    float *part_o;            // [slot][H][512]
+    float *part_ml;           // [slot][H][2]  (m in log2 units, l)
+    int2 *meta;               // by token (T <= CTAs) or by CTA: first slot, parts (0: none)
     int32_t *status;
 };
 
-__global__ void __launch_bounds__(kThreads) paged_attention_kernel(const PagedArgs A) {
-    const int h = blockIdx.x, t = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = A.L.tok_seq[t];
-    if (b == -1) return;
-    __shared__ const __nv_bfloat16 *row[kTile];
-    __shared__ float logit[kTile];
+// One segment: chunks [c0, c1) of token t.
+struct Rec {
+    int32_t t, b;             // b < 0: padding
+    int32_t n, near;          // compressed rows, window rows
+    int32_t c0, c1;
+    int32_t slot;             // partial slot
+    int32_t flags;
+    int64_t first;            // first window position
+    int64_t first_res;        // oldest position the ring holds
+};
+constexpr int kRecPart = 1;   // part of a cut token: leaves (O, m, l)
+constexpr int kRecZero = 2;   // a token without rows: zeros
+
+struct Smem {
+    uint64_t q_full, q_free;
+    uint64_t full[kStages], empty[kStages];
+    uint64_t sfull[2], sfree[2];
+    uint64_t pfull, pfree, ofree;
+    uint32_t tmem_holder;
+    uint32_t maskw[kStages][4];
+    uint32_t flag[2][4];
+    float alpha[kHG];
+    float fin[kHG];
+    float flush[kHG];
+    int32_t nrec, more;
+    int64_t t0, s0;
+    int64_t wsum[kThreads / 32][2];
+    int32_t wmax[kThreads / 32];
+    Rec rec[kMaxRec];
+};
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
+                                            int32_t z, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
+                                            int32_t z, int32_t w, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar)),
+        "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16_raw(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// threads 0..15: lanes 0..15 of the quarter, columns c ..; threads 16..31: the
+// same lanes, columns c + 32 ..
+__device__ __forceinline__ void tmem_ld16x2_raw(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16], 32;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// 2^x, relative error about 2^-22; 2^-inf = 0
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+template <int M, int N, bool kTransA>
+__device__ __forceinline__ constexpr uint32_t idesc_bf16() {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((kTransA ? 1u : 0u) << 15) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// What token t attends: b < 0 for padding, n = near = 0 for a bad token.
+__device__ __forceinline__ Rec token_rec(const PagedArgs &A, int t, int &bad) {
+    Rec r{};
+    r.t = t;
+    r.b = A.L.tok_seq[t];
     const int64_t pos = A.L.tok_pos[t];
-    int bad = 0;
-    int64_t n = 0, first = 0, near = 0;
-    if (b < 0 || b >= A.L.num_seqs || pos < 0) {
+    bad = 0;
+    if (r.b == -1) return r;
+    if (r.b < 0 || r.b >= A.L.num_seqs || pos < 0) {
         bad = CSA_DEV_BAD_LAYOUT;
-    } else {
-        n = A.L.row_len[b];
-        const int64_t cap = static_cast<int64_t>(A.L.max_pages) * A.L.page_rows;
-        if (n < 0) bad |= CSA_DEV_BAD_LENGTH, n = 0;
-        if (n > cap) bad |= CSA_DEV_CAPACITY, n = cap;
-        if (pos / A.ratio < n) n = pos / A.ratio;
-        first = window_first(pos, A.window);
-        near = A.window > 0 ? pos - first + 1 : 0;
+        r.b = 0;
+        return r;
     }
-    const __nv_bfloat16 *q = A.q + (static_cast<int64_t>(t) * A.H + h) * kHD;
-    float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-    for (int64_t j0 = 0; j0 < n + near; j0 += kTile) {
-        if (tid < kTile) {
-            const int64_t j = j0 + tid;
-            const __nv_bfloat16 *p = nullptr;
-            if (j < n) {
-                const int32_t page = A.L.table[static_cast<int64_t>(b) * A.L.max_pages + j / A.L.page_rows];
-                if (page < 0 || page >= A.num_pages) bad |= CSA_DEV_BAD_INDEX;
-                else p = A.cache + (page * A.page_stride + j % A.L.page_rows) * kHD;
-            } else if (j < n + near) {
-                const int64_t x = first + (j - n);
-                if (x < A.L.swa_first_pos[b]) bad |= CSA_DEV_MISSING_SWA;
-                else
-                    p = static_cast<const __nv_bfloat16 *>(A.L.swa_kv) +
-                        (static_cast<int64_t>(b) * A.L.swa_cap + x % A.L.swa_cap) * kHD;
-            }
-            row[tid] = p;
-        }
-        __syncthreads();
-        for (int r = warp; r < kTile; r += kThreads / 32) {
-            const __nv_bfloat16 *p = row[r];
-            float s = 0.f;
-            if (p)
-                for (int d = lane; d < kHD; d += 32) s += __bfloat162float(q[d]) * __bfloat162float(p[d]);
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == 0) logit[r] = p ? s * A.scale : -INFINITY;
-        }
-        __syncthreads();
-        float mc = m;
-        for (int r = 0; r < kTile; ++r) mc = fmaxf(mc, logit[r]);
-        if (mc != -INFINITY) {
-            const float a = expf(m - mc);
-            o0 *= a;
-            o1 *= a;
-            l *= a;
-            m = mc;
-            for (int r = 0; r < kTile; ++r) {
-                const __nv_bfloat16 *p = row[r];
-                if (!p) continue;
-                const float w = expf(logit[r] - m);
-                l += w;
-                o0 += w * __bfloat162float(p[2 * tid]);
-                o1 += w * __bfloat162float(p[2 * tid + 1]);
-            }
-        }
-        __syncthreads();
+    int64_t n = A.L.row_len[r.b];
+    const int64_t cap = static_cast<int64_t>(A.L.max_pages) * A.L.page_rows;
+    if (n < 0) {
+        bad |= CSA_DEV_BAD_LENGTH;
+        n = 0;
     }
-    raise_status(A.status, bad);
-    float z = l;
-    if (A.sinks && m != -INFINITY) z += expf(A.sinks[h] - m);
-    const float f = l > 0.f ? 1.f / z : 0.f;
-    const int64_t at = (static_cast<int64_t>(t) * A.H + h) * kHD + 2 * tid;
-    if (A.bf16_out) {
-        static_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16(o0 * f);
-        static_cast<__nv_bfloat16 *>(A.out)[at + 1] = __float2bfloat16(o1 * f);
+    if (n > cap) {
+        bad |= CSA_DEV_CAPACITY;
+        n = cap;
+    }
+    const int64_t seen = pos / A.ratio;
+    r.n = static_cast<int32_t>(n < seen ? n : seen);
+    if (A.window > 0) {
+        r.first = window_first(pos, A.window);
+        r.near = static_cast<int32_t>(pos - r.first + 1);
+        r.first_res = A.L.swa_first_pos[r.b];
+    }
+    return r;
+}
+
+__device__ __forceinline__ int rec_window_slot(const Rec &r) { return (r.n + 7) & ~7; }
+__device__ __forceinline__ int rec_slots(const Rec &r) {
+    return r.near > 0 ? rec_window_slot(r) + r.near : r.n;
+}
+__device__ __forceinline__ int rec_chunks(const Rec &r) {
+    return r.b < 0 ? 0 : (rec_slots(r) + kChunk - 1) / kChunk;
+}
+__device__ __forceinline__ int chunk_cost(int chunks) { return chunks > 0 ? chunks + kSegCost : 1; }
+
+// kTerms: bf16 terms of P (2 for an f32 output, 1 for bf16).
+template <int kTerms>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
+                           const __grid_constant__ CUtensorMap tm_rows, const PagedArgs A) {
+    constexpr int kFlush = kTerms == 2 ? kFlushF32 : kFlushBf16;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align_smem<1024>(smem_raw);
+    uint8_t *sQ = smem;
+    uint8_t *sRows = sQ + kQBytes;                       // [stage][8 groups][8 col groups][8 rows][128 B]
+    uint8_t *sP = sRows + kStages * kStageBytes;         // [term][64 heads][128 B]
+    Smem &S = *reinterpret_cast<Smem *>(sP + kTerms * kPBytes);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = gridDim.x, hg = blockIdx.y, h0 = hg * kHG;
+    const int T = A.L.num_tokens, H = A.H;
+
+    if (tid == 0) {
+        mbar_init(&S.q_full, 1);
+        mbar_init(&S.q_free, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&S.full[i], 4);
+            mbar_init(&S.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.sfull[i], 1);
+            mbar_init(&S.sfree[i], kSmThreads);
+        }
+        mbar_init(&S.pfull, kSmThreads);
+        mbar_init(&S.pfree, 1);
+        mbar_init(&S.ofree, kSmThreads);
+        mbar_fence_init();
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_rows);
+    }
+    if (warp == 1) {
+        tmem_alloc(&S.tmem_holder, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // ---------------------------------------------------- division of the work
+    // chunks and costs of all tokens, a contiguous run per thread
+    const int per = (T + kThreads - 1) / kThreads;
+    const int ta = min(T, tid * per), te = min(T, ta + per);
+    int64_t chunks = 0, cost = 0;
+    int maxc = 0;
+    for (int t = ta; t < te; ++t) {
+        int bad;
+        const int c = rec_chunks(token_rec(A, t, bad));
+        chunks += c;
+        cost += chunk_cost(c);
+        maxc = max(maxc, c);
+    }
+    int64_t incl = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+        chunks += __shfl_xor_sync(0xffffffffu, chunks, o);
+        maxc = max(maxc, __shfl_xor_sync(0xffffffffu, maxc, o));
+    }
+    if (lane == 31) {
+        S.wsum[warp][0] = incl;
+        S.wsum[warp][1] = chunks;
+        S.wmax[warp] = maxc;
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem_holder;
+    int64_t base = 0, U = 0;
+    chunks = 0;
+    maxc = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) base = U;
+        U += S.wsum[w][0];
+        chunks += S.wsum[w][1];
+        maxc = max(maxc, S.wmax[w]);
+    }
+    // Tokens are cut only where that shortens the longest CTA by more than
+    // the partials and their join cost: otherwise CTA c takes token c (T <= G), or the
+    // tokens that begin in its range.
+    const bool direct = T <= G && maxc <= chunks / G + kCutAbove;
+    const bool snap = direct || (T > G && maxc <= kCutAbove);
+    // few CTAs at work: 2 or 4 of them share a range, each with all of its
+    // logits and weights and its share of the 512 columns
+    int dparts = 1;
+    if (direct) dparts = T * 4 <= G ? 4 : T * 2 <= G ? 2 : 1;
+    else if (!snap && T <= G) dparts = chunks * 4 <= G ? 4 : chunks <= G ? 2 : 1;
+    const int nsplit = static_cast<int>(min(static_cast<int64_t>(G / dparts), U));
+    const int split = static_cast<int>(blockIdx.x) / dparts;
+    const int ndt = 4 / dparts;                                   // 128-column tiles of this CTA
+    const int dt0 = (static_cast<int>(blockIdx.x) % dparts) * ndt;
+    int64_t ua, ub;
+    if (direct) {
+        ua = 0;
+        ub = split < T ? 1 : 0;
     } else {
-        static_cast<float *>(A.out)[at] = o0 * f;
-        static_cast<float *>(A.out)[at + 1] = o1 * f;
+        ua = split < nsplit ? split * U / nsplit : U;
+        ub = split < nsplit ? (split + 1) * U / nsplit : U;
+    }
+    const bool by_token = T <= G;
+    const bool lead = hg == 0 && dt0 == 0;       // reports errors, writes the join's list
+    if (tid == 0) {
+        S.t0 = direct ? split : T;
+        S.s0 = 0;
+        if (lead && !by_token) A.meta[split] = make_int2(-1, 0);
+    }
+    __syncthreads();
+    if (!direct) {
+        // the first token of the range: the one that holds unit ua, or (whole
+        // tokens only) the first that begins at or behind it
+        int64_t s = base + incl - cost;
+        for (int t = ta; t < te; ++t) {
+            int bad;
+            const int64_t e = s + chunk_cost(rec_chunks(token_rec(A, t, bad)));
+            if (snap ? s >= ua : (s <= ua && ua < e)) {
+                if (snap) {
+                    atomicMin(reinterpret_cast<unsigned long long *>(&S.t0), static_cast<unsigned long long>(t));
+                } else {
+                    S.t0 = t;
+                    S.s0 = s;
+                }
+                break;
+            }
+            s = e;
+        }
+        __syncthreads();
+        if (snap) {
+            s = base + incl - cost;
+            for (int t = ta; t < te; ++t) {
+                if (t == S.t0) S.s0 = s;
+                int bad;
+                s += chunk_cost(rec_chunks(token_rec(A, t, bad)));
+            }
+            __syncthreads();
+        }
+    }
+    int64_t t0 = S.t0, s0 = S.s0;
+
+    // pipeline positions, kept across batches of segments
+    uint32_t n_fetch = 0;                // chunks fetched
+    uint32_t nq = 0, np = 0;             // chunks whose S / O^T product was issued
+    uint32_t n_ql = 0;                   // Q loads issued
+    uint32_t n_of = 0;                   // sub-segments begun (O^T from zero)
+    uint32_t n_sm = 0;                   // chunks through the softmax
+
+    for (;;) {
+        // ------------------------------------------------ the next segments
+        __syncthreads();                 // the previous list is done with
+        if (tid == 0) {
+            S.nrec = 0;
+            S.more = 0;
+        }
+        __syncthreads();
+        {
+            Rec r{};
+            int bad = 0, c = 0;
+            int64_t w = 0;
+            const bool in = tid < kMaxRec && t0 + tid < T && ub > ua;
+            if (in) {
+                r = token_rec(A, static_cast<int>(t0) + tid, bad);
+                c = rec_chunks(r);
+                w = chunk_cost(c);
+            }
+            int64_t run = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, run, o);
+                if (lane >= o) run += v;
+            }
+            if (lane == 31) S.wsum[warp][0] = run;
+            __syncthreads();
+            int64_t s = s0 + run - w, all = s0;
+            for (int k = 0; k < kMaxRec / 32; ++k) {
+                if (k < warp) s += S.wsum[k][0];
+                all += S.wsum[k][0];
+            }
+            const bool mine = in && (direct ? tid == 0 : s < ub);
+            if (mine) {
+                r.c0 = 0;
+                r.c1 = c;
+                bool owner = true;
+                int2 m = make_int2(-1, 0);
+                r.slot = 2 * split + 1;
+                if (!snap) {
+                    owner = s >= ua;
+                    r.c0 = static_cast<int32_t>(min(max(ua - s, int64_t(0)), int64_t(c)));
+                    r.c1 = static_cast<int32_t>(min(ub - s, int64_t(c)));
+                    if (!owner) r.slot = 2 * split;
+                    // the split that holds the token's last chunk
+                    if (owner && c > 0) {
+                        const int64_t last = ((s + c) * nsplit - 1) / U;
+                        if (last > split) m = make_int2(r.slot, static_cast<int>(last) - split + 1);
+                    }
+                    if (r.c1 - r.c0 < c) r.flags |= kRecPart;
+                }
+                if (r.b >= 0 && c == 0 && owner) r.flags |= kRecZero;
+                if (lead && owner) {
+                    raise_status(A.status, bad);
+                    if (by_token) {
+                        A.meta[r.t] = m;
+                    } else if (m.y > 0) {
+                        A.meta[split] = m;
+                        A.meta[G + split] = make_int2(r.t, 0);
+                    }
+                }
+                S.rec[tid] = r;
+                atomicAdd(&S.nrec, 1);
+                if (tid == kMaxRec - 1 && !direct) S.more = 1;
+            }
+            t0 += kMaxRec;
+            s0 = all;
+        }
+        __syncthreads();
+        const int nrec = S.nrec;
+        const bool more = S.more != 0;
+        if (nrec == 0) break;
+
+        if (warp == 1) {
+            // -------------------------------------------- MMA issuer
+            if (lane == 0) {
+                constexpr uint32_t id_qk = idesc_bf16<kHG, kChunk, false>();
+                constexpr uint32_t id_pv = idesc_bf16<128, kHG, true>();
+                const uint64_t q_desc = sw128_desc(smem_addr(sQ), 16, 1024);
+                const uint64_t r_desc = sw128_desc(smem_addr(sRows), 16, kGroupBytes);
+                const uint64_t a_desc = sw128_desc(smem_addr(sRows) + 2 * dt0 * 1024, 1024, kGroupBytes);
+                const uint64_t p_desc = sw128_desc(smem_addr(sP), 16, 1024);
+                auto off = [](uint32_t bytes) { return static_cast<uint64_t>(bytes >> 4); };
+                auto live = [&](int i) {
+                    while (i < nrec && S.rec[i].c1 <= S.rec[i].c0) ++i;
+                    return i;
+                };
+                int rl = live(0);                  // segment whose Q is loaded next
+                int rq = rl, cq = 0;               // next S product: segment, chunk of it
+                int rp = rl, cp = 0;               // next O^T product
+                bool dead = false;
+                uint32_t polls = 0;
+                uint64_t t_start = 0;
+                while (rp < nrec) {
+                    bool did = false;
+                    // Q of the next segment once the last S product of the one
+                    // before it is done with the buffer
+                    if (rl < nrec && rl == rq &&
+                        (n_ql == 0 || dead || mbar_try_wait(&S.q_free, (n_ql - 1) & 1u))) {
+                        mbar_arrive_expect_tx(&S.q_full, kQBytes);
+                        tma_load_4d(sQ, &tm_q, 0, h0, 0, S.rec[rl].t, &S.q_full, policy_evict_normal());
+                        ++n_ql;
+                        rl = live(rl + 1);
+                        did = true;
+                    }
+                    if (rq < nrec && rl != rq && nq <= np + 1) {
+                        const int st = nq % kStages, sb = nq & 1u;
+                        if (dead || (mbar_try_wait(&S.q_full, (n_ql - 1) & 1u) &&
+                                     mbar_try_wait(&S.full[st], (nq / kStages) & 1u) &&
+                                     mbar_try_wait(&S.sfree[sb], ((nq >> 1) & 1u) ^ 1u))) {
+                            tc_fence_after();
+                            const uint64_t rd = r_desc + off(st * kStageBytes);
+                            const uint32_t d = tmem + kSCol + sb * kChunk;
+#pragma unroll
+                            for (int kk = 0; kk < 32; ++kk) {
+                                const uint32_t cg = kk >> 2, ko = (kk & 3) * 32;
+                                umma_bf16(d, q_desc + off(cg * (kHG * 128) + ko), rd + off(cg * 1024 + ko),
+                                          id_qk, kk > 0 ? 1u : 0u);
+                            }
+                            umma_commit(&S.sfull[sb]);
+                            ++nq;
+                            if (++cq == S.rec[rq].c1 - S.rec[rq].c0) {
+                                umma_commit(&S.q_free);
+                                cq = 0;
+                                rq = live(rq + 1);
+                            }
+                            did = true;
+                        }
+                    }
+                    if (!did && np < nq) {
+                        const int st = np % kStages;
+                        const bool zero = cp % kFlush == 0;
+                        if (dead || (mbar_try_wait(&S.pfull, np & 1u) &&
+                                     (!zero || n_of == 0 || mbar_try_wait(&S.ofree, (n_of - 1) & 1u)))) {
+                            tc_fence_after();
+                            if (zero) ++n_of;
+                            const uint64_t ad = a_desc + off(st * kStageBytes);
+#pragma unroll 1
+                            for (int dd = 0; dd < ndt; ++dd)
+#pragma unroll
+                                for (int ks = 0; ks < kChunk / 16; ++ks) {
+                                    const uint64_t av = ad + off(2 * dd * 1024 + ks * 2 * kGroupBytes);
+                                    const uint32_t d = tmem + kOCol + dd * kHG;
+                                    umma_bf16(d, av, p_desc + off(ks * 32), id_pv, (zero && ks == 0) ? 0u : 1u);
+                                    if (kTerms == 2) umma_bf16(d, av, p_desc + off(kPBytes + ks * 32), id_pv, 1u);
+                                }
+                            umma_commit(&S.empty[st]);
+                            umma_commit(&S.pfree);
+                            ++np;
+                            if (++cp == S.rec[rp].c1 - S.rec[rp].c0) {
+                                cp = 0;
+                                rp = live(rp + 1);
+                            }
+                            did = true;
+                        }
+                    }
+                    if (did) {
+                        polls = 0;
+                    } else if (++polls == 1) {
+                        t_start = global_timer_ns();
+                    } else if ((polls & 1023u) == 0 && global_timer_ns() - t_start > kWaitNs) {
+                        raise_status(A.status, CSA_DEV_TIMEOUT);
+                        dead = true;
+                    }
+                }
+            }
+        } else if (warp == 0 || warp >= 6) {
+            // -------------------------------------------- row fetch
+            const int li = warp == 0 ? 0 : warp - 5;   // rows 16 li .. of each chunk
+            int bad = 0;
+            int pending = -1;                          // stage whose cp.async rows are in flight
+            auto land = [&](bool newer) {              // ... have landed: hand the stage over
+                if (newer) cp_async_wait<1>();
+                else cp_async_wait<0>();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.full[pending]);
+                pending = -1;
+            };
+            const uint64_t pol = policy_evict_normal();
+            for (int i = 0; i < nrec; ++i) {
+                const Rec r = S.rec[i];
+                const int wslot = rec_window_slot(r);
+                for (int c = r.c0; c < r.c1; ++c) {
+                    // lane l resolves row l of the warp's 16: a row of the pool, or of
+                    // the ring, or none
+                    const int j = c * kChunk + 16 * li + (lane & 15);
+                    int32_t row = -1;                  // row of the pool
+                    int32_t in_page = 0;
+                    const __nv_bfloat16 *src = nullptr;
+                    if (j < r.n) {
+                        const int pg = j / A.L.page_rows;
+                        in_page = j - pg * A.L.page_rows;
+                        const int32_t page = A.L.table[static_cast<int64_t>(r.b) * A.L.max_pages + pg];
+                        if (page < 0 || page >= A.num_pages) {
+                            bad |= CSA_DEV_BAD_INDEX;
+                        } else {
+                            row = static_cast<int32_t>(page * A.page_stride) + in_page;
+                            src = A.cache + static_cast<int64_t>(row) * kHD;
+                        }
+                    } else if (r.near > 0 && j >= wslot && j - wslot < r.near) {
+                        const int64_t x = r.first + (j - wslot);
+                        if (x < r.first_res) bad |= CSA_DEV_MISSING_SWA;
+                        else
+                            src = static_cast<const __nv_bfloat16 *>(A.L.swa_kv) +
+                                  (static_cast<int64_t>(r.b) * A.L.swa_cap + x % A.L.swa_cap) * kHD;
+                    }
+                    const uint32_t okm = __ballot_sync(0xffffffffu, src != nullptr) & 0xFFFFu;
+                    // a group of 8 rows of one page is one box
+                    bool box[2];
+                    int32_t y[2];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const int j0 = c * kChunk + 16 * li + 8 * g;
+                        const int32_t off0 = __shfl_sync(0xffffffffu, in_page, 8 * g);
+                        y[g] = __shfl_sync(0xffffffffu, row, 8 * g);
+                        box[g] = j0 + 8 <= r.n && off0 + 8 <= A.L.page_rows;
+                        if (y[g] < 0) y[g] = A.total_rows;      // behind the pool: zeros
+                    }
+                    const int st = n_fetch % kStages;
+                    const uint32_t ph = ((n_fetch / kStages) & 1u) ^ 1u;
+                    if (pending >= 0 && !__all_sync(0xffffffffu, mbar_try_wait(&S.empty[st], ph))) land(false);
+                    mbar_wait(&S.empty[st], ph, A.status);
+                    __syncwarp();
+                    uint8_t *rows = sRows + st * kStageBytes + 2 * li * kGroupBytes;
+                    if (lane == 0) {
+                        S.maskw[st][li] = okm;
+                        if (box[0] || box[1]) {
+                            mbar_expect_tx(&S.full[st], (box[0] && box[1] ? 2 : 1) * kGroupBytes);
+#pragma unroll
+                            for (int g = 0; g < 2; ++g)
+                                if (box[g]) tma_load_3d(rows + g * kGroupBytes, &tm_rows, 0, y[g], 0, &S.full[st], pol);
+                        }
+                    }
+                    const bool by_row = !(box[0] && box[1]);
+                    if (by_row) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            if (box[g]) continue;
+#pragma unroll 2
+                            for (int rr = 0; rr < 8; ++rr) {
+                                const __nv_bfloat16 *p = reinterpret_cast<const __nv_bfloat16 *>(__shfl_sync(
+                                    0xffffffffu, reinterpret_cast<unsigned long long>(src), 8 * g + rr));
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    const int k = lane + 32 * u;   // 16-byte piece of the row
+                                    cp_async16(rows + g * kGroupBytes + (k >> 3) * 1024 + rr * 128 + (((k & 7) ^ rr) << 4),
+                                               p ? static_cast<const void *>(p + k * 8) : A.cache, p != nullptr);
+                                }
+                            }
+                        }
+                        cp_async_commit();
+                    }
+                    if (pending >= 0) land(by_row);
+                    if (by_row) pending = st;
+                    else if (lane == 0) mbar_arrive(&S.full[st]);
+                    ++n_fetch;
+                }
+            }
+            if (pending >= 0) land(false);
+            bad = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bad)));
+            if (lane == 0 && lead) raise_status(A.status, bad);
+        } else {
+            // -------------------------------------------- softmax, epilogue
+            const int q = warp & 3;                  // TMEM lane quarter
+            const int hl = q * 16 + (lane & 15);     // head of this lane (two lanes per head)
+            const bool upper = lane >= 16;           // rows 32..63 of the chunk
+            const bool hv = h0 + hl < H;
+            const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+            const int hmax = min(kHG, H - h0);
+            for (int i = 0; i < nrec; ++i) {
+                const Rec r = S.rec[i];
+                const int nch = r.c1 - r.c0;
+                const int64_t obase = (static_cast<int64_t>(r.t) * H + h0) * kHD;
+                if (nch <= 0) {
+                    if (r.flags & kRecZero) {
+                        for (int e = tid - 64; e < hmax * 128 * ndt; e += kSmThreads) {
+                            const int64_t at = obase + (e / (128 * ndt)) * kHD + dt0 * 128 + e % (128 * ndt);
+                            if (A.bf16_out) static_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16(0.f);
+                            else static_cast<float *>(A.out)[at] = 0.f;
+                        }
+                    }
+                    continue;
+                }
+                float m_ref = -INFINITY, l = 0.f, m_flush = -INFINITY;
+                float *const po = A.part_o + (static_cast<int64_t>(r.slot) * H + h0) * kHD;
+                for (int k = 0; k < nch; ++k, ++n_sm) {
+                    const int st = n_sm % kStages, sb = n_sm & 1u;
+                    mbar_wait(&S.sfull[sb], (n_sm >> 1) & 1u, A.status);
+                    tc_fence_after();
+                    uint32_t sr[2][16];
+                    tmem_ld16x2_raw(tmem + lane_off + kSCol + sb * kChunk, sr[0]);
+                    tmem_ld16x2_raw(tmem + lane_off + kSCol + sb * kChunk + 16, sr[1]);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                    mbar_arrive(&S.sfree[sb]);
+                    mbar_wait(&S.full[st], (n_sm / kStages) & 1u, A.status);   // orders the mask words
+                    uint64_t msk = 0;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) msk |= static_cast<uint64_t>(S.maskw[st][w]) << (16 * w);
+                    // Every row real and a scale >= 0: the maximum of the raw
+                    // logits, the scale in the exponent's fma.  Otherwise
+                    // scaled logits, rows that do not exist at -inf.
+                    float x[32];
+                    float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float xs = 1.f;
+                    if (msk == ~0ull && A.scale_log2 >= 0.f) {
+                        xs = A.scale_log2;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            x[j] = __uint_as_float(sr[j >> 4][j & 15]);
+                            mq[j & 3] = fmaxf(mq[j & 3], x[j]);
+                        }
+                    } else {
+                        const uint32_t mh = static_cast<uint32_t>(msk >> (upper ? 32 : 0));
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const uint32_t v = sr[j >> 4][j & 15];
+                            x[j] = ((mh >> j) & 1u) ? __uint_as_float(v) * A.scale_log2 : -INFINITY;
+                            mq[j & 3] = fmaxf(mq[j & 3], x[j]);
+                        }
+                    }
+                    float mc = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+                    mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, 16)) * xs;
+                    // a head whose maximum rises by more than kRescaleAbove rescales
+                    // what has been accumulated
+                    const bool need = hv && m_ref != -INFINITY && mc > m_ref + kRescaleAbove;
+                    const uint32_t wneed = __ballot_sync(0xffffffffu, need);
+                    if (lane == 0) S.flag[sb][q] = wneed;
+                    float alpha = 1.f;
+                    if (need) {
+                        alpha = exp2f(m_ref - mc);
+                        m_ref = mc;
+                        l *= alpha;
+                    } else if (m_ref == -INFINITY) {
+                        m_ref = mc;
+                    }
+                    named_bar_sync(kBarSm, kSmThreads);
+                    const bool any = (S.flag[sb][0] | S.flag[sb][1] | S.flag[sb][2] | S.flag[sb][3]) != 0;
+                    if (any && k % kFlush != 0) {
+                        if (!upper) S.alpha[hl] = alpha;
+                        mbar_wait(&S.pfree, (n_sm - 1) & 1u, A.status);   // the product before this one
+                        named_bar_sync(kBarSm, kSmThreads);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int dd = 0; dd < ndt; ++dd)
+#pragma unroll 1
+                            for (int hb = 0; hb < 4; ++hb) {
+                                uint32_t o[16];
+                                const uint32_t ta2 = tmem + lane_off + kOCol + dd * kHG + hb * 16;
+                                tmem_ld16_raw(ta2, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * S.alpha[hb * 16 + e]);
+                                tmem_st16(ta2, o);
+                            }
+                        tmem_wait_st();
+                        tc_fence_before();
+                        named_bar_sync(kBarSm, kSmThreads);
+                    }
+                    // P = 2^(x - m_ref), rounded to bf16 (one term: the sum
+                    // is that of the rounded weights, so they add up to 1) or as
+                    // hi + lo with lo the rounded rest
+                    const float mr = m_ref == -INFINITY ? 0.f : m_ref;
+                    float sq[2] = {0.f, 0.f};
+                    uint32_t phi[16], plo[kTerms == 2 ? 16 : 1];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float p0 = fast_exp2(fmaf(x[j], xs, -mr));
+                        const float p1 = fast_exp2(fmaf(x[j + 1], xs, -mr));
+                        const uint32_t hi = pack_bf16x2(p0, p1);
+                        const float g0 = __uint_as_float(hi << 16), g1 = __uint_as_float(hi & 0xFFFF0000u);
+                        phi[j >> 1] = hi;
+                        if (kTerms == 2) {
+                            sq[(j >> 1) & 1] += p0 + p1;
+                            plo[kTerms == 2 ? (j >> 1) : 0] = pack_bf16x2(p0 - g0, p1 - g1);
+                        } else {
+                            sq[(j >> 1) & 1] += g0 + g1;
+                        }
+                    }
+                    const float sum = sq[0] + sq[1];
+                    l += sum + __shfl_xor_sync(0xffffffffu, sum, 16);
+                    if (n_sm > 0) mbar_wait(&S.pfree, (n_sm - 1) & 1u, A.status);
+                    {
+                        uint8_t *pr = sP + hl * 128;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t sw = static_cast<uint32_t>((((upper ? 4 : 0) + e) ^ (hl & 7)) << 4);
+                            *reinterpret_cast<uint4 *>(pr + sw) =
+                                make_uint4(phi[4 * e], phi[4 * e + 1], phi[4 * e + 2], phi[4 * e + 3]);
+                            if (kTerms == 2)
+                                *reinterpret_cast<uint4 *>(pr + kPBytes + sw) =
+                                    make_uint4(plo[(4 * e) % (kTerms == 2 ? 16 : 1)], plo[(4 * e + 1) % (kTerms == 2 ? 16 : 1)],
+                                               plo[(4 * e + 2) % (kTerms == 2 ? 16 : 1)], plo[(4 * e + 3) % (kTerms == 2 ? 16 : 1)]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(&S.pfull);
+
+                    const bool last = k + 1 == nch;
+                    if (!last && (k + 1) % kFlush != 0) continue;
+                    // ---- O^T into the partial, or the output
+                    const bool add = k >= kFlush;        // the partial already holds earlier chunks
+                    const bool part = (r.flags & kRecPart) || !last;
+                    if (!upper) {
+                        S.flush[hl] = m_flush == -INFINITY ? 1.f : exp2f(m_flush - m_ref);
+                        float f = 1.f;
+                        if (!part) {
+                            float z = l;
+                            if (A.sinks && hv && m_ref != -INFINITY) z += exp2f(A.sinks[h0 + hl] * kLog2e - m_ref);
+                            f = (z > 0.f && l > 0.f) ? 1.f / z : 0.f;
+                        }
+                        S.fin[hl] = f;
+                    }
+                    m_flush = m_ref;
+                    mbar_wait(&S.pfree, n_sm & 1u, A.status);
+                    named_bar_sync(kBarSm, kSmThreads);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int dd = 0; dd < ndt; ++dd) {
+                        const int d = (dt0 + dd) * 128 + q * 32 + lane;
+                        uint32_t o[4][16];
+#pragma unroll
+                        for (int hb = 0; hb < 4; ++hb) tmem_ld16_raw(tmem + lane_off + kOCol + dd * kHG + hb * 16, o[hb]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int hb = 0; hb < 4; ++hb)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const int h = hb * 16 + e;
+                                if (h >= hmax) continue;
+                                float v = __uint_as_float(o[hb][e]);
+                                if (add) v = fmaf(po[h * kHD + d], S.flush[h], v);
+                                if (part) po[h * kHD + d] = v;
+                                else if (kTerms == 1)
+                                    static_cast<__nv_bfloat16 *>(A.out)[obase + h * kHD + d] = __float2bfloat16(v * S.fin[h]);
+                                else static_cast<float *>(A.out)[obase + h * kHD + d] = v * S.fin[h];
+                            }
+                    }
+                    tc_fence_before();
+                    mbar_arrive(&S.ofree);
+                    if (last && (r.flags & kRecPart) && !upper && hv && dt0 == 0) {
+                        float *ml = A.part_ml + (static_cast<int64_t>(r.slot) * H + h0 + hl) * 2;
+                        ml[0] = m_ref;
+                        ml[1] = l;
+                    }
+                }
+            }
+        }
+        if (!more) break;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
     }
 }
 
+// Joins the parts of a cut token, a CTA per (token, head, column part):
+//   out = sum_s 2^(m_s - M) O_s / (sum_s 2^(m_s - M) l_s [+ 2^(sink - M)]).
+// Thread (sub, c4) adds four columns of parts sub, sub + nsub, ... in order;
+// the subs meet in shared memory in order.
+constexpr int kJoinThreads = 256;
+
+template <int kCw, bool kBf16>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArgs A) {
+    constexpr int kSub = kJoinThreads / kCw;
+    __shared__ float wgt[kMaxCtas];
+    __shared__ float inv_z;
+    __shared__ float4 red[kJoinThreads];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int2 meta = A.meta[blockIdx.x];
+    const int ns = meta.y;
+    if (ns <= 0 || ns > kMaxCtas) return;
+    const int split = meta.x >> 1;
+    // by token: entry x is token x; by CTA: the token is written behind the list
+    const int t = A.L.num_tokens <= static_cast<int>(gridDim.x) ? static_cast<int>(blockIdx.x)
+                                                                 : A.meta[gridDim.x + blockIdx.x].x;
+    const int h = blockIdx.y, tid = threadIdx.x, c4 = tid % kCw, sub = tid / kCw;
+    const int col = static_cast<int>(blockIdx.z) * 4 * kCw + 4 * c4;
+    auto slot = [&](int k) { return k == 0 ? meta.x : 2 * (split + k); };
+    if (tid < 32) {
+        float M = -INFINITY;
+        for (int k = tid; k < ns; k += 32)
+            M = fmaxf(M, A.part_ml[(static_cast<int64_t>(slot(k)) * A.H + h) * 2]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float sink = A.sinks ? A.sinks[h] * kLog2e : -INFINITY;
+        const float Mall = fmaxf(M, sink);
+        float z = 0.f;
+        for (int k = tid; k < ns; k += 32) {
+            const float2 ml = *reinterpret_cast<const float2 *>(
+                A.part_ml + (static_cast<int64_t>(slot(k)) * A.H + h) * 2);
+            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - Mall);
+            wgt[k] = w;
+            z += w * ml.y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (tid == 0) {
+            const bool some = M != -INFINITY;
+            if (A.sinks && some) z += exp2f(sink - Mall);
+            inv_z = some && z > 0.f ? 1.f / z : 0.f;
+        }
+    }
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = sub; k < ns; k += kSub) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+            A.part_o + (static_cast<int64_t>(slot(k)) * A.H + h) * kHD + col));
+        const float w = wgt[k];
+        if (w != 0.f) {
+            acc.x = fmaf(w, v.x, acc.x);
+            acc.y = fmaf(w, v.y, acc.y);
+            acc.z = fmaf(w, v.z, acc.z);
+            acc.w = fmaf(w, v.w, acc.w);
+        }
+    }
+    red[tid] = acc;
+    __syncthreads();
+    if (sub == 0) {
+        for (int j = 1; j < kSub; ++j) {
+            const float4 v = red[j * kCw + c4];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+        }
+        const float f = inv_z;
+        const int64_t at = (static_cast<int64_t>(t) * A.H + h) * kHD + col;
+        if (kBf16)
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(A.out) + at) =
+                make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(A.out) + at) =
+                make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    }
+}
+
+int groups_of(const csa_params_t &p) { return (p.n_heads + kHG - 1) / kHG; }
+
+struct Ws {
+    size_t meta, ml, o, total;
+};
+Ws ws_plan(const csa_params_t &p) {
+    const size_t slots = 2 * static_cast<size_t>(kMaxCtas / groups_of(p));
+    Ws w{};
+    w.meta = 0;
+    w.ml = 2 * kMaxCtas * sizeof(int2) / 256 * 256 + 256;
+    w.o = w.ml + (slots * p.n_heads * 8 + 255) / 256 * 256;
+    w.total = w.o + slots * p.n_heads * kHD * 4;
+    return w;
+}
+
+template <int kTerms>
+size_t smem_bytes() { return 1024 + kQBytes + kStages * kStageBytes + kTerms * kPBytes + sizeof(Smem); }
+
 }  // namespace
 
-size_t paged_attention_workspace(const csa_paged_layout_t &, const csa_params_t &) { return 256; }
+size_t paged_attention_workspace(const csa_paged_layout_t &, const csa_params_t &p) {
+    return ws_plan(p).total;
+}
 
 cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L,
                                    const csa_params_t &p, const void *cache, int64_t num_pages,
                                    int64_t page_stride, const void *q, const float *sinks,
-                                   csa_type_t out_type, void *out, int32_t *status, void *) {
+                                   csa_type_t out_type, void *out, int32_t *status, void *ws) {
+    const int H = p.n_heads, groups = groups_of(p);
+    const int64_t total_rows = (num_pages - 1) * page_stride + L.page_rows;
+    CUtensorMap tq, tr;
+    {
+        // [64 columns][heads][8 column groups][tokens]
+        const uint64_t dims[4] = {64, static_cast<uint64_t>(H), 8, static_cast<uint64_t>(L.num_tokens)};
+        const uint64_t strides[3] = {kHD * 2, 128, static_cast<uint64_t>(H) * kHD * 2};
+        const uint32_t box[4] = {64, kHG, 8, 1};
+        if (encode_tensor_map_bf16(&tq, q, 4, dims, strides, box) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    {
+        // [64 columns][rows of the pool][8 column groups]
+        const uint64_t dims[3] = {64, static_cast<uint64_t>(total_rows), 8};
+        const uint64_t strides[2] = {kHD * 2, 128};
+        const uint32_t box[3] = {64, 8, 8};
+        if (encode_tensor_map_bf16(&tr, cache, 3, dims, strides, box) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    const Ws w = ws_plan(p);
+    uint8_t *wb = static_cast<uint8_t *>(ws);
     PagedArgs A{};
     A.L = L;
-    A.H = p.n_heads;
+    A.H = H;
     A.window = p.window;
     A.ratio = p.ratio;
-    A.scale = p.scale;
-    A.cache = static_cast<const __nv_bfloat16 *>(cache);
+    A.bf16_out = out_type == CSA_BF16;
+    A.scale_log2 = p.scale * kLog2e;
+    A.total_rows = static_cast<int32_t>(total_rows);
     A.num_pages = num_pages;
     A.page_stride = page_stride;
-    A.q = static_cast<const __nv_bfloat16 *>(q);
+    A.cache = static_cast<const __nv_bfloat16 *>(cache);
     A.sinks = sinks;
     A.out = out;
-    A.bf16_out = out_type == CSA_BF16;
+    A.meta = reinterpret_cast<int2 *>(wb + w.meta);
+    A.part_ml = reinterpret_cast<float *>(wb + w.ml);
+    A.part_o = reinterpret_cast<float *>(wb + w.o);
     A.status = status;
-    paged_attention_kernel<<<dim3(p.n_heads, L.num_tokens), kThreads, 0, lc.stream>>>(A);
-    return cudaGetLastError();
+    const int ctas = (lc.sm_count < kMaxCtas ? lc.sm_count : kMaxCtas) / groups;
+    auto kern = A.bf16_out ? paged_attention_kernel<1> : paged_attention_kernel<2>;
+    const size_t smem = A.bf16_out ? smem_bytes<1>() : smem_bytes<2>();
+    cudaError_t e = set_kernel_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(ctas, groups), dim3(kThreads), smem, lc.stream, tq, tr, A);
+    if (e != cudaSuccess) return e;
+    // no token can be cut: nothing to join
+    const int64_t slots_max = (static_cast<int64_t>(L.max_pages) * L.page_rows + 7) / 8 * 8 + p.window;
+    if (slots_max <= kCutAbove * kChunk) return cudaSuccess;
+    const int entries = L.num_tokens < ctas ? L.num_tokens : ctas;
+    const bool wide = static_cast<int64_t>(entries) * H > 2 * lc.sm_count;
+    auto join = wide ? (A.bf16_out ? paged_join_kernel<128, true> : paged_join_kernel<128, false>)
+                     : (A.bf16_out ? paged_join_kernel<32, true> : paged_join_kernel<32, false>);
+    return launch_pdl(join, dim3(entries, H, wide ? 1 : 4), dim3(kJoinThreads), 0, lc.stream, A);
 }
 
 }  // namespace csa
