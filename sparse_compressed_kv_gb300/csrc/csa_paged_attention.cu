@@ -29,6 +29,8 @@
 // into the CTA's own f32 partial and starts again from zero.
 #include <math.h>
 
+#include <type_traits>
+
 #include "csa_device.cuh"
 #include "csa_internal.h"
 
@@ -86,7 +88,7 @@ constexpr int kRecZero = 2;   // a token without rows: zeros
 
 struct Smem {
     uint64_t q_full, q_free;
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kStages], empty[kStages][4];   // a stage is released 16 rows at a time
     uint64_t sfull[2], sfree[2];
     uint64_t pfull, pfree, ofree;
     uint32_t tmem_holder;
@@ -106,6 +108,18 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
                  "r"(bytes)
                  : "memory");
+}
+
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, P;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
@@ -236,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&S.q_free, 1);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&S.full[i], 4);
-            mbar_init(&S.empty[i], 1);
+            for (int k = 0; k < 4; ++k) mbar_init(&S.empty[i][k], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.sfull[i], 1);
@@ -437,93 +451,118 @@ __global__ void __launch_bounds__(kThreads, 1)
 
         if (warp == 1) {
             // -------------------------------------------- MMA issuer
-            if (lane == 0) {
-                constexpr uint32_t id_qk = idesc_bf16<kHG, kChunk, false>();
-                constexpr uint32_t id_pv = idesc_bf16<128, kHG, true>();
-                const uint64_t q_desc = sw128_desc(smem_addr(sQ), 16, 1024);
-                const uint64_t r_desc = sw128_desc(smem_addr(sRows), 16, kGroupBytes);
-                const uint64_t a_desc = sw128_desc(smem_addr(sRows) + 2 * dt0 * 1024, 1024, kGroupBytes);
-                const uint64_t p_desc = sw128_desc(smem_addr(sP), 16, 1024);
-                auto off = [](uint32_t bytes) { return static_cast<uint64_t>(bytes >> 4); };
-                auto live = [&](int i) {
-                    while (i < nrec && S.rec[i].c1 <= S.rec[i].c0) ++i;
-                    return i;
-                };
-                int rl = live(0);                  // segment whose Q is loaded next
-                int rq = rl, cq = 0;               // next S product: segment, chunk of it
-                int rp = rl, cp = 0;               // next O^T product
-                bool dead = false;
-                uint32_t polls = 0;
-                uint64_t t_start = 0;
-                while (rp < nrec) {
-                    bool did = false;
-                    // Q of the next segment once the last S product of the one
-                    // before it is done with the buffer
-                    if (rl < nrec && rl == rq &&
-                        (n_ql == 0 || dead || mbar_try_wait(&S.q_free, (n_ql - 1) & 1u))) {
+            // The whole warp keeps step and one elected thread issues: behind
+            // elect.sync the descriptors stay in uniform registers (a 64 x 64 x 16
+            // instruction every 33 cycles; behind `lane == 0`, every 54).
+            constexpr uint32_t id_qk = idesc_bf16<kHG, kChunk, false>();
+            constexpr uint32_t id_pv = idesc_bf16<128, kHG, true>();
+            const uint64_t q_desc = sw128_desc(smem_addr(sQ), 16, 1024);
+            const uint64_t r_desc = sw128_desc(smem_addr(sRows), 16, kGroupBytes);
+            const uint64_t a_desc = sw128_desc(smem_addr(sRows) + 2 * dt0 * 1024, 1024, kGroupBytes);
+            const uint64_t p_desc = sw128_desc(smem_addr(sP), 16, 1024);
+            auto off = [](uint32_t bytes) { return static_cast<uint64_t>(bytes >> 4); };
+            // O^T of one chunk over ntile column tiles, 16 rows at a time, each
+            // 16 rows' slice of the stage released when its products are done
+            auto pv = [&](auto ntile, uint64_t ad, int st, bool zero) {
+#pragma unroll
+                for (int ks = 0; ks < kChunk / 16; ++ks) {
+#pragma unroll
+                    for (int dd = 0; dd < ntile; ++dd) {
+                        const uint64_t av = ad + off(2 * dd * 1024 + ks * 2 * kGroupBytes);
+                        const uint32_t d = tmem + kOCol + dd * kHG;
+                        umma_bf16(d, av, p_desc + off(ks * 32), id_pv, ks > 0 ? 1u : (zero ? 0u : 1u));
+                        if (kTerms == 2) umma_bf16(d, av, p_desc + off(kPBytes + ks * 32), id_pv, 1u);
+                    }
+                    umma_commit(&S.empty[st][ks]);
+                }
+                umma_commit(&S.pfree);
+            };
+            // (test_wait: a try_wait may sleep on one barrier while another is ready)
+            auto ready = [&](uint64_t *bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) != 0;
+            };
+            auto live = [&](int i) {
+                while (i < nrec && S.rec[i].c1 <= S.rec[i].c0) ++i;
+                return i;
+            };
+            int rl = live(0);                  // segment whose Q is loaded next
+            int rq = rl, cq = 0;               // next S product: segment, chunk of it
+            int rp = rl, cp = 0;               // next O^T product
+            bool dead = false;
+            uint32_t polls = 0;
+            uint64_t t_start = 0;
+            while (rp < nrec) {
+                bool did = false;
+                // Q of the next segment once the last S product of the one
+                // before it is done with the buffer
+                if (rl < nrec && rl == rq && (n_ql == 0 || dead || ready(&S.q_free, (n_ql - 1) & 1u))) {
+                    if (elect_one()) {
                         mbar_arrive_expect_tx(&S.q_full, kQBytes);
                         tma_load_4d(sQ, &tm_q, 0, h0, 0, S.rec[rl].t, &S.q_full, policy_evict_normal());
-                        ++n_ql;
-                        rl = live(rl + 1);
-                        did = true;
                     }
-                    if (rq < nrec && rl != rq && nq <= np + 1) {
-                        const int st = nq % kStages, sb = nq & 1u;
-                        if (dead || (mbar_try_wait(&S.q_full, (n_ql - 1) & 1u) &&
-                                     mbar_try_wait(&S.full[st], (nq / kStages) & 1u) &&
-                                     mbar_try_wait(&S.sfree[sb], ((nq >> 1) & 1u) ^ 1u))) {
-                            tc_fence_after();
+                    __syncwarp();
+                    ++n_ql;
+                    rl = live(rl + 1);
+                    did = true;
+                }
+                if (rq < nrec && rl != rq && nq <= np + 1) {
+                    const int st = nq % kStages, sb = nq & 1u;
+                    if (dead || (ready(&S.q_full, (n_ql - 1) & 1u) && ready(&S.full[st], (nq / kStages) & 1u) &&
+                                 ready(&S.sfree[sb], ((nq >> 1) & 1u) ^ 1u))) {
+                        tc_fence_after();
+                        const bool end = cq + 1 == S.rec[rq].c1 - S.rec[rq].c0;
+                        if (elect_one()) {
                             const uint64_t rd = r_desc + off(st * kStageBytes);
                             const uint32_t d = tmem + kSCol + sb * kChunk;
 #pragma unroll
                             for (int kk = 0; kk < 32; ++kk) {
                                 const uint32_t cg = kk >> 2, ko = (kk & 3) * 32;
-                                umma_bf16(d, q_desc + off(cg * (kHG * 128) + ko), rd + off(cg * 1024 + ko),
-                                          id_qk, kk > 0 ? 1u : 0u);
+                                umma_bf16(d, q_desc + off(cg * (kHG * 128) + ko), rd + off(cg * 1024 + ko), id_qk,
+                                          kk > 0 ? 1u : 0u);
                             }
                             umma_commit(&S.sfull[sb]);
-                            ++nq;
-                            if (++cq == S.rec[rq].c1 - S.rec[rq].c0) {
-                                umma_commit(&S.q_free);
-                                cq = 0;
-                                rq = live(rq + 1);
-                            }
-                            did = true;
+                            if (end) umma_commit(&S.q_free);
                         }
+                        __syncwarp();
+                        ++nq;
+                        ++cq;
+                        if (end) {
+                            cq = 0;
+                            rq = live(rq + 1);
+                        }
+                        did = true;
                     }
-                    if (!did && np < nq) {
-                        const int st = np % kStages;
-                        const bool zero = cp % kFlush == 0;
-                        if (dead || (mbar_try_wait(&S.pfull, np & 1u) &&
-                                     (!zero || n_of == 0 || mbar_try_wait(&S.ofree, (n_of - 1) & 1u)))) {
-                            tc_fence_after();
-                            if (zero) ++n_of;
+                }
+                if (!did && np < nq) {
+                    const int st = np % kStages;
+                    const bool zero = cp % kFlush == 0;
+                    if (dead || (ready(&S.pfull, np & 1u) &&
+                                 (!zero || n_of == 0 || ready(&S.ofree, (n_of - 1) & 1u)))) {
+                        tc_fence_after();
+                        if (zero) ++n_of;
+                        if (elect_one()) {
                             const uint64_t ad = a_desc + off(st * kStageBytes);
-#pragma unroll 1
-                            for (int dd = 0; dd < ndt; ++dd)
-#pragma unroll
-                                for (int ks = 0; ks < kChunk / 16; ++ks) {
-                                    const uint64_t av = ad + off(2 * dd * 1024 + ks * 2 * kGroupBytes);
-                                    const uint32_t d = tmem + kOCol + dd * kHG;
-                                    umma_bf16(d, av, p_desc + off(ks * 32), id_pv, (zero && ks == 0) ? 0u : 1u);
-                                    if (kTerms == 2) umma_bf16(d, av, p_desc + off(kPBytes + ks * 32), id_pv, 1u);
-                                }
-                            umma_commit(&S.empty[st]);
-                            umma_commit(&S.pfree);
-                            ++np;
-                            if (++cp == S.rec[rp].c1 - S.rec[rp].c0) {
-                                cp = 0;
-                                rp = live(rp + 1);
-                            }
-                            did = true;
+                            if (ndt == 4) pv(std::integral_constant<int, 4>{}, ad, st, zero);
+                            else if (ndt == 2) pv(std::integral_constant<int, 2>{}, ad, st, zero);
+                            else pv(std::integral_constant<int, 1>{}, ad, st, zero);
                         }
+                        __syncwarp();
+                        ++np;
+                        if (++cp == S.rec[rp].c1 - S.rec[rp].c0) {
+                            cp = 0;
+                            rp = live(rp + 1);
+                        }
+                        did = true;
                     }
-                    if (did) {
-                        polls = 0;
-                    } else if (++polls == 1) {
-                        t_start = global_timer_ns();
-                    } else if ((polls & 1023u) == 0 && global_timer_ns() - t_start > kWaitNs) {
-                        raise_status(A.status, CSA_DEV_TIMEOUT);
+                }
+                if (did) {
+                    polls = 0;
+                } else if (++polls == 1) {
+                    t_start = global_timer_ns();
+                } else if ((polls & 1023u) == 0) {
+                    const bool late = global_timer_ns() - t_start > kWaitNs;
+                    if (__any_sync(0xffffffffu, late)) {
+                        if (lane == 0) raise_status(A.status, CSA_DEV_TIMEOUT);
                         dead = true;
                     }
                 }
@@ -583,8 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const int st = n_fetch % kStages;
                     const uint32_t ph = ((n_fetch / kStages) & 1u) ^ 1u;
-                    if (pending >= 0 && !__all_sync(0xffffffffu, mbar_try_wait(&S.empty[st], ph))) land(false);
-                    mbar_wait(&S.empty[st], ph, A.status);
+                    if (pending >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(&S.empty[st][li], ph))) land(false);
+                    mbar_wait(&S.empty[st][li], ph, A.status);
                     __syncwarp();
                     uint8_t *rows = sRows + st * kStageBytes + 2 * li * kGroupBytes;
                     if (lane == 0) {
@@ -781,26 +820,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_wait(&S.pfree, n_sm & 1u, A.status);
                     named_bar_sync(kBarSm, kSmThreads);
                     tc_fence_after();
+                    const bool full_group = hmax == kHG;
 #pragma unroll 1
                     for (int dd = 0; dd < ndt; ++dd) {
                         const int d = (dt0 + dd) * 128 + q * 32 + lane;
-                        uint32_t o[4][16];
+                        float *const pd = po + d;
+#pragma unroll 1
+                        for (int hb = 0; hb < kHG; hb += 32) {
+                            uint32_t o[32];
+                            tmem_ld16_raw(tmem + lane_off + kOCol + dd * kHG + hb, *reinterpret_cast<uint32_t(*)[16]>(o));
+                            tmem_ld16_raw(tmem + lane_off + kOCol + dd * kHG + hb + 16,
+                                          *reinterpret_cast<uint32_t(*)[16]>(o + 16));
+                            tmem_wait_ld();
+                            float *const ph2 = pd + hb * kHD;
+                            if (add) {
+                                float old[32];
 #pragma unroll
-                        for (int hb = 0; hb < 4; ++hb) tmem_ld16_raw(tmem + lane_off + kOCol + dd * kHG + hb * 16, o[hb]);
-                        tmem_wait_ld();
+                                for (int e = 0; e < 32; ++e) old[e] = hb + e < hmax ? ph2[e * kHD] : 0.f;
 #pragma unroll
-                        for (int hb = 0; hb < 4; ++hb)
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const int h = hb * 16 + e;
-                                if (h >= hmax) continue;
-                                float v = __uint_as_float(o[hb][e]);
-                                if (add) v = fmaf(po[h * kHD + d], S.flush[h], v);
-                                if (part) po[h * kHD + d] = v;
-                                else if (kTerms == 1)
-                                    static_cast<__nv_bfloat16 *>(A.out)[obase + h * kHD + d] = __float2bfloat16(v * S.fin[h]);
-                                else static_cast<float *>(A.out)[obase + h * kHD + d] = v * S.fin[h];
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(fmaf(old[e], S.flush[hb + e], __uint_as_float(o[e])));
                             }
+                            if (part && full_group) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) ph2[e * kHD] = __uint_as_float(o[e]);
+                            } else if (part) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (hb + e < hmax) ph2[e * kHD] = __uint_as_float(o[e]);
+                            } else if (kTerms == 1) {
+                                __nv_bfloat16 *const od = static_cast<__nv_bfloat16 *>(A.out) + obase + hb * kHD + d;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (hb + e < hmax)
+                                        od[e * kHD] = __float2bfloat16(__uint_as_float(o[e]) * S.fin[hb + e]);
+                            } else {
+                                float *const od = static_cast<float *>(A.out) + obase + hb * kHD + d;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (hb + e < hmax) od[e * kHD] = __uint_as_float(o[e]) * S.fin[hb + e];
+                            }
+                        }
                     }
                     tc_fence_before();
                     mbar_arrive(&S.ofree);
