@@ -56,6 +56,10 @@ constexpr int kMaxRec = 128;                    // segments a CTA lists at a tim
 constexpr int kMaxCtas = 152;                   // CTAs of the grid at most (sizes the workspace)
 constexpr int kSegCost = 2;                     // a segment's epilogue, in chunks
 constexpr int kCutAbove = 4;                    // chunks a token may exceed the mean before tokens are cut
+#ifndef AHEAD
+#define AHEAD 2
+#endif
+constexpr int kAhead = AHEAD;
 constexpr int kFlushF32 = 32, kFlushBf16 = 512; // chunks between roundings of the accumulator
 
 struct PagedArgs {
@@ -129,6 +133,13 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, int
         ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
         "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
         : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_l2_3d(const CUtensorMap *m, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
@@ -653,6 +664,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         cp_async_commit();
+                    }
+                    // the boxes of a later chunk on their way into L2 (lanes 0 and 1)
+                    if (lane < 2 && c + kAhead < r.c1) {
+                        const int j0 = (c + kAhead) * kChunk + 16 * li + 8 * lane;
+                        const int pg = j0 / A.L.page_rows, off0 = j0 - pg * A.L.page_rows;
+                        if (j0 + 8 <= r.n && off0 + 8 <= A.L.page_rows) {
+                            const int32_t page = A.L.table[static_cast<int64_t>(r.b) * A.L.max_pages + pg];
+                            if (page >= 0 && page < A.num_pages)
+                                tma_prefetch_l2_3d(&tm_rows, 0, static_cast<int32_t>(page * A.page_stride) + off0, 0);
+                        }
                     }
                     if (pending >= 0) land(by_row);
                     if (by_row) pending = st;
