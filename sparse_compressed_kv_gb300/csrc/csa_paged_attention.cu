@@ -13,9 +13,9 @@
 //                  groups: 8 KiB whatever the page size), other groups
 //                  (page ends, the last rows, the window) go row by row with
 //                  16-byte cp.async, rows that do not exist as zeros
-//   warp 1         issues  S = Q . rows^T        (M = 64 heads, N = 64 rows)
-//                          O^T += rows^T . P^T   (M = 128 columns, N = 64 heads)
-//                  whichever is ready, Q^T of the next segment included
+//   warp 1         Q of the next segment;  S = Q . rows^T  (M = 64 heads,
+//                  N = 64 rows, K = 512), one chunk ahead of
+//   warp 9         O^T += rows^T . P^T  (M = 128 columns a tile, N = 64 heads)
 //   warps 2..5     softmax with a lazily raised maximum; a segment's epilogue
 // A group's 8 KiB hold 8 column groups of 8 rows x 128 bytes (the swizzle
 // atom), so the same bytes are the K-major operand of S (row groups 8 KiB
@@ -37,7 +37,7 @@
 namespace csa {
 namespace {
 
-constexpr int kThreads = 288;
+constexpr int kThreads = 320;
 constexpr int kSmThreads = 128;                 // warps 2..5
 constexpr int kBarSm = 1;
 constexpr int kHG = 64;                         // heads per CTA
@@ -190,6 +190,10 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uin
     d |= static_cast<uint64_t>(2u) << 61;
     return d;
 }
+
+// a byte offset as a step of a descriptor's start-address field (every shared
+// address is below 256 KiB, so the field never carries)
+__device__ __forceinline__ constexpr uint64_t off(uint32_t bytes) { return bytes >> 4; }
 
 template <int M, int N, bool kTransA>
 __device__ __forceinline__ constexpr uint32_t idesc_bf16() {
@@ -461,19 +465,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (nrec == 0) break;
 
         if (warp == 1) {
-            // -------------------------------------------- MMA issuer
+            // -------------------------------------------- S = Q . rows^T
             // The whole warp keeps step and one elected thread issues: behind
             // elect.sync the descriptors stay in uniform registers (a 64 x 64 x 16
             // instruction every 33 cycles; behind `lane == 0`, every 54).
             constexpr uint32_t id_qk = idesc_bf16<kHG, kChunk, false>();
-            constexpr uint32_t id_pv = idesc_bf16<128, kHG, true>();
             const uint64_t q_desc = sw128_desc(smem_addr(sQ), 16, 1024);
             const uint64_t r_desc = sw128_desc(smem_addr(sRows), 16, kGroupBytes);
+            for (int i = 0; i < nrec; ++i) {
+                const int nch = S.rec[i].c1 - S.rec[i].c0;
+                if (nch <= 0) continue;
+                // the last product of the segment before is done with the buffer
+                if (n_ql > 0) mbar_wait(&S.q_free, (n_ql - 1) & 1u, A.status);
+                __syncwarp();
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&S.q_full, kQBytes);
+                    tma_load_4d(sQ, &tm_q, 0, h0, 0, S.rec[i].t, &S.q_full, policy_evict_normal());
+                }
+                __syncwarp();
+                mbar_wait(&S.q_full, n_ql & 1u, A.status);
+                ++n_ql;
+                for (int k = 0; k < nch; ++k, ++nq) {
+                    const int st = nq % kStages, sb = nq & 1u;
+                    mbar_wait(&S.full[st], (nq / kStages) & 1u, A.status);
+                    mbar_wait(&S.sfree[sb], ((nq >> 1) & 1u) ^ 1u, A.status);
+                    __syncwarp();
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t rd = r_desc + off(st * kStageBytes);
+                        const uint32_t d = tmem + kSCol + sb * kChunk;
+#pragma unroll
+                        for (int kk = 0; kk < 32; ++kk) {
+                            const uint32_t cg = kk >> 2, ko = (kk & 3) * 32;
+                            umma_bf16(d, q_desc + off(cg * (kHG * 128) + ko), rd + off(cg * 1024 + ko), id_qk,
+                                      kk > 0 ? 1u : 0u);
+                        }
+                        umma_commit(&S.sfull[sb]);
+                        if (k + 1 == nch) umma_commit(&S.q_free);
+                    }
+                    __syncwarp();
+                }
+            }
+        } else if (warp == 9) {
+            // -------------------------------------------- O^T += rows^T . P^T
+            // 16 rows at a time, each 16 rows' slice of the stage released when
+            // its products are done
+            constexpr uint32_t id_pv = idesc_bf16<128, kHG, true>();
             const uint64_t a_desc = sw128_desc(smem_addr(sRows) + 2 * dt0 * 1024, 1024, kGroupBytes);
             const uint64_t p_desc = sw128_desc(smem_addr(sP), 16, 1024);
-            auto off = [](uint32_t bytes) { return static_cast<uint64_t>(bytes >> 4); };
-            // O^T of one chunk over ntile column tiles, 16 rows at a time, each
-            // 16 rows' slice of the stage released when its products are done
             auto pv = [&](auto ntile, uint64_t ad, int st, bool zero) {
 #pragma unroll
                 for (int ks = 0; ks < kChunk / 16; ++ks) {
@@ -488,94 +527,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 umma_commit(&S.pfree);
             };
-            // (test_wait: a try_wait may sleep on one barrier while another is ready)
-            auto ready = [&](uint64_t *bar, uint32_t parity) {
-                return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) != 0;
-            };
-            auto live = [&](int i) {
-                while (i < nrec && S.rec[i].c1 <= S.rec[i].c0) ++i;
-                return i;
-            };
-            int rl = live(0);                  // segment whose Q is loaded next
-            int rq = rl, cq = 0;               // next S product: segment, chunk of it
-            int rp = rl, cp = 0;               // next O^T product
-            bool dead = false;
-            uint32_t polls = 0;
-            uint64_t t_start = 0;
-            while (rp < nrec) {
-                bool did = false;
-                // Q of the next segment once the last S product of the one
-                // before it is done with the buffer
-                if (rl < nrec && rl == rq && (n_ql == 0 || dead || ready(&S.q_free, (n_ql - 1) & 1u))) {
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&S.q_full, kQBytes);
-                        tma_load_4d(sQ, &tm_q, 0, h0, 0, S.rec[rl].t, &S.q_full, policy_evict_normal());
+            for (int i = 0; i < nrec; ++i) {
+                const int nch = S.rec[i].c1 - S.rec[i].c0;
+                for (int k = 0; k < nch; ++k, ++np) {
+                    const int st = np % kStages;
+                    const bool zero = k % kFlush == 0;
+                    mbar_wait(&S.pfull, np & 1u, A.status);
+                    if (zero) {
+                        if (n_of > 0) mbar_wait(&S.ofree, (n_of - 1) & 1u, A.status);
+                        ++n_of;
                     }
                     __syncwarp();
-                    ++n_ql;
-                    rl = live(rl + 1);
-                    did = true;
-                }
-                if (rq < nrec && rl != rq && nq <= np + 1) {
-                    const int st = nq % kStages, sb = nq & 1u;
-                    if (dead || (ready(&S.q_full, (n_ql - 1) & 1u) && ready(&S.full[st], (nq / kStages) & 1u) &&
-                                 ready(&S.sfree[sb], ((nq >> 1) & 1u) ^ 1u))) {
-                        tc_fence_after();
-                        const bool end = cq + 1 == S.rec[rq].c1 - S.rec[rq].c0;
-                        if (elect_one()) {
-                            const uint64_t rd = r_desc + off(st * kStageBytes);
-                            const uint32_t d = tmem + kSCol + sb * kChunk;
-#pragma unroll
-                            for (int kk = 0; kk < 32; ++kk) {
-                                const uint32_t cg = kk >> 2, ko = (kk & 3) * 32;
-                                umma_bf16(d, q_desc + off(cg * (kHG * 128) + ko), rd + off(cg * 1024 + ko), id_qk,
-                                          kk > 0 ? 1u : 0u);
-                            }
-                            umma_commit(&S.sfull[sb]);
-                            if (end) umma_commit(&S.q_free);
-                        }
-                        __syncwarp();
-                        ++nq;
-                        ++cq;
-                        if (end) {
-                            cq = 0;
-                            rq = live(rq + 1);
-                        }
-                        did = true;
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t ad = a_desc + off(st * kStageBytes);
+                        if (ndt == 4) pv(std::integral_constant<int, 4>{}, ad, st, zero);
+                        else if (ndt == 2) pv(std::integral_constant<int, 2>{}, ad, st, zero);
+                        else pv(std::integral_constant<int, 1>{}, ad, st, zero);
                     }
-                }
-                if (!did && np < nq) {
-                    const int st = np % kStages;
-                    const bool zero = cp % kFlush == 0;
-                    if (dead || (ready(&S.pfull, np & 1u) &&
-                                 (!zero || n_of == 0 || ready(&S.ofree, (n_of - 1) & 1u)))) {
-                        tc_fence_after();
-                        if (zero) ++n_of;
-                        if (elect_one()) {
-                            const uint64_t ad = a_desc + off(st * kStageBytes);
-                            if (ndt == 4) pv(std::integral_constant<int, 4>{}, ad, st, zero);
-                            else if (ndt == 2) pv(std::integral_constant<int, 2>{}, ad, st, zero);
-                            else pv(std::integral_constant<int, 1>{}, ad, st, zero);
-                        }
-                        __syncwarp();
-                        ++np;
-                        if (++cp == S.rec[rp].c1 - S.rec[rp].c0) {
-                            cp = 0;
-                            rp = live(rp + 1);
-                        }
-                        did = true;
-                    }
-                }
-                if (did) {
-                    polls = 0;
-                } else if (++polls == 1) {
-                    t_start = global_timer_ns();
-                } else if ((polls & 1023u) == 0) {
-                    const bool late = global_timer_ns() - t_start > kWaitNs;
-                    if (__any_sync(0xffffffffu, late)) {
-                        if (lane == 0) raise_status(A.status, CSA_DEV_TIMEOUT);
-                        dead = true;
-                    }
+                    __syncwarp();
                 }
             }
         } else if (warp == 0 || warp >= 6) {
