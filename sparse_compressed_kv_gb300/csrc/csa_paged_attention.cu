@@ -71,8 +71,8 @@ struct PagedArgs {
     const __nv_bfloat16 *cache;
     const float *sinks;
     void *out;
-    float *part_o;            // [slot][H][512]
-    float *part_ml;           // [slot][H][2]  (m in log2 units, l)
+    float4 *part_o;           // [slot][head group][tile][16 quads of heads][128 columns]: 4 heads
+    float2 *part_ml;          // [slot][head group][64 heads]: m (log2 units), l
     int2 *meta;               // by token (T <= CTAs) or by CTA: first slot, parts (0: none)
     int32_t *status;
 };
@@ -99,8 +99,8 @@ struct Smem {
     uint32_t maskw[kStages][4];
     uint32_t flag[2][4];
     float alpha[kHG];
-    float fin[kHG];
-    float flush[kHG];
+    alignas(16) float fin[kHG];
+    alignas(16) float flush[kHG];
     int32_t nrec, more;
     int64_t t0, s0;
     int64_t wsum[kThreads / 32][2];
@@ -201,12 +201,26 @@ __device__ __forceinline__ constexpr uint32_t idesc_bf16() {
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Positions and unit counts are 64-bit; a 64-bit division costs a few hundred
+// cycles on the way to the first row, so those that fit take a 32-bit one.
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+__device__ __forceinline__ int64_t mod_pos(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) % static_cast<uint32_t>(b) : a % b;
+}
+
 // What token t attends: b < 0 for padding, n = near = 0 for a bad token.
-__device__ __forceinline__ Rec token_rec(const PagedArgs &A, int t, int &bad) {
+// `per` tokens a sequence is the guess by which the sequence's length is
+// loaded in the same round trip as its number.
+__device__ __forceinline__ Rec token_rec(const PagedArgs &A, int t, int per, int &bad) {
     Rec r{};
     r.t = t;
+    const int g = min(t / per, A.L.num_seqs - 1);
     r.b = A.L.tok_seq[t];
     const int64_t pos = A.L.tok_pos[t];
+    int64_t n = A.L.row_len[g];
+    if (A.window > 0) r.first_res = A.L.swa_first_pos[g];
     bad = 0;
     if (r.b == -1) return r;
     if (r.b < 0 || r.b >= A.L.num_seqs || pos < 0) {
@@ -214,7 +228,10 @@ __device__ __forceinline__ Rec token_rec(const PagedArgs &A, int t, int &bad) {
         r.b = 0;
         return r;
     }
-    int64_t n = A.L.row_len[r.b];
+    if (r.b != g) {
+        n = A.L.row_len[r.b];
+        if (A.window > 0) r.first_res = A.L.swa_first_pos[r.b];
+    }
     const int64_t cap = static_cast<int64_t>(A.L.max_pages) * A.L.page_rows;
     if (n < 0) {
         bad |= CSA_DEV_BAD_LENGTH;
@@ -224,12 +241,11 @@ __device__ __forceinline__ Rec token_rec(const PagedArgs &A, int t, int &bad) {
         bad |= CSA_DEV_CAPACITY;
         n = cap;
     }
-    const int64_t seen = pos / A.ratio;
+    const int64_t seen = div_pos(pos, A.ratio);
     r.n = static_cast<int32_t>(n < seen ? n : seen);
     if (A.window > 0) {
         r.first = window_first(pos, A.window);
         r.near = static_cast<int32_t>(pos - r.first + 1);
-        r.first_res = A.L.swa_first_pos[r.b];
     }
     return r;
 }
@@ -283,21 +299,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     tc_fence_before();
-    pdl_wait();
-    pdl_launch_dependents();
 
     // ---------------------------------------------------- division of the work
-    // chunks and costs of all tokens, a contiguous run per thread
+    // (the layout is read before the wait for the preceding kernel, as
+    // everywhere in this library)  Chunks and costs of all tokens, a
+    // contiguous run of tokens per thread; with one token a thread its record
+    // stays in registers.
+    const int tps = max(1, T / A.L.num_seqs);
     const int per = (T + kThreads - 1) / kThreads;
     const int ta = min(T, tid * per), te = min(T, ta + per);
+    Rec own{};
+    int own_c = 0, own_bad = 0;
     int64_t chunks = 0, cost = 0;
     int maxc = 0;
     for (int t = ta; t < te; ++t) {
-        int bad;
-        const int c = rec_chunks(token_rec(A, t, bad));
-        chunks += c;
-        cost += chunk_cost(c);
-        maxc = max(maxc, c);
+        own = token_rec(A, t, tps, own_bad);
+        own_c = rec_chunks(own);
+        chunks += own_c;
+        cost += chunk_cost(own_c);
+        maxc = max(maxc, own_c);
     }
     int64_t incl = cost;
 #pragma unroll
@@ -312,12 +332,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         S.wsum[warp][1] = chunks;
         S.wmax[warp] = maxc;
     }
+    if (tid == 0) {
+        S.t0 = T;
+        S.nrec = 0;
+        S.more = 0;
+    }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem_holder;
     int64_t base = 0, U = 0;
     chunks = 0;
     maxc = 0;
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w == warp) base = U;
         U += S.wsum[w][0];
@@ -325,42 +351,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         maxc = max(maxc, S.wmax[w]);
     }
     // Tokens are cut only where that shortens the longest CTA by more than
-    // the partials and their join cost: otherwise CTA c takes token c (T <= G), or the
-    // tokens that begin in its range.
-    const bool direct = T <= G && maxc <= chunks / G + kCutAbove;
+    // the partials and their join cost: otherwise CTA c takes token c (T <= G),
+    // or the tokens that begin in its range.
+    const bool direct = T <= G && maxc <= div_pos(chunks, G) + kCutAbove;
     const bool snap = direct || (T > G && maxc <= kCutAbove);
     // few CTAs at work: 2 or 4 of them share a range, each with all of its
     // logits and weights and its share of the 512 columns
-    int dparts = 1;
-    if (direct) dparts = T * 4 <= G ? 4 : T * 2 <= G ? 2 : 1;
-    else if (!snap && T <= G) dparts = chunks * 4 <= G ? 4 : chunks <= G ? 2 : 1;
-    const int nsplit = static_cast<int>(min(static_cast<int64_t>(G / dparts), U));
-    const int split = static_cast<int>(blockIdx.x) / dparts;
-    const int ndt = 4 / dparts;                                   // 128-column tiles of this CTA
-    const int dt0 = (static_cast<int>(blockIdx.x) % dparts) * ndt;
-    int64_t ua, ub;
-    if (direct) {
-        ua = 0;
-        ub = split < T ? 1 : 0;
-    } else {
-        ua = split < nsplit ? split * U / nsplit : U;
-        ub = split < nsplit ? (split + 1) * U / nsplit : U;
+    int dlog = 0;
+    if (direct) dlog = T * 4 <= G ? 2 : T * 2 <= G ? 1 : 0;
+    else if (!snap && T <= G) dlog = chunks * 4 <= G ? 2 : chunks <= G ? 1 : 0;
+    const int dparts = 1 << dlog;
+    const int nsplit = static_cast<int>(min(static_cast<int64_t>(G >> dlog), U));
+    const int split = static_cast<int>(blockIdx.x) >> dlog;
+    const int ndt = 4 >> dlog;                                    // 128-column tiles of this CTA
+    const int dt0 = (static_cast<int>(blockIdx.x) & (dparts - 1)) * ndt;
+    int64_t ua = 0, ub = split < T ? 1 : 0;
+    if (!direct) {
+        ua = split < nsplit ? div_pos(split * U, nsplit) : U;
+        ub = split < nsplit ? div_pos((split + 1) * U, nsplit) : U;
     }
     const bool by_token = T <= G;
     const bool lead = hg == 0 && dt0 == 0;       // reports errors, writes the join's list
-    if (tid == 0) {
-        S.t0 = direct ? split : T;
-        S.s0 = 0;
-        if (lead && !by_token) A.meta[split] = make_int2(-1, 0);
-    }
-    __syncthreads();
-    if (!direct) {
-        // the first token of the range: the one that holds unit ua, or (whole
-        // tokens only) the first that begins at or behind it
+    // The first token of the range: the one that holds unit ua, or (whole
+    // tokens only) the first that begins at or behind it.
+    if (direct) {
+        if (tid == 0) S.t0 = split;
+    } else {
         int64_t s = base + incl - cost;
         for (int t = ta; t < te; ++t) {
             int bad;
-            const int64_t e = s + chunk_cost(rec_chunks(token_rec(A, t, bad)));
+            const int c = per == 1 ? own_c : rec_chunks(token_rec(A, t, tps, bad));
+            const int64_t e = s + chunk_cost(c);
             if (snap ? s >= ua : (s <= ua && ua < e)) {
                 if (snap) {
                     atomicMin(reinterpret_cast<unsigned long long *>(&S.t0), static_cast<unsigned long long>(t));
@@ -372,20 +393,108 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             s = e;
         }
-        __syncthreads();
-        if (snap) {
-            s = base + incl - cost;
-            for (int t = ta; t < te; ++t) {
-                if (t == S.t0) S.s0 = s;
-                int bad;
-                s += chunk_cost(rec_chunks(token_rec(A, t, bad)));
-            }
-            __syncthreads();
+    }
+    __syncthreads();
+    if (per > 1 && snap && !direct) {
+        int64_t s = base + incl - cost;
+        for (int t = ta; t < te; ++t) {
+            if (t == S.t0) S.s0 = s;
+            int bad;
+            s += chunk_cost(rec_chunks(token_rec(A, t, tps, bad)));
         }
+        __syncthreads();
     }
     int64_t t0 = S.t0, s0 = S.s0;
 
-    // pipeline positions, kept across batches of segments
+    // Lists the segment of one token (whose units begin at s) as entry `at`.
+    // Returns the token's entry for the join; `owner`: its first chunk is here.
+    auto list = [&](Rec &r, int c, int64_t s, int at, bool &owner) {
+        int2 m = make_int2(-1, 0);
+        owner = true;
+        r.c0 = 0;
+        r.c1 = c;
+        r.slot = 2 * split + 1;
+        if (!snap) {
+            owner = s >= ua;
+            r.c0 = static_cast<int32_t>(min(max(ua - s, int64_t(0)), int64_t(c)));
+            r.c1 = static_cast<int32_t>(min(ub - s, int64_t(c)));
+            if (!owner) r.slot = 2 * split;
+            // the split that holds the token's last chunk
+            if (owner && c > 0) {
+                const int64_t last = div_pos((s + c) * nsplit - 1, U);
+                if (last > split) m = make_int2(r.slot, static_cast<int>(last) - split + 1);
+            }
+            if (r.c1 - r.c0 < c) r.flags |= kRecPart;
+        }
+        if (r.b >= 0 && c == 0 && owner) r.flags |= kRecZero;
+        S.rec[at] = r;
+        atomicAdd(&S.nrec, 1);
+        if (at == kMaxRec - 1 && !direct) {
+            S.more = 1;
+            S.s0 = s + chunk_cost(c);
+        }
+        return m;
+    };
+    auto report = [&](const Rec &r, int bad, int2 m) {
+        raise_status(A.status, bad);
+        if (by_token) {
+            A.meta[r.t] = m;
+        } else if (m.y > 0) {
+            A.meta[split] = m;
+            A.meta[G + split] = make_int2(r.t, 0);
+        }
+    };
+    // thread i lists token t0 + i
+    auto list_next = [&]() {
+        Rec r{};
+        int bad = 0, c = 0;
+        int64_t w = 0;
+        const bool in = tid < kMaxRec && t0 + tid < T && ub > ua;
+        if (in) {
+            r = token_rec(A, static_cast<int>(t0) + tid, tps, bad);
+            c = rec_chunks(r);
+            w = chunk_cost(c);
+        }
+        int64_t run = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += v;
+        }
+        if (lane == 31) S.wsum[warp][0] = run;
+        __syncthreads();
+        int64_t s = s0 + run - w;
+        for (int k = 0; k < kMaxRec / 32; ++k)
+            if (k < warp) s += S.wsum[k][0];
+        if (in && s < ub) {
+            bool owner;
+            const int2 m = list(r, c, s, tid, owner);
+            if (lead && owner) report(r, bad, m);
+        }
+    };
+    if (per == 1) {
+        // the first list, from the registers
+        const int at = tid - static_cast<int>(t0);
+        const int64_t s = base + incl - cost;
+        bool owner = false;
+        int2 m = make_int2(-1, 0);
+        if (at >= 0 && at < kMaxRec && tid < T && ub > ua && (direct ? at == 0 : s < ub))
+            m = list(own, own_c, s, at, owner);
+        pdl_wait();
+        pdl_launch_dependents();
+        if (!by_token) {
+            if (lead && tid == 0) A.meta[split] = make_int2(-1, 0);
+            __syncthreads();
+        }
+        if (lead && owner) report(own, own_bad, m);
+    } else {
+        pdl_wait();
+        pdl_launch_dependents();
+        if (lead && tid == 0) A.meta[split] = make_int2(-1, 0);
+        list_next();
+    }
+
+    // pipeline positions, kept across lists of segments
     uint32_t n_fetch = 0;                // chunks fetched
     uint32_t nq = 0, np = 0;             // chunks whose S / O^T product was issued
     uint32_t n_ql = 0;                   // Q loads issued
@@ -393,73 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n_sm = 0;                   // chunks through the softmax
 
     for (;;) {
-        // ------------------------------------------------ the next segments
-        __syncthreads();                 // the previous list is done with
-        if (tid == 0) {
-            S.nrec = 0;
-            S.more = 0;
-        }
         __syncthreads();
-        {
-            Rec r{};
-            int bad = 0, c = 0;
-            int64_t w = 0;
-            const bool in = tid < kMaxRec && t0 + tid < T && ub > ua;
-            if (in) {
-                r = token_rec(A, static_cast<int>(t0) + tid, bad);
-                c = rec_chunks(r);
-                w = chunk_cost(c);
-            }
-            int64_t run = w;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += v;
-            }
-            if (lane == 31) S.wsum[warp][0] = run;
-            __syncthreads();
-            int64_t s = s0 + run - w, all = s0;
-            for (int k = 0; k < kMaxRec / 32; ++k) {
-                if (k < warp) s += S.wsum[k][0];
-                all += S.wsum[k][0];
-            }
-            const bool mine = in && (direct ? tid == 0 : s < ub);
-            if (mine) {
-                r.c0 = 0;
-                r.c1 = c;
-                bool owner = true;
-                int2 m = make_int2(-1, 0);
-                r.slot = 2 * split + 1;
-                if (!snap) {
-                    owner = s >= ua;
-                    r.c0 = static_cast<int32_t>(min(max(ua - s, int64_t(0)), int64_t(c)));
-                    r.c1 = static_cast<int32_t>(min(ub - s, int64_t(c)));
-                    if (!owner) r.slot = 2 * split;
-                    // the split that holds the token's last chunk
-                    if (owner && c > 0) {
-                        const int64_t last = ((s + c) * nsplit - 1) / U;
-                        if (last > split) m = make_int2(r.slot, static_cast<int>(last) - split + 1);
-                    }
-                    if (r.c1 - r.c0 < c) r.flags |= kRecPart;
-                }
-                if (r.b >= 0 && c == 0 && owner) r.flags |= kRecZero;
-                if (lead && owner) {
-                    raise_status(A.status, bad);
-                    if (by_token) {
-                        A.meta[r.t] = m;
-                    } else if (m.y > 0) {
-                        A.meta[split] = m;
-                        A.meta[G + split] = make_int2(r.t, 0);
-                    }
-                }
-                S.rec[tid] = r;
-                atomicAdd(&S.nrec, 1);
-                if (tid == kMaxRec - 1 && !direct) S.more = 1;
-            }
-            t0 += kMaxRec;
-            s0 = all;
-        }
-        __syncthreads();
+        t0 += kMaxRec;
+        s0 = S.s0;
         const int nrec = S.nrec;
         const bool more = S.more != 0;
         if (nrec == 0) break;
@@ -587,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (x < r.first_res) bad |= CSA_DEV_MISSING_SWA;
                         else
                             src = static_cast<const __nv_bfloat16 *>(A.L.swa_kv) +
-                                  (static_cast<int64_t>(r.b) * A.L.swa_cap + x % A.L.swa_cap) * kHD;
+                                  (static_cast<int64_t>(r.b) * A.L.swa_cap + mod_pos(x, A.L.swa_cap)) * kHD;
                     }
                     const uint32_t okm = __ballot_sync(0xffffffffu, src != nullptr) & 0xFFFFu;
                     // a group of 8 rows of one page is one box
@@ -677,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     continue;
                 }
                 float m_ref = -INFINITY, l = 0.f, m_flush = -INFINITY;
-                float *const po = A.part_o + (static_cast<int64_t>(r.slot) * H + h0) * kHD;
+                const int64_t pslot = static_cast<int64_t>(r.slot) * gridDim.y + hg;
                 for (int k = 0; k < nch; ++k, ++n_sm) {
                     const int st = n_sm % kStages, sb = n_sm & 1u;
                     mbar_wait(&S.sfull[sb], (n_sm >> 1) & 1u, A.status);
@@ -811,59 +856,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_wait(&S.pfree, n_sm & 1u, A.status);
                     named_bar_sync(kBarSm, kSmThreads);
                     tc_fence_after();
-                    const bool full_group = hmax == kHG;
 #pragma unroll 1
                     for (int dd = 0; dd < ndt; ++dd) {
-                        const int d = (dt0 + dd) * 128 + q * 32 + lane;
-                        float *const pd = po + d;
+                        // one column per lane; a partial keeps four heads together, so
+                        // that a warp stores 512 contiguous bytes
+                        const int dl = q * 32 + lane;
+                        float4 *const pd = A.part_o + (pslot * 4 + dt0 + dd) * (16 * 128) + dl;
 #pragma unroll 1
                         for (int hb = 0; hb < kHG; hb += 32) {
+                            if (hb >= hmax) break;
                             uint32_t o[32];
                             tmem_ld16_raw(tmem + lane_off + kOCol + dd * kHG + hb, *reinterpret_cast<uint32_t(*)[16]>(o));
                             tmem_ld16_raw(tmem + lane_off + kOCol + dd * kHG + hb + 16,
                                           *reinterpret_cast<uint32_t(*)[16]>(o + 16));
-                            tmem_wait_ld();
-                            float *const ph2 = pd + hb * kHD;
+                            float4 *const pq = pd + hb / 4 * 128;
                             if (add) {
-                                float old[32];
+                                float4 old[8];
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) old[e] = hb + e < hmax ? ph2[e * kHD] : 0.f;
+                                for (int e = 0; e < 8; ++e) old[e] = pq[e * 128];
+                                tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    o[e] = __float_as_uint(fmaf(old[e], S.flush[hb + e], __uint_as_float(o[e])));
+                                for (int e = 0; e < 8; ++e) {
+                                    const float4 f = *reinterpret_cast<const float4 *>(S.flush + hb + 4 * e);
+                                    o[4 * e] = __float_as_uint(fmaf(old[e].x, f.x, __uint_as_float(o[4 * e])));
+                                    o[4 * e + 1] = __float_as_uint(fmaf(old[e].y, f.y, __uint_as_float(o[4 * e + 1])));
+                                    o[4 * e + 2] = __float_as_uint(fmaf(old[e].z, f.z, __uint_as_float(o[4 * e + 2])));
+                                    o[4 * e + 3] = __float_as_uint(fmaf(old[e].w, f.w, __uint_as_float(o[4 * e + 3])));
+                                }
                             }
-                            if (part && full_group) {
+                            tmem_wait_ld();
+                            if (part) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) ph2[e * kHD] = __uint_as_float(o[e]);
-                            } else if (part) {
+                                for (int e = 0; e < 8; ++e)
+                                    pq[e * 128] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                              __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                                continue;
+                            }
+                            const int64_t at = obase + hb * kHD + (dt0 + dd) * 128 + dl;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (hb + e < hmax) ph2[e * kHD] = __uint_as_float(o[e]);
-                            } else if (kTerms == 1) {
-                                __nv_bfloat16 *const od = static_cast<__nv_bfloat16 *>(A.out) + obase + hb * kHD + d;
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (hb + e < hmax)
-                                        od[e * kHD] = __float2bfloat16(__uint_as_float(o[e]) * S.fin[hb + e]);
-                            } else {
-                                float *const od = static_cast<float *>(A.out) + obase + hb * kHD + d;
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (hb + e < hmax) od[e * kHD] = __uint_as_float(o[e]) * S.fin[hb + e];
+                            for (int e = 0; e < 32; ++e) {
+                                if (hb + e >= hmax) continue;
+                                const float v = __uint_as_float(o[e]) * S.fin[hb + e];
+                                if (kTerms == 1) static_cast<__nv_bfloat16 *>(A.out)[at + e * kHD] = __float2bfloat16(v);
+                                else static_cast<float *>(A.out)[at + e * kHD] = v;
                             }
                         }
                     }
                     tc_fence_before();
                     mbar_arrive(&S.ofree);
-                    if (last && (r.flags & kRecPart) && !upper && hv && dt0 == 0) {
-                        float *ml = A.part_ml + (static_cast<int64_t>(r.slot) * H + h0 + hl) * 2;
-                        ml[0] = m_ref;
-                        ml[1] = l;
-                    }
+                    if (last && (r.flags & kRecPart) && !upper && dt0 == 0)
+                        A.part_ml[pslot * kHG + hl] = make_float2(m_ref, l);
                 }
             }
         }
         if (!more) break;
+        __syncthreads();                 // the list is done with
+        if (tid == 0) {
+            S.nrec = 0;
+            S.more = 0;
+        }
+        list_next();
     }
     tc_fence_before();
     __syncthreads();
@@ -873,86 +925,124 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the parts of a cut token, a CTA per (token, head, column part):
+// Joins the parts of a cut token:
 //   out = sum_s 2^(m_s - M) O_s / (sum_s 2^(m_s - M) l_s [+ 2^(sink - M)]).
-// Thread (sub, c4) adds four columns of parts sub, sub + nsub, ... in order;
-// the subs meet in shared memory in order.
-constexpr int kJoinThreads = 256;
-
-template <int kCw, bool kBf16>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArgs A) {
-    constexpr int kSub = kJoinThreads / kCw;
-    __shared__ float wgt[kMaxCtas];
-    __shared__ float inv_z;
-    __shared__ float4 red[kJoinThreads];
+// A CTA takes one 128-column tile of 4 kQuads heads; thread (sub, column)
+// adds parts sub, sub + kSub, ... of its column in order, four heads a load,
+// the first loads in flight while the first warps make the weights; the subs
+// meet in shared memory in order.
+template <int kSub, int kQuads, bool kBf16>
+__global__ void __launch_bounds__(128 * kSub) paged_join_kernel(const PagedArgs A) {
+    constexpr int kPer = 8 / kQuads > 0 ? 8 / kQuads : 1;      // parts a thread has in flight
+    constexpr int kHeads = 4 * kQuads, kWarps = 4 * kSub;
+    __shared__ float wgt[kHeads][kMaxCtas];
+    __shared__ float inv_z[kHeads];
+    __shared__ float4 red[kSub > 1 ? (kSub - 1) * kQuads * 128 : 1];
     pdl_wait();
     pdl_launch_dependents();
     const int2 meta = A.meta[blockIdx.x];
     const int ns = meta.y;
     if (ns <= 0 || ns > kMaxCtas) return;
-    const int split = meta.x >> 1;
-    // by token: entry x is token x; by CTA: the token is written behind the list
-    const int t = A.L.num_tokens <= static_cast<int>(gridDim.x) ? static_cast<int>(blockIdx.x)
-                                                                 : A.meta[gridDim.x + blockIdx.x].x;
-    const int h = blockIdx.y, tid = threadIdx.x, c4 = tid % kCw, sub = tid / kCw;
-    const int col = static_cast<int>(blockIdx.z) * 4 * kCw + 4 * c4;
-    auto slot = [&](int k) { return k == 0 ? meta.x : 2 * (split + k); };
-    if (tid < 32) {
+    const int first = meta.x >> 1;               // the split of the first part
+    const int tid = threadIdx.x, lane = tid & 31, col = tid & 127, sub = tid >> 7;
+    // blockIdx.y: (head group, tile, quads)
+    constexpr int kBlocks = 16 / kQuads;
+    const int qb = blockIdx.y % kBlocks, tile = blockIdx.y / kBlocks % 4, hg = blockIdx.y / (4 * kBlocks);
+    const int groups = static_cast<int>(gridDim.y) / (4 * kBlocks);
+    const int h0 = hg * kHG + qb * kHeads;       // first head of this CTA
+    if (h0 >= A.H) return;
+    auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? meta.x : 2 * (first + k)) * groups + hg; };
+    const int64_t at = static_cast<int64_t>(tile) * (16 * 128) + qb * kQuads * 128 + col;
+    float4 v[kPer][kQuads];
+    auto load = [&](int k0) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+#pragma unroll
+            for (int e = 0; e < kQuads; ++e)
+                if (k0 + k * kSub < ns) v[k][e] = __ldcg(A.part_o + slot(k0 + k * kSub) * (4 * 16 * 128) + at + e * 128);
+    };
+    load(sub);
+    for (int h = tid >> 5; h < kHeads; h += kWarps) {
+        constexpr int kMl = (kMaxCtas + 31) / 32;
+        float2 ml[kMl];
         float M = -INFINITY;
-        for (int k = tid; k < ns; k += 32)
-            M = fmaxf(M, A.part_ml[(static_cast<int64_t>(slot(k)) * A.H + h) * 2]);
+#pragma unroll
+        for (int k = 0; k < kMl; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (lane + 32 * k < ns) ml[k] = __ldcg(A.part_ml + slot(lane + 32 * k) * kHG + qb * kHeads + h);
+        }
+#pragma unroll
+        for (int k = 0; k < kMl; ++k) M = fmaxf(M, ml[k].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float sink = A.sinks ? A.sinks[h] * kLog2e : -INFINITY;
+        const float sink = A.sinks && h0 + h < A.H ? A.sinks[h0 + h] * kLog2e : -INFINITY;
         const float Mall = fmaxf(M, sink);
         float z = 0.f;
-        for (int k = tid; k < ns; k += 32) {
-            const float2 ml = *reinterpret_cast<const float2 *>(
-                A.part_ml + (static_cast<int64_t>(slot(k)) * A.H + h) * 2);
-            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - Mall);
-            wgt[k] = w;
-            z += w * ml.y;
+#pragma unroll
+        for (int k = 0; k < kMl; ++k) {
+            const float w = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - Mall);
+            if (lane + 32 * k < ns) wgt[h][lane + 32 * k] = w;
+            z += w * ml[k].y;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        if (tid == 0) {
+        if (lane == 0) {
             const bool some = M != -INFINITY;
-            if (A.sinks && some) z += exp2f(sink - Mall);
-            inv_z = some && z > 0.f ? 1.f / z : 0.f;
+            if (some && sink != -INFINITY) z += exp2f(sink - Mall);
+            inv_z[h] = some && z > 0.f ? 1.f / z : 0.f;
         }
     }
     __syncthreads();
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = sub; k < ns; k += kSub) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-            A.part_o + (static_cast<int64_t>(slot(k)) * A.H + h) * kHD + col));
-        const float w = wgt[k];
-        if (w != 0.f) {
-            acc.x = fmaf(w, v.x, acc.x);
-            acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z);
-            acc.w = fmaf(w, v.w, acc.w);
+    float4 acc[kQuads];
+#pragma unroll
+    for (int e = 0; e < kQuads; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = sub; k0 < ns; k0 += kPer * kSub) {
+        if (k0 != sub) load(k0);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int p = k0 + k * kSub;
+            if (p >= ns) break;
+#pragma unroll
+            for (int e = 0; e < kQuads; ++e) {
+                // (heads behind the last hold nothing and are not stored)
+                acc[e].x = fmaf(wgt[4 * e][p], v[k][e].x, acc[e].x);
+                acc[e].y = fmaf(wgt[4 * e + 1][p], v[k][e].y, acc[e].y);
+                acc[e].z = fmaf(wgt[4 * e + 2][p], v[k][e].z, acc[e].z);
+                acc[e].w = fmaf(wgt[4 * e + 3][p], v[k][e].w, acc[e].w);
+            }
         }
     }
-    red[tid] = acc;
-    __syncthreads();
-    if (sub == 0) {
-        for (int j = 1; j < kSub; ++j) {
-            const float4 v = red[j * kCw + c4];
-            acc.x += v.x;
-            acc.y += v.y;
-            acc.z += v.z;
-            acc.w += v.w;
+    if (kSub > 1) {
+        if (sub > 0)
+#pragma unroll
+            for (int e = 0; e < kQuads; ++e) red[((sub - 1) * kQuads + e) * 128 + col] = acc[e];
+        __syncthreads();
+        if (sub > 0) return;
+        for (int j = 1; j < kSub; ++j)
+#pragma unroll
+            for (int e = 0; e < kQuads; ++e) {
+                const float4 u = red[((j - 1) * kQuads + e) * 128 + col];
+                acc[e].x += u.x;
+                acc[e].y += u.y;
+                acc[e].z += u.z;
+                acc[e].w += u.w;
+            }
+    }
+    // by token: entry x is token x; by CTA: the token stands behind the list
+    const int t = A.L.num_tokens <= static_cast<int>(gridDim.x) ? static_cast<int>(blockIdx.x)
+                                                                 : A.meta[gridDim.x + blockIdx.x].x;
+#pragma unroll
+    for (int e = 0; e < kQuads; ++e) {
+        const float o[4] = {acc[e].x, acc[e].y, acc[e].z, acc[e].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int h = 4 * e + i;
+            if (h0 + h >= A.H) continue;
+            const int64_t to = (static_cast<int64_t>(t) * A.H + h0 + h) * kHD + tile * 128 + col;
+            const float x = o[i] * inv_z[h];
+            if (kBf16) static_cast<__nv_bfloat16 *>(A.out)[to] = __float2bfloat16(x);
+            else static_cast<float *>(A.out)[to] = x;
         }
-        const float f = inv_z;
-        const int64_t at = (static_cast<int64_t>(t) * A.H + h) * kHD + col;
-        if (kBf16)
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(A.out) + at) =
-                make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-        else
-            *reinterpret_cast<float4 *>(static_cast<float *>(A.out) + at) =
-                make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
     }
 }
 
@@ -962,12 +1052,13 @@ struct Ws {
     size_t meta, ml, o, total;
 };
 Ws ws_plan(const csa_params_t &p) {
-    const size_t slots = 2 * static_cast<size_t>(kMaxCtas / groups_of(p));
+    const int groups = groups_of(p);
+    const size_t slots = 2 * static_cast<size_t>(kMaxCtas / groups) * groups;
     Ws w{};
     w.meta = 0;
-    w.ml = 2 * kMaxCtas * sizeof(int2) / 256 * 256 + 256;
-    w.o = w.ml + (slots * p.n_heads * 8 + 255) / 256 * 256;
-    w.total = w.o + slots * p.n_heads * kHD * 4;
+    w.ml = (2 * kMaxCtas * sizeof(int2) + 255) / 256 * 256;
+    w.o = w.ml + slots * kHG * sizeof(float2);
+    w.total = w.o + slots * kHG * kHD * sizeof(float);
     return w;
 }
 
@@ -1019,8 +1110,8 @@ cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L
     A.sinks = sinks;
     A.out = out;
     A.meta = reinterpret_cast<int2 *>(wb + w.meta);
-    A.part_ml = reinterpret_cast<float *>(wb + w.ml);
-    A.part_o = reinterpret_cast<float *>(wb + w.o);
+    A.part_ml = reinterpret_cast<float2 *>(wb + w.ml);
+    A.part_o = reinterpret_cast<float4 *>(wb + w.o);
     A.status = status;
     const int ctas = (lc.sm_count < kMaxCtas ? lc.sm_count : kMaxCtas) / groups;
     auto kern = A.bf16_out ? paged_attention_kernel<1> : paged_attention_kernel<2>;
@@ -1033,10 +1124,14 @@ cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L
     const int64_t slots_max = (static_cast<int64_t>(L.max_pages) * L.page_rows + 7) / 8 * 8 + p.window;
     if (slots_max <= kCutAbove * kChunk) return cudaSuccess;
     const int entries = L.num_tokens < ctas ? L.num_tokens : ctas;
-    const bool wide = static_cast<int64_t>(entries) * H > 2 * lc.sm_count;
-    auto join = wide ? (A.bf16_out ? paged_join_kernel<128, true> : paged_join_kernel<128, false>)
-                     : (A.bf16_out ? paged_join_kernel<32, true> : paged_join_kernel<32, false>);
-    return launch_pdl(join, dim3(entries, H, wide ? 1 : 4), dim3(kJoinThreads), 0, lc.stream, A);
+    // few cut tokens in many parts: eight threads share a column's parts; many
+    // tokens in few parts: a thread takes 16 heads of its column
+    if (entries <= 8) {
+        auto join = A.bf16_out ? paged_join_kernel<8, 1, true> : paged_join_kernel<8, 1, false>;
+        return launch_pdl(join, dim3(entries, groups * 64), dim3(1024), 0, lc.stream, A);
+    }
+    auto join = A.bf16_out ? paged_join_kernel<2, 4, true> : paged_join_kernel<2, 4, false>;
+    return launch_pdl(join, dim3(entries, groups * 16), dim3(256), 0, lc.stream, A);
 }
 
 }  // namespace csa
