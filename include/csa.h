@@ -500,8 +500,12 @@ csa_status_t csa_paged_append(const csa_append_job_t *jobs /* (host) */, int32_t
  * A table entry outside the pool sets CSA_DEV_BAD_INDEX and its rows are
  * skipped; row_len above max_pages * page_rows sets CSA_DEV_CAPACITY and is
  * cut there; a negative one sets CSA_DEV_BAD_LENGTH (read as 0).
- * num_tokens <= 8192; num_pages * page_stride, max_pages * page_rows and
- * num_seqs * swa_cap below 2^31, else CSA_ERR_UNSUPPORTED.
+ * num_tokens <= 8192; num_pages * page_stride and num_seqs * swa_cap below
+ * 2^31, a token's rows (max_pages * page_rows + window) below 2^31 - 64 and
+ * num_tokens times them below 2^36, else CSA_ERR_UNSUPPORTED.
+ * As with csa_layout_t, the layout's arrays may be read as soon as the
+ * kernels start: a preceding kernel that allows programmatic dependent
+ * launch must not write them (csa_page_plan does not allow it).
  * Workspace: csa_paged_workspace_size bytes, 256-byte aligned; it needs no
  * zeroing, and calls that may run at the same time need separate ones (two
  * captured graphs too, unless one stream replays them). */

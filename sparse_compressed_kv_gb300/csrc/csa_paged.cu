@@ -232,7 +232,8 @@ csa_status_t check_paged(const csa_paged_layout_t *L, const csa_params_t *p) {
     if (L->num_seqs < 1 || L->num_tokens < 0 || L->page_rows < 1 || L->max_pages < 1)
         return CSA_ERR_INVALID_ARGUMENT;
     if (L->num_tokens > kPagedMaxTokens) return CSA_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(L->max_pages) * L->page_rows >= k2G) return CSA_ERR_UNSUPPORTED;
+    const int64_t rows = static_cast<int64_t>(L->max_pages) * L->page_rows + p->window;
+    if (rows >= k2G - 64 || rows * L->num_tokens >= int64_t(1) << 36) return CSA_ERR_UNSUPPORTED;
     return CSA_OK;
 }
 

@@ -102,9 +102,8 @@ struct Smem {
     alignas(16) float fin[kHG];
     alignas(16) float flush[kHG];
     int32_t nrec, more;
-    int64_t t0, s0;
-    int64_t wsum[kThreads / 32][2];
-    int32_t wmax[kThreads / 32];
+    int32_t t0, s0;
+    int2 wsum[kThreads / 32];    // cost, most chunks of a token
     Rec rec[kMaxRec];
 };
 
@@ -310,28 +309,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ta = min(T, tid * per), te = min(T, ta + per);
     Rec own{};
     int own_c = 0, own_bad = 0;
-    int64_t chunks = 0, cost = 0;
-    int maxc = 0;
+    int cost = 0, maxc = 0;
     for (int t = ta; t < te; ++t) {
         own = token_rec(A, t, tps, own_bad);
         own_c = rec_chunks(own);
-        chunks += own_c;
         cost += chunk_cost(own_c);
         maxc = max(maxc, own_c);
     }
-    int64_t incl = cost;
+    int incl = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
-        chunks += __shfl_xor_sync(0xffffffffu, chunks, o);
-        maxc = max(maxc, __shfl_xor_sync(0xffffffffu, maxc, o));
     }
-    if (lane == 31) {
-        S.wsum[warp][0] = incl;
-        S.wsum[warp][1] = chunks;
-        S.wmax[warp] = maxc;
-    }
+    maxc = __reduce_max_sync(0xffffffffu, maxc);
+    if (lane == 31) S.wsum[warp] = make_int2(incl, maxc);
     if (tid == 0) {
         S.t0 = T;
         S.nrec = 0;
@@ -340,35 +332,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem_holder;
-    int64_t base = 0, U = 0;
-    chunks = 0;
+    int base = 0, U = 0;                 // units in front of this warp, of all tokens
     maxc = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w == warp) base = U;
-        U += S.wsum[w][0];
-        chunks += S.wsum[w][1];
-        maxc = max(maxc, S.wmax[w]);
+        U += S.wsum[w].x;
+        maxc = max(maxc, S.wsum[w].y);
     }
     // Tokens are cut only where that shortens the longest CTA by more than
     // the partials and their join cost: otherwise CTA c takes token c (T <= G),
     // or the tokens that begin in its range.
-    const bool direct = T <= G && maxc <= div_pos(chunks, G) + kCutAbove;
+    const bool direct = T <= G && maxc <= U / G + kCutAbove;
     const bool snap = direct || (T > G && maxc <= kCutAbove);
     // few CTAs at work: 2 or 4 of them share a range, each with all of its
     // logits and weights and its share of the 512 columns
     int dlog = 0;
     if (direct) dlog = T * 4 <= G ? 2 : T * 2 <= G ? 1 : 0;
-    else if (!snap && T <= G) dlog = chunks * 4 <= G ? 2 : chunks <= G ? 1 : 0;
+    else if (!snap && T <= G) dlog = U <= G / 4 ? 2 : U <= G ? 1 : 0;
     const int dparts = 1 << dlog;
-    const int nsplit = static_cast<int>(min(static_cast<int64_t>(G >> dlog), U));
+    const int nsplit = min(G >> dlog, U);
     const int split = static_cast<int>(blockIdx.x) >> dlog;
     const int ndt = 4 >> dlog;                                    // 128-column tiles of this CTA
     const int dt0 = (static_cast<int>(blockIdx.x) & (dparts - 1)) * ndt;
-    int64_t ua = 0, ub = split < T ? 1 : 0;
+    // range k begins at unit floor(k U / nsplit)
+    const int uq = U / nsplit, ur = U - uq * nsplit;
+    auto begin = [&](int k) { return k * uq + k * ur / nsplit; };
+    int ua = 0, ub = split < T ? 1 : 0;
     if (!direct) {
-        ua = split < nsplit ? div_pos(split * U, nsplit) : U;
-        ub = split < nsplit ? div_pos((split + 1) * U, nsplit) : U;
+        ua = split < nsplit ? begin(split) : U;
+        ub = split < nsplit ? begin(split + 1) : U;
     }
     const bool by_token = T <= G;
     const bool lead = hg == 0 && dt0 == 0;       // reports errors, writes the join's list
@@ -377,14 +370,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (direct) {
         if (tid == 0) S.t0 = split;
     } else {
-        int64_t s = base + incl - cost;
+        int s = base + incl - cost;
         for (int t = ta; t < te; ++t) {
             int bad;
             const int c = per == 1 ? own_c : rec_chunks(token_rec(A, t, tps, bad));
-            const int64_t e = s + chunk_cost(c);
+            const int e = s + chunk_cost(c);
             if (snap ? s >= ua : (s <= ua && ua < e)) {
                 if (snap) {
-                    atomicMin(reinterpret_cast<unsigned long long *>(&S.t0), static_cast<unsigned long long>(t));
+                    atomicMin(&S.t0, t);
                 } else {
                     S.t0 = t;
                     S.s0 = s;
@@ -396,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     if (per > 1 && snap && !direct) {
-        int64_t s = base + incl - cost;
+        int s = base + incl - cost;
         for (int t = ta; t < te; ++t) {
             if (t == S.t0) S.s0 = s;
             int bad;
@@ -404,11 +397,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncthreads();
     }
-    int64_t t0 = S.t0, s0 = S.s0;
+    int t0 = S.t0, s0 = S.s0;
 
     // Lists the segment of one token (whose units begin at s) as entry `at`.
     // Returns the token's entry for the join; `owner`: its first chunk is here.
-    auto list = [&](Rec &r, int c, int64_t s, int at, bool &owner) {
+    auto list = [&](Rec &r, int c, int s, int at, bool &owner) {
         int2 m = make_int2(-1, 0);
         owner = true;
         r.c0 = 0;
@@ -416,19 +409,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         r.slot = 2 * split + 1;
         if (!snap) {
             owner = s >= ua;
-            r.c0 = static_cast<int32_t>(min(max(ua - s, int64_t(0)), int64_t(c)));
-            r.c1 = static_cast<int32_t>(min(ub - s, int64_t(c)));
+            r.c0 = min(max(ua - s, 0), c);
+            r.c1 = min(ub - s, c);
             if (!owner) r.slot = 2 * split;
             // the split that holds the token's last chunk
             if (owner && c > 0) {
-                const int64_t last = div_pos((s + c) * nsplit - 1, U);
-                if (last > split) m = make_int2(r.slot, static_cast<int>(last) - split + 1);
+                const int u = s + c - 1;
+                int last = min(u / uq, nsplit - 1);      // at or behind it: ranges have uq or uq + 1 units
+                while (begin(last) > u) --last;
+                if (last > split) m = make_int2(r.slot, last - split + 1);
             }
             if (r.c1 - r.c0 < c) r.flags |= kRecPart;
         }
         if (r.b >= 0 && c == 0 && owner) r.flags |= kRecZero;
         S.rec[at] = r;
         atomicAdd(&S.nrec, 1);
+        // its first table entry on its way while the roles start
+        if (r.c0 * kChunk < r.n)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(A.L.table + static_cast<int64_t>(r.b) * A.L.max_pages +
+                                                          r.c0 * kChunk / A.L.page_rows));
         if (at == kMaxRec - 1 && !direct) {
             S.more = 1;
             S.s0 = s + chunk_cost(c);
@@ -447,25 +446,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     // thread i lists token t0 + i
     auto list_next = [&]() {
         Rec r{};
-        int bad = 0, c = 0;
-        int64_t w = 0;
+        int bad = 0, c = 0, w = 0;
         const bool in = tid < kMaxRec && t0 + tid < T && ub > ua;
         if (in) {
-            r = token_rec(A, static_cast<int>(t0) + tid, tps, bad);
+            r = token_rec(A, t0 + tid, tps, bad);
             c = rec_chunks(r);
             w = chunk_cost(c);
         }
-        int64_t run = w;
+        int run = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, run, o);
+            const int v = __shfl_up_sync(0xffffffffu, run, o);
             if (lane >= o) run += v;
         }
-        if (lane == 31) S.wsum[warp][0] = run;
+        if (lane == 31) S.wsum[warp].x = run;
         __syncthreads();
-        int64_t s = s0 + run - w;
+        int s = s0 + run - w;
         for (int k = 0; k < kMaxRec / 32; ++k)
-            if (k < warp) s += S.wsum[k][0];
+            if (k < warp) s += S.wsum[k].x;
         if (in && s < ub) {
             bool owner;
             const int2 m = list(r, c, s, tid, owner);
@@ -474,8 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (per == 1) {
         // the first list, from the registers
-        const int at = tid - static_cast<int>(t0);
-        const int64_t s = base + incl - cost;
+        const int at = tid - t0;
+        const int s = base + incl - cost;
         bool owner = false;
         int2 m = make_int2(-1, 0);
         if (at >= 0 && at < kMaxRec && tid < T && ub > ua && (direct ? at == 0 : s < ub))
@@ -933,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // meet in shared memory in order.
 template <int kSub, int kQuads, bool kBf16>
 __global__ void __launch_bounds__(128 * kSub) paged_join_kernel(const PagedArgs A) {
-    constexpr int kPer = 8 / kQuads > 0 ? 8 / kQuads : 1;      // parts a thread has in flight
+    constexpr int kPer = kSub > 1 ? 8 / kQuads : 3;            // parts a thread has in flight
     constexpr int kHeads = 4 * kQuads, kWarps = 4 * kSub;
     __shared__ float wgt[kHeads][kMaxCtas];
     __shared__ float inv_z[kHeads];
@@ -1130,8 +1128,8 @@ cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L
         auto join = A.bf16_out ? paged_join_kernel<8, 1, true> : paged_join_kernel<8, 1, false>;
         return launch_pdl(join, dim3(entries, groups * 64), dim3(1024), 0, lc.stream, A);
     }
-    auto join = A.bf16_out ? paged_join_kernel<2, 4, true> : paged_join_kernel<2, 4, false>;
-    return launch_pdl(join, dim3(entries, groups * 16), dim3(256), 0, lc.stream, A);
+    auto join = A.bf16_out ? paged_join_kernel<1, 2, true> : paged_join_kernel<1, 2, false>;
+    return launch_pdl(join, dim3(entries, groups * 32), dim3(128), 0, lc.stream, A);
 }
 
 }  // namespace csa
