@@ -56,10 +56,6 @@ constexpr int kMaxRec = 128;                    // segments a CTA lists at a tim
 constexpr int kMaxCtas = 152;                   // CTAs of the grid at most (sizes the workspace)
 constexpr int kSegCost = 2;                     // a segment's epilogue, in chunks
 constexpr int kCutAbove = 4;                    // chunks a token may exceed the mean before tokens are cut
-#ifndef AHEAD
-#define AHEAD 2
-#endif
-constexpr int kAhead = AHEAD;
 constexpr int kFlushF32 = 32, kFlushBf16 = 512; // chunks between roundings of the accumulator
 
 struct PagedArgs {
@@ -593,8 +589,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 0 || warp >= 6) {
             // -------------------------------------------- row fetch
-            const int li = warp == 0 ? 0 : warp - 5;   // rows 16 li .. of each chunk
+            // The warp walks the list's chunks, 16 rows of each.  Lane l (and
+            // l + 16) looks after row l; three chunks ahead its page number is
+            // on its way from the table, two ahead it is a row of the pool
+            // whose bytes are on their way into L2, then it is copied.
+            const int li = warp == 0 ? 0 : warp - 5;
+            const int rl = lane & 15;
             int bad = 0;
+            struct Cursor {
+                int i, c;
+            };
+            auto settle = [&](Cursor &k) {             // to the next segment that has chunks
+                while (k.i < nrec && k.c >= S.rec[k.i].c1) {
+                    ++k.i;
+                    if (k.i < nrec) k.c = S.rec[k.i].c0;
+                }
+            };
+            auto advance = [&](Cursor &k) {
+                ++k.c;
+                settle(k);
+            };
+            struct Entry {
+                int32_t page, in_page;                 // in_page < 0: not a row of the pool
+                bool box;                              // 8 rows of one page from here on
+            };
+            auto look_up = [&](const Cursor &k) {
+                Entry e{-1, -1, false};
+                if (k.i >= nrec) return e;
+                const int n = S.rec[k.i].n, j = k.c * kChunk + 16 * li + rl;
+                if (j < n) {
+                    const int pg = j / A.L.page_rows;
+                    e.in_page = j - pg * A.L.page_rows;
+                    e.page = A.L.table[static_cast<int64_t>(S.rec[k.i].b) * A.L.max_pages + pg];
+                    e.box = j + 8 <= n && e.in_page + 8 <= A.L.page_rows;
+                }
+                return e;
+            };
+            struct Place {
+                int32_t row;                           // row of the pool, or -1
+                uint32_t box;                          // bit g: group g of 8 rows is one box
+            };
+            auto place = [&](const Entry &e, bool ahead) {
+                Place p{-1, 0};
+                if (e.in_page >= 0) {
+                    if (e.page < 0 || e.page >= A.num_pages) bad |= CSA_DEV_BAD_INDEX;
+                    else p.row = static_cast<int32_t>(e.page * A.page_stride) + e.in_page;
+                }
+                const uint32_t bx = __ballot_sync(0xffffffffu, e.box);
+                p.box = (bx & 1u) | (bx >> 7 & 2u);
+                if (ahead && lane < 16 && p.row >= 0) {
+                    if (!(p.box >> (lane >> 3) & 1u))
+                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                         A.cache + static_cast<int64_t>(p.row) * kHD),
+                                     "r"(kHD * 2)
+                                     : "memory");
+                    else if ((lane & 7) == 0)
+                        tma_prefetch_l2_3d(&tm_rows, 0, p.row, 0);
+                }
+                return p;
+            };
             int pending = -1;                          // stage whose cp.async rows are in flight
             auto land = [&](bool newer) {              // ... have landed: hand the stage over
                 if (newer) cp_async_wait<1>();
@@ -605,94 +658,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pending = -1;
             };
             const uint64_t pol = policy_evict_normal();
-            for (int i = 0; i < nrec; ++i) {
-                const Rec r = S.rec[i];
-                const int wslot = rec_window_slot(r);
-                for (int c = r.c0; c < r.c1; ++c) {
-                    // lane l resolves row l of the warp's 16: a row of the pool, or of
-                    // the ring, or none
-                    const int j = c * kChunk + 16 * li + (lane & 15);
-                    int32_t row = -1;                  // row of the pool
-                    int32_t in_page = 0;
-                    const __nv_bfloat16 *src = nullptr;
-                    if (j < r.n) {
-                        const int pg = j / A.L.page_rows;
-                        in_page = j - pg * A.L.page_rows;
-                        const int32_t page = A.L.table[static_cast<int64_t>(r.b) * A.L.max_pages + pg];
-                        if (page < 0 || page >= A.num_pages) {
-                            bad |= CSA_DEV_BAD_INDEX;
-                        } else {
-                            row = static_cast<int32_t>(page * A.page_stride) + in_page;
-                            src = A.cache + static_cast<int64_t>(row) * kHD;
-                        }
-                    } else if (r.near > 0 && j >= wslot && j - wslot < r.near) {
-                        const int64_t x = r.first + (j - wslot);
-                        if (x < r.first_res) bad |= CSA_DEV_MISSING_SWA;
-                        else
-                            src = static_cast<const __nv_bfloat16 *>(A.L.swa_kv) +
-                                  (static_cast<int64_t>(r.b) * A.L.swa_cap + mod_pos(x, A.L.swa_cap)) * kHD;
+            Cursor cur{0, S.rec[0].c0};
+            settle(cur);
+            Cursor far = cur;
+            const Entry e0 = look_up(far);
+            advance(far);
+            const Entry e1 = look_up(far);
+            advance(far);
+            Entry ahead = look_up(far);
+            Place now = place(e0, false), next = place(e1, false);
+            while (cur.i < nrec) {
+                const Rec &r = S.rec[cur.i];
+                const int j0 = cur.c * kChunk + 16 * li, wslot = rec_window_slot(r);
+                const __nv_bfloat16 *src = nullptr;
+                if (now.row >= 0) {
+                    src = A.cache + static_cast<int64_t>(now.row) * kHD;
+                } else if (r.near > 0 && j0 + rl >= wslot && j0 + rl - wslot < r.near) {
+                    const int64_t x = r.first + (j0 + rl - wslot);
+                    if (x < r.first_res) bad |= CSA_DEV_MISSING_SWA;
+                    else
+                        src = static_cast<const __nv_bfloat16 *>(A.L.swa_kv) +
+                              (static_cast<int64_t>(r.b) * A.L.swa_cap + mod_pos(x, A.L.swa_cap)) * kHD;
+                }
+                const uint32_t okm = __ballot_sync(0xffffffffu, src != nullptr) & 0xFFFFu;
+                const int32_t y1 = __shfl_sync(0xffffffffu, now.row, 8);
+                const int st = n_fetch % kStages;
+                const uint32_t ph = ((n_fetch / kStages) & 1u) ^ 1u;
+                if (pending >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(&S.empty[st][li], ph))) land(false);
+                mbar_wait(&S.empty[st][li], ph, A.status);
+                __syncwarp();
+                uint8_t *rows = sRows + st * kStageBytes + 2 * li * kGroupBytes;
+                if (lane == 0) {
+                    S.maskw[st][li] = okm;
+                    if (now.box) {
+                        // (a bad page: a box behind the pool reads as zeros)
+                        mbar_expect_tx(&S.full[st], (now.box == 3u ? 2 : 1) * kGroupBytes);
+                        if (now.box & 1u)
+                            tma_load_3d(rows, &tm_rows, 0, now.row >= 0 ? now.row : A.total_rows, 0, &S.full[st], pol);
+                        if (now.box & 2u)
+                            tma_load_3d(rows + kGroupBytes, &tm_rows, 0, y1 >= 0 ? y1 : A.total_rows, 0, &S.full[st], pol);
                     }
-                    const uint32_t okm = __ballot_sync(0xffffffffu, src != nullptr) & 0xFFFFu;
-                    // a group of 8 rows of one page is one box
-                    bool box[2];
-                    int32_t y[2];
-#pragma unroll
+                }
+                const bool by_row = now.box != 3u;
+                if (by_row) {
+#pragma unroll 1
                     for (int g = 0; g < 2; ++g) {
-                        const int j0 = c * kChunk + 16 * li + 8 * g;
-                        const int32_t off0 = __shfl_sync(0xffffffffu, in_page, 8 * g);
-                        y[g] = __shfl_sync(0xffffffffu, row, 8 * g);
-                        box[g] = j0 + 8 <= r.n && off0 + 8 <= A.L.page_rows;
-                        if (y[g] < 0) y[g] = A.total_rows;      // behind the pool: zeros
-                    }
-                    const int st = n_fetch % kStages;
-                    const uint32_t ph = ((n_fetch / kStages) & 1u) ^ 1u;
-                    if (pending >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(&S.empty[st][li], ph))) land(false);
-                    mbar_wait(&S.empty[st][li], ph, A.status);
-                    __syncwarp();
-                    uint8_t *rows = sRows + st * kStageBytes + 2 * li * kGroupBytes;
-                    if (lane == 0) {
-                        S.maskw[st][li] = okm;
-                        if (box[0] || box[1]) {
-                            mbar_expect_tx(&S.full[st], (box[0] && box[1] ? 2 : 1) * kGroupBytes);
+                        if (now.box >> g & 1u) continue;
 #pragma unroll
-                            for (int g = 0; g < 2; ++g)
-                                if (box[g]) tma_load_3d(rows + g * kGroupBytes, &tm_rows, 0, y[g], 0, &S.full[st], pol);
-                        }
-                    }
-                    const bool by_row = !(box[0] && box[1]);
-                    if (by_row) {
+                        for (int rr = 0; rr < 8; ++rr) {
+                            const __nv_bfloat16 *p = reinterpret_cast<const __nv_bfloat16 *>(__shfl_sync(
+                                0xffffffffu, reinterpret_cast<unsigned long long>(src), 8 * g + rr));
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            if (box[g]) continue;
-#pragma unroll 2
-                            for (int rr = 0; rr < 8; ++rr) {
-                                const __nv_bfloat16 *p = reinterpret_cast<const __nv_bfloat16 *>(__shfl_sync(
-                                    0xffffffffu, reinterpret_cast<unsigned long long>(src), 8 * g + rr));
-#pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const int k = lane + 32 * u;   // 16-byte piece of the row
-                                    cp_async16(rows + g * kGroupBytes + (k >> 3) * 1024 + rr * 128 + (((k & 7) ^ rr) << 4),
-                                               p ? static_cast<const void *>(p + k * 8) : A.cache, p != nullptr);
-                                }
+                            for (int u = 0; u < 2; ++u) {
+                                const int k = lane + 32 * u;   // 16-byte piece of the row
+                                cp_async16(rows + g * kGroupBytes + (k >> 3) * 1024 + rr * 128 + (((k & 7) ^ rr) << 4),
+                                           p ? static_cast<const void *>(p + k * 8) : A.cache, p != nullptr);
                             }
                         }
-                        cp_async_commit();
                     }
-                    // the boxes of a later chunk on their way into L2 (lanes 0 and 1)
-                    if (lane < 2 && c + kAhead < r.c1) {
-                        const int j0 = (c + kAhead) * kChunk + 16 * li + 8 * lane;
-                        const int pg = j0 / A.L.page_rows, off0 = j0 - pg * A.L.page_rows;
-                        if (j0 + 8 <= r.n && off0 + 8 <= A.L.page_rows) {
-                            const int32_t page = A.L.table[static_cast<int64_t>(r.b) * A.L.max_pages + pg];
-                            if (page >= 0 && page < A.num_pages)
-                                tma_prefetch_l2_3d(&tm_rows, 0, static_cast<int32_t>(page * A.page_stride) + off0, 0);
-                        }
-                    }
-                    if (pending >= 0) land(by_row);
-                    if (by_row) pending = st;
-                    else if (lane == 0) mbar_arrive(&S.full[st]);
-                    ++n_fetch;
+                    cp_async_commit();
                 }
+                // the queue moves up
+                now = next;
+                next = place(ahead, true);
+                advance(far);
+                ahead = look_up(far);
+                advance(cur);
+                if (pending >= 0) land(by_row);
+                if (by_row) pending = st;
+                else if (lane == 0) mbar_arrive(&S.full[st]);
+                ++n_fetch;
             }
             if (pending >= 0) land(false);
             bad = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bad)));
