@@ -25,7 +25,7 @@
 // A segment that is a whole token writes the output; the parts of a token cut
 // between CTAs go to the workspace as (O, m, l) and a second kernel joins
 // them.  The accumulator of tcgen05 drops bits below its last place, so
-// sums of thousands of rows drift; every kFlush chunks O^T is added, rounded,
+// sums of thousands of rows drift; at least every kFlush chunks O^T is added, rounded,
 // into the CTA's own f32 partial and starts again from zero.
 #include <math.h>
 
@@ -56,7 +56,7 @@ constexpr int kMaxRec = 128;                    // segments a CTA lists at a tim
 constexpr int kMaxCtas = 152;                   // CTAs of the grid at most (sizes the workspace)
 constexpr int kSegCost = 2;                     // a segment's epilogue, in chunks
 constexpr int kCutAbove = 4;                    // chunks a token may exceed the mean before tokens are cut
-constexpr int kFlushF32 = 32, kFlushBf16 = 512; // chunks between roundings of the accumulator
+constexpr int kFlushF32 = 40, kFlushBf16 = 512; // chunks between roundings of the accumulator, at most
 
 struct PagedArgs {
     csa_paged_layout_t L;
@@ -253,6 +253,14 @@ __device__ __forceinline__ int rec_chunks(const Rec &r) {
     return r.b < 0 ? 0 : (rec_slots(r) + kChunk - 1) / kChunk;
 }
 __device__ __forceinline__ int chunk_cost(int chunks) { return chunks > 0 ? chunks + kSegCost : 1; }
+
+// Chunks after which a segment of nch chunks rounds its accumulator into the
+// partial: equal stretches of at most kMost.
+template <int kMost>
+__device__ __forceinline__ int flush_every(int nch) {
+    const int n = (nch + kMost - 1) / kMost;
+    return n > 1 ? (nch + n - 1) / n : nch;
+}
 
 // kTerms: bf16 terms of P (2 for an f32 output, 1 for bf16).
 template <int kTerms>
@@ -567,10 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_commit(&S.pfree);
             };
             for (int i = 0; i < nrec; ++i) {
-                const int nch = S.rec[i].c1 - S.rec[i].c0;
-                for (int k = 0; k < nch; ++k, ++np) {
+                const int nch = S.rec[i].c1 - S.rec[i].c0, every = flush_every<kFlush>(nch);
+                for (int k = 0, z = 0; k < nch; ++k, ++np, z = z + 1 == every ? 0 : z + 1) {
                     const int st = np % kStages;
-                    const bool zero = k % kFlush == 0;
+                    const bool zero = z == 0;
                     mbar_wait(&S.pfull, np & 1u, A.status);
                     if (zero) {
                         if (n_of > 0) mbar_wait(&S.ofree, (n_of - 1) & 1u, A.status);
@@ -756,7 +764,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float m_ref = -INFINITY, l = 0.f, m_flush = -INFINITY;
                 const int64_t pslot = static_cast<int64_t>(r.slot) * gridDim.y + hg;
-                for (int k = 0; k < nch; ++k, ++n_sm) {
+                const int every = flush_every<kFlush>(nch);
+                for (int k = 0, z = 0; k < nch; ++k, ++n_sm, z = z + 1 == every ? 0 : z + 1) {
                     const int st = n_sm % kStages, sb = n_sm & 1u;
                     mbar_wait(&S.sfull[sb], (n_sm >> 1) & 1u, A.status);
                     tc_fence_after();
@@ -809,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     named_bar_sync(kBarSm, kSmThreads);
                     const bool any = (S.flag[sb][0] | S.flag[sb][1] | S.flag[sb][2] | S.flag[sb][3]) != 0;
-                    if (any && k % kFlush != 0) {
+                    if (any && z != 0) {
                         if (!upper) S.alpha[hl] = alpha;
                         mbar_wait(&S.pfree, (n_sm - 1) & 1u, A.status);   // the product before this one
                         named_bar_sync(kBarSm, kSmThreads);
@@ -871,9 +880,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&S.pfull);
 
                     const bool last = k + 1 == nch;
-                    if (!last && (k + 1) % kFlush != 0) continue;
+                    if (!last && z + 1 != every) continue;
                     // ---- O^T into the partial, or the output
-                    const bool add = k >= kFlush;        // the partial already holds earlier chunks
+                    const bool add = k >= every;        // the partial already holds earlier chunks
                     const bool part = (r.flags & kRecPart) || !last;
                     if (!upper) {
                         S.flush[hl] = m_flush == -INFINITY ? 1.f : exp2f(m_flush - m_ref);
@@ -960,61 +969,80 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of a cut token:
 //   out = sum_s 2^(m_s - M) O_s / (sum_s 2^(m_s - M) l_s [+ 2^(sink - M)]).
-// A CTA takes one 128-column tile of 4 kQuads heads; thread (sub, column)
-// adds parts sub, sub + kSub, ... of its column in order, four heads a load,
-// the first loads in flight while the first warps make the weights; the subs
-// meet in shared memory in order.
-template <int kSub, int kQuads, bool kBf16>
-__global__ void __launch_bounds__(128 * kSub) paged_join_kernel(const PagedArgs A) {
-    constexpr int kPer = kSub > 1 ? 8 / kQuads : 3;            // parts a thread has in flight
-    constexpr int kHeads = 4 * kQuads, kWarps = 4 * kSub;
-    __shared__ float wgt[kHeads][kMaxCtas];
-    __shared__ float inv_z[kHeads];
-    __shared__ float4 red[kSub > 1 ? (kSub - 1) * kQuads * 128 : 1];
+// Two shapes: a few tokens cut into up to 152 parts (one long context), and
+// many tokens in a few parts each.
+struct JoinEntry {
+    int t, ns, slot0, split0;
+    __device__ int64_t slot(int k) const { return k == 0 ? slot0 : 2 * (split0 + k); }
+};
+
+__device__ __forceinline__ JoinEntry join_entry(const PagedArgs &A) {
+    const int2 meta = A.meta[blockIdx.x];
+    JoinEntry e;
+    e.ns = meta.y > kMaxCtas ? 0 : meta.y;
+    e.slot0 = meta.x;
+    e.split0 = meta.x >> 1;
+    // by token: entry x is token x; by CTA: the token stands behind the list
+    e.t = blockIdx.x;
+    if (A.L.num_tokens > static_cast<int>(gridDim.x)) e.t = A.meta[gridDim.x + blockIdx.x].x;
+    return e;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void join_store(const PagedArgs &A, int64_t at, float x) {
+    if (kBf16) static_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16(x);
+    else static_cast<float *>(A.out)[at] = x;
+}
+
+// Many parts: a CTA takes four heads of one 128-column tile; eight (one token)
+// or four threads share a column's parts, eight loads of four heads each in
+// flight (issued before the weights are known), and meet in shared memory in
+// order.
+constexpr int kDeepPer = 8;
+
+template <int kDeepSub, bool kBf16>
+__global__ void __launch_bounds__(128 * kDeepSub) join_deep_kernel(const PagedArgs A) {
+    __shared__ float wgt[4][kMaxCtas];
+    __shared__ float inv_z[4];
+    __shared__ float4 red[(kDeepSub - 1) * 128];
     pdl_wait();
     pdl_launch_dependents();
-    const int2 meta = A.meta[blockIdx.x];
-    const int ns = meta.y;
-    if (ns <= 0 || ns > kMaxCtas) return;
-    const int first = meta.x >> 1;               // the split of the first part
-    const int tid = threadIdx.x, lane = tid & 31, col = tid & 127, sub = tid >> 7;
-    // blockIdx.y: (head group, tile, quads)
-    constexpr int kBlocks = 16 / kQuads;
-    const int qb = blockIdx.y % kBlocks, tile = blockIdx.y / kBlocks % 4, hg = blockIdx.y / (4 * kBlocks);
-    const int groups = static_cast<int>(gridDim.y) / (4 * kBlocks);
-    const int h0 = hg * kHG + qb * kHeads;       // first head of this CTA
+    const JoinEntry J = join_entry(A);
+    const int ns = J.ns;
+    if (ns <= 0) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = tid & 127, sub = tid >> 7;
+    const int quad = blockIdx.y & 15, tile = blockIdx.y >> 4 & 3, hg = blockIdx.y >> 6;
+    const int groups = static_cast<int>(gridDim.y) >> 6, h0 = hg * kHG + 4 * quad;
     if (h0 >= A.H) return;
-    auto slot = [&](int k) { return static_cast<int64_t>(k == 0 ? meta.x : 2 * (first + k)) * groups + hg; };
-    const int64_t at = static_cast<int64_t>(tile) * (16 * 128) + qb * kQuads * 128 + col;
-    float4 v[kPer][kQuads];
+    const float4 *const po = A.part_o + tile * (16 * 128) + quad * 128 + col;
+    float4 v[kDeepPer];
     auto load = [&](int k0) {
 #pragma unroll
-        for (int k = 0; k < kPer; ++k)
-#pragma unroll
-            for (int e = 0; e < kQuads; ++e)
-                if (k0 + k * kSub < ns) v[k][e] = __ldcg(A.part_o + slot(k0 + k * kSub) * (4 * 16 * 128) + at + e * 128);
+        for (int k = 0; k < kDeepPer; ++k)
+            if (k0 + k * kDeepSub < ns) v[k] = __ldcg(po + (J.slot(k0 + k * kDeepSub) * groups + hg) * (4 * 16 * 128));
     };
     load(sub);
-    for (int h = tid >> 5; h < kHeads; h += kWarps) {
+    if (warp < 4) {                              // the weights of head `warp`
         constexpr int kMl = (kMaxCtas + 31) / 32;
         float2 ml[kMl];
         float M = -INFINITY;
 #pragma unroll
         for (int k = 0; k < kMl; ++k) {
             ml[k] = make_float2(-INFINITY, 0.f);
-            if (lane + 32 * k < ns) ml[k] = __ldcg(A.part_ml + slot(lane + 32 * k) * kHG + qb * kHeads + h);
+            if (lane + 32 * k < ns)
+                ml[k] = __ldcg(A.part_ml + (J.slot(lane + 32 * k) * groups + hg) * kHG + 4 * quad + warp);
         }
 #pragma unroll
         for (int k = 0; k < kMl; ++k) M = fmaxf(M, ml[k].x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float sink = A.sinks && h0 + h < A.H ? A.sinks[h0 + h] * kLog2e : -INFINITY;
+        const float sink = A.sinks && h0 + warp < A.H ? A.sinks[h0 + warp] * kLog2e : -INFINITY;
         const float Mall = fmaxf(M, sink);
         float z = 0.f;
 #pragma unroll
         for (int k = 0; k < kMl; ++k) {
             const float w = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - Mall);
-            if (lane + 32 * k < ns) wgt[h][lane + 32 * k] = w;
+            if (lane + 32 * k < ns) wgt[warp][lane + 32 * k] = w;
             z += w * ml[k].y;
         }
 #pragma unroll
@@ -1022,59 +1050,111 @@ __global__ void __launch_bounds__(128 * kSub) paged_join_kernel(const PagedArgs 
         if (lane == 0) {
             const bool some = M != -INFINITY;
             if (some && sink != -INFINITY) z += exp2f(sink - Mall);
-            inv_z[h] = some && z > 0.f ? 1.f / z : 0.f;
+            inv_z[warp] = some && z > 0.f ? 1.f / z : 0.f;
         }
     }
     __syncthreads();
-    float4 acc[kQuads];
-#pragma unroll
-    for (int e = 0; e < kQuads; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = sub; k0 < ns; k0 += kPer * kSub) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = sub; k0 < ns; k0 += kDeepPer * kDeepSub) {
         if (k0 != sub) load(k0);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int p = k0 + k * kSub;
+        for (int k = 0; k < kDeepPer; ++k) {
+            const int p = k0 + k * kDeepSub;
             if (p >= ns) break;
-#pragma unroll
-            for (int e = 0; e < kQuads; ++e) {
-                // (heads behind the last hold nothing and are not stored)
-                acc[e].x = fmaf(wgt[4 * e][p], v[k][e].x, acc[e].x);
-                acc[e].y = fmaf(wgt[4 * e + 1][p], v[k][e].y, acc[e].y);
-                acc[e].z = fmaf(wgt[4 * e + 2][p], v[k][e].z, acc[e].z);
-                acc[e].w = fmaf(wgt[4 * e + 3][p], v[k][e].w, acc[e].w);
-            }
+            // (heads behind the last hold anything and are not stored)
+            acc.x = fmaf(wgt[0][p], v[k].x, acc.x);
+            acc.y = fmaf(wgt[1][p], v[k].y, acc.y);
+            acc.z = fmaf(wgt[2][p], v[k].z, acc.z);
+            acc.w = fmaf(wgt[3][p], v[k].w, acc.w);
         }
     }
-    if (kSub > 1) {
-        if (sub > 0)
-#pragma unroll
-            for (int e = 0; e < kQuads; ++e) red[((sub - 1) * kQuads + e) * 128 + col] = acc[e];
-        __syncthreads();
-        if (sub > 0) return;
-        for (int j = 1; j < kSub; ++j)
-#pragma unroll
-            for (int e = 0; e < kQuads; ++e) {
-                const float4 u = red[((j - 1) * kQuads + e) * 128 + col];
-                acc[e].x += u.x;
-                acc[e].y += u.y;
-                acc[e].z += u.z;
-                acc[e].w += u.w;
-            }
+    if (sub > 0) red[(sub - 1) * 128 + col] = acc;
+    __syncthreads();
+    if (sub > 0) return;
+    for (int j = 0; j + 1 < kDeepSub; ++j) {
+        const float4 u = red[j * 128 + col];
+        acc.x += u.x;
+        acc.y += u.y;
+        acc.z += u.z;
+        acc.w += u.w;
     }
-    // by token: entry x is token x; by CTA: the token stands behind the list
-    const int t = A.L.num_tokens <= static_cast<int>(gridDim.x) ? static_cast<int>(blockIdx.x)
-                                                                 : A.meta[gridDim.x + blockIdx.x].x;
+    const float o[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
-    for (int e = 0; e < kQuads; ++e) {
-        const float o[4] = {acc[e].x, acc[e].y, acc[e].z, acc[e].w};
+    for (int i = 0; i < 4; ++i)
+        if (h0 + i < A.H)
+            join_store<kBf16>(A, (static_cast<int64_t>(J.t) * A.H + h0 + i) * kHD + tile * 128 + col, o[i] * inv_z[i]);
+}
+
+// Few parts: a CTA takes 32 or 16 heads of a tile (gridDim.z of them share the
+// tile); a thread walks its half of the quads of its column, all parts of
+// two quads in flight.
+constexpr int kWidePer = 3;                      // parts in flight
+
+template <bool kBf16>
+__global__ void __launch_bounds__(256) join_wide_kernel(const PagedArgs A) {
+    __shared__ float4 wgt[kMaxCtas][kHG / 4];    // scaled by 1 / z
+    pdl_wait();
+    pdl_launch_dependents();
+    const JoinEntry J = join_entry(A);
+    const int ns = J.ns;
+    if (ns <= 0) return;
+    const int tid = threadIdx.x, col = tid & 127, half = tid >> 7;
+    const int tile = blockIdx.y & 3, hg = blockIdx.y >> 2, groups = static_cast<int>(gridDim.y) >> 2;
+    const int h0 = hg * kHG, heads = min(kHG, A.H - h0);
+    const int quads = 16 / static_cast<int>(gridDim.z), q0 = quads * static_cast<int>(blockIdx.z);
+    if (4 * q0 >= heads) return;
+    if (tid >= 4 * q0 && tid < 4 * (q0 + quads)) {
+        const float2 *const ml = A.part_ml + hg * kHG + tid;
+        const float sink = A.sinks && tid < heads ? A.sinks[h0 + tid] * kLog2e : -INFINITY;
+        float M = -INFINITY;
+#pragma unroll 4
+        for (int k = 0; k < ns; ++k) M = fmaxf(M, __ldcg(ml + J.slot(k) * groups * kHG).x);
+        const float Mall = fmaxf(M, sink);
+        float z = M != -INFINITY && sink != -INFINITY ? exp2f(sink - Mall) : 0.f;
+#pragma unroll 4
+        for (int k = 0; k < ns; ++k) {
+            const float2 x = __ldcg(ml + J.slot(k) * groups * kHG);
+            const float w = x.x == -INFINITY ? 0.f : exp2f(x.x - Mall);
+            reinterpret_cast<float *>(wgt[k])[tid] = w;
+            z += w * x.y;
+        }
+        const float f = M != -INFINITY && z > 0.f ? 1.f / z : 0.f;
+        for (int k = 0; k < ns; ++k) reinterpret_cast<float *>(wgt[k])[tid] *= f;
+    }
+    __syncthreads();
+    const float4 *const po = A.part_o + tile * (16 * 128) + col;
+    const int64_t to = (static_cast<int64_t>(J.t) * A.H + h0) * kHD + tile * 128 + col;
+#pragma unroll 1
+    for (int qd = q0 + half * quads / 2; qd < q0 + (half + 1) * quads / 2; qd += 2) {
+        if (4 * qd >= heads) break;
+        float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int k0 = 0; k0 < ns; k0 += kWidePer) {
+            float4 v[kWidePer][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int h = 4 * e + i;
-            if (h0 + h >= A.H) continue;
-            const int64_t to = (static_cast<int64_t>(t) * A.H + h0 + h) * kHD + tile * 128 + col;
-            const float x = o[i] * inv_z[h];
-            if (kBf16) static_cast<__nv_bfloat16 *>(A.out)[to] = __float2bfloat16(x);
-            else static_cast<float *>(A.out)[to] = x;
+            for (int k = 0; k < kWidePer; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (k0 + k < ns) v[k][e] = __ldcg(po + (J.slot(k0 + k) * groups + hg) * (4 * 16 * 128) + (qd + e) * 128);
+#pragma unroll
+            for (int k = 0; k < kWidePer; ++k) {
+                if (k0 + k >= ns) break;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float4 w = wgt[k0 + k][qd + e];
+                    acc[e].x = fmaf(w.x, v[k][e].x, acc[e].x);
+                    acc[e].y = fmaf(w.y, v[k][e].y, acc[e].y);
+                    acc[e].z = fmaf(w.z, v[k][e].z, acc[e].z);
+                    acc[e].w = fmaf(w.w, v[k][e].w, acc[e].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = 4 * (qd + e);
+            const float o[4] = {acc[e].x, acc[e].y, acc[e].z, acc[e].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (h + i < heads) join_store<kBf16>(A, to + static_cast<int64_t>(h + i) * kHD, o[i]);
         }
     }
 }
@@ -1157,14 +1237,16 @@ cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L
     const int64_t slots_max = (static_cast<int64_t>(L.max_pages) * L.page_rows + 7) / 8 * 8 + p.window;
     if (slots_max <= kCutAbove * kChunk) return cudaSuccess;
     const int entries = L.num_tokens < ctas ? L.num_tokens : ctas;
-    // few cut tokens in many parts: eight threads share a column's parts; many
-    // tokens in few parts: a thread takes 16 heads of its column
-    if (entries <= 8) {
-        auto join = A.bf16_out ? paged_join_kernel<8, 1, true> : paged_join_kernel<8, 1, false>;
-        return launch_pdl(join, dim3(entries, groups * 64), dim3(1024), 0, lc.stream, A);
-    }
-    auto join = A.bf16_out ? paged_join_kernel<1, 2, true> : paged_join_kernel<1, 2, false>;
-    return launch_pdl(join, dim3(entries, groups * 32), dim3(128), 0, lc.stream, A);
+    // one long context is cut into many parts, a batch's tokens into few
+    if (entries == 1)
+        return launch_pdl(A.bf16_out ? join_deep_kernel<8, true> : join_deep_kernel<8, false>, dim3(1, groups * 64),
+                          dim3(1024), 0, lc.stream, A);
+    if (entries <= 12)
+        return launch_pdl(A.bf16_out ? join_deep_kernel<4, true> : join_deep_kernel<4, false>,
+                          dim3(entries, groups * 64), dim3(512), 0, lc.stream, A);
+    const int share = entries * groups >= 64 ? 2 : 4;
+    return launch_pdl(A.bf16_out ? join_wide_kernel<true> : join_wide_kernel<false>,
+                      dim3(entries, groups * 4, share), dim3(256), 0, lc.stream, A);
 }
 
 }  // namespace csa

@@ -194,8 +194,8 @@ class Paged:
 #   f32: weights as two bf16 terms (2^-8 of 2^-8); sums of 16 products at a
 #     time into a truncating f32 accumulator, one step (2^-23) each: 32 of
 #     them in a logit of magnitude at most 6 (six sigma), which is the weight's
-#     relative error; at most 128 of them (2048 rows) in an output before
-#     partial sums are added with rounding.
+#     relative error; at most 160 of them (2560 rows) in an output before
+#     partial sums are added with rounding, each half a step on average.
 REL = {torch.bfloat16: 2 ** 0.5 * 2 ** -8,
        torch.float32: 2 ** -16 + 6 * 32 * 2 ** -23 + 128 * 2 ** -23}
 
