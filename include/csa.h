@@ -458,8 +458,8 @@ csa_status_t csa_page_plan(const csa_page_plan_t *plan, int32_t *dev_status, voi
  * it.  Everything else in the cache stays as it was.  Slots of one call must
  * differ (those of a plan do): where two rows have the same slot, each 16
  * bytes of it come from one of them.  rows and cache must not overlap.
- * num_pages * page_rows < 2^31, row_bytes <= 65536, else
- * CSA_ERR_UNSUPPORTED. */
+ * num_pages * page_rows and num_rows < 2^31, row_bytes <= 65536, num_rows *
+ * row_bytes < 2^36, else CSA_ERR_UNSUPPORTED. */
 typedef struct {
     const void *rows;        /* [num_rows, row_bytes], row i at i * row_pitch */
     const int64_t *slots;    /* [num_rows] */

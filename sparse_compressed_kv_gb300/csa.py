@@ -378,9 +378,21 @@ def _arg(name: str, t, dtype, shape=None, contiguous=True) -> int:
     return t.data_ptr()
 
 
-def _same_device(fn: str, index: int):
+def _device_stream(fn: str, index: int, stream=None) -> int:
+    """The stream's address for a call on tensors of device `index`, which has
+    to be the current one.  (These calls take a few microseconds on the GPU:
+    torch.cuda.current_stream's object alone would cost three.)"""
     if index != torch.cuda.current_device():
         raise ValueError(f"{fn}: tensors live on cuda:{index}, not on the current device")
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+
+
+def _ptr(t, index: int) -> int:
+    if not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"tensor must live on cuda:{index}")
+    if not t.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    return t.data_ptr()
 
 
 class PagePlan:
@@ -411,12 +423,12 @@ class PagePlan:
         self.c = csa_page_plan_t(num_seqs=B, ratio=ratio, page_rows=page_rows,
                                  max_pages=int(table.shape[1]), num_pages=int(free_ring.shape[0]),
                                  tok_cap=tok_cap, row_cap=row_cap, swa_cap=swa_cap, **at)
+        self.ref = ctypes.byref(self.c)
 
 
 def csa_page_plan(plan: PagePlan, dev_status, stream=None):
-    _same_device("csa_page_plan", plan.device)
-    _check("csa_page_plan", load().csa_page_plan(ctypes.byref(plan.c), _p(dev_status),
-                                                 _stream(stream)))
+    s = _device_stream("csa_page_plan", plan.device, stream)
+    _check("csa_page_plan", load().csa_page_plan(plan.ref, _ptr(dev_status, plan.device), s))
 
 
 class AppendJob:
@@ -450,9 +462,9 @@ class AppendJobs:
 
 
 def csa_paged_append(jobs: AppendJobs, dev_status, stream=None):
-    _same_device("csa_paged_append", jobs.device)
-    _check("csa_paged_append", load().csa_paged_append(jobs.c, len(jobs.jobs), _p(dev_status),
-                                                       _stream(stream)))
+    s = _device_stream("csa_paged_append", jobs.device, stream)
+    _check("csa_paged_append", load().csa_paged_append(jobs.c, len(jobs.jobs),
+                                                       _ptr(dev_status, jobs.device), s))
 
 
 class PagedLayout:
@@ -480,6 +492,7 @@ class PagedLayout:
             tok_pos=_arg("tok_pos", tok_pos, torch.int64, (T,)),
             row_len=_arg("row_len", row_len, torch.int64, (B,)),
             table=_arg("table", table, torch.int32), **ring)
+        self.ref = ctypes.byref(self.c)
 
 
 def csa_paged_workspace_size(layout: PagedLayout, prm: csa_params_t) -> int:
@@ -498,19 +511,20 @@ def csa_paged_attention(layout: PagedLayout, prm: csa_params_t, cache, q, out, d
                         sinks=None, stream=None):
     """cache bf16 [num_pages, page_stride, 512], q bf16 [T, H, 512], out f32 or
     bf16 [T, H, 512]."""
-    _same_device("csa_paged_attention", layout.device)
+    dev = layout.device
+    s = _device_stream("csa_paged_attention", dev, stream)
     if cache.dtype != torch.bfloat16 or q.dtype != torch.bfloat16:
         raise ValueError("cache and q must be bfloat16")
-    if out.dtype not in (torch.float32, torch.bfloat16):
+    if out.dtype != torch.float32 and out.dtype != torch.bfloat16:
         raise ValueError("out must be float32 or bfloat16")
     shape = (layout.num_tokens, prm.n_heads, prm.hd)
-    if tuple(q.shape) != shape or tuple(out.shape) != shape:
+    if q.shape != shape or out.shape != shape:
         raise ValueError(f"q and out must have shape {shape}")
     if cache.dim() != 3 or cache.shape[2] != prm.hd:
         raise ValueError(f"cache must have shape (num_pages, page_stride, {prm.hd})")
-    if sinks is not None and (sinks.dtype != torch.float32 or tuple(sinks.shape) != (prm.n_heads,)):
+    if sinks is not None and (sinks.dtype != torch.float32 or sinks.shape != (prm.n_heads,)):
         raise ValueError(f"sinks must be float32 [{prm.n_heads}]")
     _check("csa_paged_attention", load().csa_paged_attention(
-        ctypes.byref(layout.c), ctypes.byref(prm), _p(cache), int(cache.shape[0]),
-        int(cache.shape[1]), _p(q), _p(sinks), 1 if out.dtype == torch.bfloat16 else 0, _p(out),
-        _p(dev_status), _p(ws), int(ws.numel()), _stream(stream)))
+        layout.ref, ctypes.byref(prm), _ptr(cache, dev), cache.shape[0], cache.shape[1], _ptr(q, dev),
+        None if sinks is None else _ptr(sinks, dev), 1 if out.dtype == torch.bfloat16 else 0,
+        _ptr(out, dev), _ptr(dev_status, dev), _ptr(ws, dev), ws.numel(), s))

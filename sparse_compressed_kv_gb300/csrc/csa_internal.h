@@ -7,6 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "csa.h"
@@ -224,6 +225,21 @@ cudaError_t set_kernel_smem(K kernel, size_t dyn_bytes) {
     if (dyn_bytes > 48 * 1024)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(dyn_bytes));
+    return e;
+}
+
+// set_kernel_smem once per kernel and device (its two attribute calls take
+// longer than a launch); dyn_bytes is the most the kernel is launched with.
+template <auto kKernel>
+cudaError_t prepare_kernel(size_t dyn_bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    const cudaError_t g = cudaGetDevice(&dev);
+    if (g != cudaSuccess) return g;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    const cudaError_t e = set_kernel_smem(kKernel, dyn_bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
 }
 

@@ -12,14 +12,17 @@ namespace {
 // ---------------------------------------------------------------- page plan
 
 // Four exclusive prefix sums over the requests (tokens, new blocks, pages
-// taken, pages given back) fix everything; after them every output element is
-// computed by itself: token i belongs to the request whose token range holds
-// i, found by bisection.  Every CTA makes the sums for itself from the 12
-// bytes per request (no exchange between CTAs), keeps them in shared memory
-// and writes its share of the outputs.
-constexpr int kPlanThreads = 512;
+// taken, pages given back) fix everything.  Every CTA makes the sums for itself
+// from the 12 bytes per request (no exchange between CTAs) and writes its share
+// of the outputs: the kernel is a chain of latencies (load, divide, scan,
+// store), not of bytes.  In a decode step, where every request brings a few
+// tokens, the thread that summed a request writes all of its entries; with
+// prompts among them each output entry is computed by itself, its request found
+// by bisection of the sums in shared memory.
+constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxSeqs = 8192;
 constexpr int64_t kPlanMaxLen = int64_t(1) << 48;
+constexpr int kPlanFew = 8;       // tokens a request, at most, for a thread to write them in turn
 
 struct Req {
     int64_t len, end, old_rows, rows;
@@ -28,17 +31,16 @@ struct Req {
     bool over;
 };
 
-__device__ __forceinline__ Req plan_request(const csa_page_plan_t &P, int b) {
+__device__ __forceinline__ Req plan_request(const csa_page_plan_t &P, int64_t len, int32_t nl) {
     Req r;
-    r.len = P.seq_len[b];
-    const int32_t nl = P.new_len[b];
+    r.len = len;
     r.over = nl < 0;
     r.add = nl > 0 ? nl : 0;
-    r.end = r.over ? 0 : r.len + r.add;
-    r.old_rows = r.len / P.ratio;
-    r.rows = r.end / P.ratio;
-    r.old_pages = (r.old_rows + P.page_rows - 1) / P.page_rows;
-    r.pages = (r.rows + P.page_rows - 1) / P.page_rows;
+    r.end = r.over ? 0 : len + r.add;
+    r.old_rows = div_pos(len, P.ratio);
+    r.rows = div_pos(r.end, P.ratio);
+    r.old_pages = div_pos(r.old_rows + P.page_rows - 1, P.page_rows);
+    r.pages = div_pos(r.rows + P.page_rows - 1, P.page_rows);
     return r;
 }
 
@@ -73,16 +75,18 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const csa_page_
     const int B = P.num_seqs;
     int32_t *tok_off = sm, *row_off = sm + B, *need_off = sm + 2 * B, *rel_off = sm + 3 * B;
     __shared__ Sums warp_sum[kPlanThreads / 32];
-    __shared__ int bad_all;
+    __shared__ int warp_bad[kPlanThreads / 32], warp_most[kPlanThreads / 32];
+    const int nthreads = blockDim.x, nwarps = nthreads >> 5;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) bad_all = 0;
-    __syncthreads();
+    pdl_wait();      // (and no early start for what follows: it may read the maps before its own wait)
 
     // this thread's contiguous run of requests
-    const int per = (B + kPlanThreads - 1) / kPlanThreads;
+    const int per = (B + nthreads - 1) / nthreads;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    const int64_t head = P.free_pos[0], tail = P.free_pos[1], N = P.num_pages;
     Sums mine{0, 0, 0, 0};
-    int bad = 0;
+    int bad = 0, most = 0;
+    Req own{};
     for (int b = b0; b < b1; ++b) {
         const int64_t len = P.seq_len[b];
         const int32_t nl = P.new_len[b];
@@ -90,9 +94,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const csa_page_
             bad |= CSA_DEV_BAD_LENGTH;
             continue;
         }
-        const Req r = plan_request(P, b);
-        if (r.old_pages > P.max_pages || r.pages > P.max_pages) bad |= CSA_DEV_CAPACITY;
-        mine = mine + plan_sums(r);
+        own = plan_request(P, len, nl);
+        if (own.old_pages > P.max_pages || own.pages > P.max_pages) bad |= CSA_DEV_CAPACITY;
+        mine = mine + plan_sums(own);
+        most = max(most, own.add);
     }
     Sums incl = mine;
 #pragma unroll
@@ -104,117 +109,211 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const csa_page_
         v.rel = __shfl_up_sync(0xffffffffu, incl.rel, o);
         if (lane >= o) incl = incl + v;
     }
-    if (lane == 31) warp_sum[warp] = incl;
-    if (bad) atomicOr(&bad_all, bad);
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 31) {
+        warp_sum[warp] = incl;
+        warp_bad[warp] = bad;
+        warp_most[warp] = most;
+    }
     __syncthreads();
     Sums base{0, 0, 0, 0}, total{0, 0, 0, 0};
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w == warp) base = total;
-        total = total + warp_sum[w];
+    {
+        // each lane one warp's sums, scanned again by shuffles
+        Sums v{0, 0, 0, 0};
+        bad = most = 0;
+        if (lane < nwarps) {
+            v = warp_sum[lane];
+            bad = warp_bad[lane];
+            most = warp_most[lane];
+        }
+        bad = __reduce_or_sync(0xffffffffu, bad);
+        most = __reduce_max_sync(0xffffffffu, most);
+        Sums w = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            Sums u;
+            u.tok = __shfl_up_sync(0xffffffffu, w.tok, o);
+            u.row = __shfl_up_sync(0xffffffffu, w.row, o);
+            u.need = __shfl_up_sync(0xffffffffu, w.need, o);
+            u.rel = __shfl_up_sync(0xffffffffu, w.rel, o);
+            if (lane >= o) w = w + u;
+        }
+        total.tok = __shfl_sync(0xffffffffu, w.tok, 31);
+        total.row = __shfl_sync(0xffffffffu, w.row, 31);
+        total.need = __shfl_sync(0xffffffffu, w.need, 31);
+        total.rel = __shfl_sync(0xffffffffu, w.rel, 31);
+        base.tok = __shfl_sync(0xffffffffu, w.tok - v.tok, warp);
+        base.row = __shfl_sync(0xffffffffu, w.row - v.row, warp);
+        base.need = __shfl_sync(0xffffffffu, w.need - v.need, warp);
+        base.rel = __shfl_sync(0xffffffffu, w.rel - v.rel, warp);
     }
-    bad = bad_all;
-    const int64_t head = P.free_pos[0], tail = P.free_pos[1], N = P.num_pages;
     if (head < 0 || tail < head || tail - head > N || tail >= kPlanMaxLen) bad |= CSA_DEV_BAD_LAYOUT;
     else if (total.need > tail - head) bad |= CSA_DEV_CAPACITY;
     else if (tail + total.rel - head > N) bad |= CSA_DEV_BAD_LAYOUT;   // more pages than the pool has
     if (total.tok > P.tok_cap || total.row > P.row_cap) bad |= CSA_DEV_CAPACITY;
     const bool ok = bad == 0;
     if (blockIdx.x == 0 && tid == 0) raise_status(status, bad);
-
-    // exclusive offsets; a step that is refused has no tokens, blocks or pages
+    // a step that is refused has no tokens, blocks or pages
     Sums at{base.tok + incl.tok - mine.tok, base.row + incl.row - mine.row,
             base.need + incl.need - mine.need, base.rel + incl.rel - mine.rel};
-    for (int b = b0; b < b1; ++b) {
-        tok_off[b] = ok ? static_cast<int32_t>(at.tok) : 0;
-        row_off[b] = ok ? static_cast<int32_t>(at.row) : 0;
-        need_off[b] = ok ? static_cast<int32_t>(at.need) : 0;
-        rel_off[b] = ok ? static_cast<int32_t>(at.rel) : 0;
-        if (ok) at = at + plan_sums(plan_request(P, b));
-    }
     if (!ok) total = Sums{0, 0, 0, 0};
-    __syncthreads();
-
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kPlanThreads;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid;
-    for (int64_t b = first; b <= B; b += step) {
-        P.tok_off[b] = b < B ? tok_off[b] : total.tok;
-        P.row_off[b] = b < B ? row_off[b] : total.row;
-        if (b == B) break;
-        const int64_t len = P.seq_len[b];
-        const int64_t end = ok ? plan_request(P, b).end : len;
-        P.seq_len_out[b] = end;
-        P.row_len[b] = end > 0 ? end / P.ratio : 0;
-        P.swa_first_pos[b] = end > P.swa_cap ? end - P.swa_cap : 0;
-    }
-    if (first < 2) P.free_pos_out[first] = first == 0 ? head + total.need : tail + total.rel;
-    for (int64_t i = first; i < P.tok_cap; i += step) {
-        int b = -1;
-        int64_t pos = -1, slot = -1;
-        if (i < total.tok) {
-            b = plan_find(tok_off, B, static_cast<int32_t>(i));
-            const Req r = plan_request(P, b);
-            pos = r.len + (i - tok_off[b]);
-            if (pos >= r.end - P.swa_cap) slot = static_cast<int64_t>(b) * P.swa_cap + pos % P.swa_cap;
-        }
+    const bool few = ok && most <= kPlanFew;
+    const bool search = ok && (!few || total.rel > 0);
+    // place k of the ring (positions are below 2^48: their remainder once)
+    const int64_t h0 = mod_pos(ok ? head : 0, N), t0 = mod_pos(ok ? tail : 0, N);
+    auto ring = [&](int64_t base0, int64_t k) {
+        const int64_t i = base0 + k;                 // k < N: at most once around
+        return P.free_ring + (i >= N ? i - N : i);
+    };
+    auto put_token = [&](int64_t i, int b, const Req &r, int64_t k) {
+        const int64_t pos = r.len + k;
         P.tok_seq[i] = b;
         P.tok_pos[i] = pos;
-        P.swa_slot[i] = slot;
-    }
-    for (int64_t i = first; i < P.row_cap; i += step) {
-        int64_t slot = -1;
-        if (i < total.row) {
-            const int b = plan_find(row_off, B, static_cast<int32_t>(i));
-            const Req r = plan_request(P, b);
-            const int64_t g = r.old_rows + (i - row_off[b]);
-            const int64_t pg = g / P.page_rows;
-            const int32_t page = pg < r.old_pages
-                                     ? P.table[static_cast<int64_t>(b) * P.max_pages + pg]
-                                     : P.free_ring[(head + need_off[b] + (pg - r.old_pages)) % N];
-            slot = static_cast<int64_t>(page) * P.page_rows + g % P.page_rows;
+        P.swa_slot[i] = pos >= r.end - P.swa_cap ? static_cast<int64_t>(b) * P.swa_cap + mod_pos(pos, P.swa_cap) : -1;
+    };
+    // block k of the step's new ones of request b, whose new pages start at `need`
+    auto put_row = [&](int64_t i, int b, const Req &r, int64_t k, int64_t need) {
+        const int64_t g = r.old_rows + k;
+        const int64_t pg = div_pos(g, P.page_rows);
+        const int32_t page = pg < r.old_pages ? P.table[static_cast<int64_t>(b) * P.max_pages + pg]
+                                              : *ring(h0, need + (pg - r.old_pages));
+        P.row_slot[i] = static_cast<int64_t>(page) * P.page_rows + (g - pg * P.page_rows);
+    };
+
+    // per request
+    for (int b = b0; b < b1; ++b) {
+        if (per > 1 && ok) own = plan_request(P, P.seq_len[b], P.new_len[b]);
+        const int64_t before = ok ? own.len : P.seq_len[b];
+        if (search) {
+            tok_off[b] = static_cast<int32_t>(at.tok);
+            row_off[b] = static_cast<int32_t>(at.row);
+            need_off[b] = static_cast<int32_t>(at.need);
+            rel_off[b] = static_cast<int32_t>(at.rel);
         }
-        P.row_slot[i] = slot;
+        if (b % static_cast<int>(gridDim.x) == static_cast<int>(blockIdx.x)) {
+            P.tok_off[b] = ok ? at.tok : 0;
+            P.row_off[b] = ok ? at.row : 0;
+            const int64_t end = ok ? own.end : before;
+            P.seq_len_out[b] = end;
+            P.row_len[b] = end > 0 ? div_pos(end, P.ratio) : 0;
+            P.swa_first_pos[b] = end > P.swa_cap ? end - P.swa_cap : 0;
+            if (few && !own.over) {
+                for (int k = 0; k < own.add; ++k) put_token(at.tok + k, b, own, k);
+                for (int64_t k = 0; k < own.rows - own.old_rows; ++k) put_row(at.row + k, b, own, k, at.need);
+                for (int64_t k = 0; k < own.pages - own.old_pages; ++k)
+                    P.table[static_cast<int64_t>(b) * P.max_pages + own.old_pages + k] = *ring(h0, at.need + k);
+            }
+        }
+        if (ok) at = at + plan_sums(own);
     }
-    for (int64_t i = first; i < total.need; i += step) {
-        const int b = plan_find(need_off, B, static_cast<int32_t>(i));
-        const int64_t pg = plan_request(P, b).old_pages + (i - need_off[b]);
-        P.table[static_cast<int64_t>(b) * P.max_pages + pg] = P.free_ring[(head + i) % N];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * nthreads;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * nthreads + tid;
+    if (first == 0) {
+        P.tok_off[B] = total.tok;
+        P.row_off[B] = total.row;
+        P.free_pos_out[0] = head + total.need;
+        P.free_pos_out[1] = tail + total.rel;
     }
-    for (int64_t i = first; i < total.rel; i += step) {
-        const int b = plan_find(rel_off, B, static_cast<int32_t>(i));
-        P.free_ring[(tail + i) % N] = P.table[static_cast<int64_t>(b) * P.max_pages + (i - rel_off[b])];
+    for (int64_t i = total.tok + first; i < P.tok_cap; i += step) {
+        P.tok_seq[i] = -1;
+        P.tok_pos[i] = -1;
+        P.swa_slot[i] = -1;
     }
+    for (int64_t i = total.row + first; i < P.row_cap; i += step) P.row_slot[i] = -1;
+    if (search) {
+        __syncthreads();
+        if (!few) {
+            for (int64_t i = first; i < total.tok; i += step) {
+                const int b = plan_find(tok_off, B, static_cast<int32_t>(i));
+                Req r;
+                r.len = P.seq_len[b];
+                r.end = r.len + P.new_len[b];
+                put_token(i, b, r, i - tok_off[b]);
+            }
+            for (int64_t i = first; i < total.row; i += step) {
+                const int b = plan_find(row_off, B, static_cast<int32_t>(i));
+                put_row(i, b, plan_request(P, P.seq_len[b], P.new_len[b]), i - row_off[b], need_off[b]);
+            }
+            for (int64_t i = first; i < total.need; i += step) {
+                const int b = plan_find(need_off, B, static_cast<int32_t>(i));
+                const int64_t pg = plan_request(P, P.seq_len[b], P.new_len[b]).old_pages + (i - need_off[b]);
+                P.table[static_cast<int64_t>(b) * P.max_pages + pg] = *ring(h0, i);
+            }
+        }
+        for (int64_t i = first; i < total.rel; i += step) {
+            const int b = plan_find(rel_off, B, static_cast<int32_t>(i));
+            *ring(t0, i) = P.table[static_cast<int64_t>(b) * P.max_pages + (i - rel_off[b])];
+        }
+    }
+    __threadfence();
 }
 
 // ---------------------------------------------------------------- append
 
+struct AppendJob {
+    const char *rows;
+    const int64_t *slots;
+    char *cache;
+    int64_t row_pitch, page_stride;
+    uint32_t pieces, page_rows, slot_end, row_bytes;   // 16-byte pieces a row; num_pages * page_rows
+};
 struct AppendArgs {
-    csa_append_job_t job[CSA_MAX_APPEND_JOBS];
+    AppendJob job[CSA_MAX_APPEND_JOBS];
+    int64_t start[CSA_MAX_APPEND_JOBS + 1];            // first piece of each pair, all of them
     int32_t num_jobs;
 };
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendPer = 4;     // pieces a thread has in flight
 
-// One thread per 16 bytes, grid-stride over each pair's pieces.
+// A plain copy: bound by DRAM when large, by two dependent round trips (slot,
+// row) when small.  The 16-byte pieces of all pairs are one index range; a
+// thread loads four pieces and their slots before it stores the first.
+// Index arithmetic is 32-bit inside a pair: in 64 bits its divisions, four a
+// piece, took longer than the copy.
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs A, int32_t *status) {
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kAppendThreads;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x;
-    for (int j = 0; j < A.num_jobs; ++j) {
-        const csa_append_job_t &J = A.job[j];
-        const int64_t pieces = J.row_bytes / 16;
-        for (int64_t i = first; i < J.num_rows * pieces; i += step) {
-            const int64_t row = i / pieces, c = i % pieces;
-            const int64_t slot = J.slots[row];
-            if (slot < 0) continue;
-            if (slot >= J.num_pages * J.page_rows) {
-                raise_status(status, CSA_DEV_BAD_INDEX);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t all = A.start[A.num_jobs];
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kAppendThreads * kAppendPer;
+    int bad = 0;
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kAppendThreads * kAppendPer + threadIdx.x; i0 < all;
+         i0 += step) {
+        uint4 v[kAppendPer];
+        int64_t slot[kAppendPer];
+        uint32_t c[kAppendPer];
+        int j[kAppendPer];
+#pragma unroll
+        for (int k = 0; k < kAppendPer; ++k) {
+            const int64_t i = i0 + k * kAppendThreads;
+            slot[k] = -1;
+            if (i >= all) continue;
+            j[k] = 0;
+#pragma unroll
+            for (int q = 1; q < CSA_MAX_APPEND_JOBS; ++q)
+                if (q < A.num_jobs && i >= A.start[q]) j[k] = q;
+            const AppendJob &J = A.job[j[k]];
+            const uint32_t e = static_cast<uint32_t>(i - A.start[j[k]]);
+            const uint32_t row = e / J.pieces;
+            c[k] = (e - row * J.pieces) * 16;
+            slot[k] = J.slots[row];
+            v[k] = __ldcs(reinterpret_cast<const uint4 *>(J.rows + row * J.row_pitch + c[k]));
+        }
+#pragma unroll
+        for (int k = 0; k < kAppendPer; ++k) {
+            if (slot[k] < 0) continue;
+            const AppendJob &J = A.job[j[k]];
+            if (slot[k] >= J.slot_end) {
+                bad = CSA_DEV_BAD_INDEX;
                 continue;
             }
-            const int64_t at = slot / J.page_rows * J.page_stride + slot % J.page_rows;
-            const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const char *>(J.rows) +
-                                                             row * J.row_pitch + c * 16);
-            *reinterpret_cast<uint4 *>(static_cast<char *>(J.cache) + at * J.row_bytes + c * 16) = v;
+            const uint32_t s = static_cast<uint32_t>(slot[k]), page = s / J.page_rows;
+            const int64_t at = page * J.page_stride + (s - page * J.page_rows);
+            *reinterpret_cast<uint4 *>(J.cache + at * J.row_bytes + c[k]) = v[k];
         }
     }
+    raise_status(status, bad);
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -273,15 +372,15 @@ extern "C" csa_status_t csa_page_plan(const csa_page_plan_t *plan, int32_t *dev_
     int sms = 0;
     csa_status_t st = current_device(&sms);
     if (st != CSA_OK) return st;
+    if (prepare_kernel<page_plan_kernel>(kPlanMaxSeqs * 16) != cudaSuccess) return CSA_ERR_CUDA;
     const size_t smem = static_cast<size_t>(P.num_seqs) * 16;
-    if (set_kernel_smem(page_plan_kernel, smem) != cudaSuccess) return CSA_ERR_CUDA;
+    const int threads = P.num_seqs <= 128 ? 128 : P.num_seqs <= 512 ? 512 : kPlanThreads;
     int64_t items = P.tok_cap > P.row_cap ? P.tok_cap : P.row_cap;
-    if (P.num_seqs > items) items = P.num_seqs;
-    int64_t grid = (items + kPlanThreads - 1) / kPlanThreads;
+    int64_t grid = (items + 2 * threads - 1) / (2 * threads);    // two entries a thread, one CTA an SM
+    if (grid < 1) grid = 1;
     if (grid > sms) grid = sms;
-    page_plan_kernel<<<static_cast<unsigned>(grid), kPlanThreads, smem,
-                       static_cast<cudaStream_t>(stream)>>>(P, dev_status);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_pdl(page_plan_kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), smem,
+                                  static_cast<cudaStream_t>(stream), P, dev_status));
 }
 
 extern "C" csa_status_t csa_paged_append(const csa_append_job_t *jobs, int32_t num_jobs,
@@ -289,7 +388,6 @@ extern "C" csa_status_t csa_paged_append(const csa_append_job_t *jobs, int32_t n
     if (!jobs || num_jobs < 1 || !dev_status) return CSA_ERR_INVALID_ARGUMENT;
     if (num_jobs > CSA_MAX_APPEND_JOBS) return CSA_ERR_UNSUPPORTED;
     AppendArgs A{};
-    int64_t pieces = 0;
     for (int j = 0; j < num_jobs; ++j) {
         const csa_append_job_t &J = jobs[j];
         if (J.num_rows < 0 || J.row_bytes < 16 || J.row_bytes % 16 || J.page_rows < 1 ||
@@ -297,24 +395,35 @@ extern "C" csa_status_t csa_paged_append(const csa_append_job_t *jobs, int32_t n
             J.row_pitch % 16)
             return CSA_ERR_INVALID_ARGUMENT;
         if (J.num_pages >= k2G || J.num_pages * J.page_rows >= k2G || J.row_bytes > 65536 ||
-            J.page_stride >= k2G || J.num_rows >= k2G)
+            J.page_stride >= k2G || J.num_rows >= k2G || J.num_rows * J.row_bytes >= int64_t(1) << 36)
             return CSA_ERR_UNSUPPORTED;
         if (J.num_rows == 0) continue;
         if (!J.rows || !J.slots || !J.cache) return CSA_ERR_INVALID_ARGUMENT;
         if (!aligned(J.rows, 16) || !aligned(J.cache, 16) || !aligned(J.slots, 8))
             return CSA_ERR_INVALID_ARGUMENT;
-        A.job[A.num_jobs++] = J;
-        pieces += J.num_rows * (J.row_bytes / 16);
+        AppendJob &K = A.job[A.num_jobs];
+        K.rows = static_cast<const char *>(J.rows);
+        K.slots = J.slots;
+        K.cache = static_cast<char *>(J.cache);
+        K.row_pitch = J.row_pitch;
+        K.page_stride = J.page_stride;
+        K.pieces = J.row_bytes / 16;
+        K.page_rows = J.page_rows;
+        K.slot_end = static_cast<uint32_t>(J.num_pages * J.page_rows);
+        K.row_bytes = J.row_bytes;
+        A.start[A.num_jobs + 1] = A.start[A.num_jobs] + J.num_rows * K.pieces;
+        ++A.num_jobs;
     }
     if (A.num_jobs == 0) return CSA_OK;
     int sms = 0;
     csa_status_t st = current_device(&sms);
     if (st != CSA_OK) return st;
-    int64_t grid = (pieces + kAppendThreads - 1) / kAppendThreads;
+    if (prepare_kernel<append_kernel>(0) != cudaSuccess) return CSA_ERR_CUDA;
+    const int64_t per_cta = kAppendThreads * kAppendPer;
+    int64_t grid = (A.start[A.num_jobs] + per_cta - 1) / per_cta;
     if (grid > 8 * sms) grid = 8 * sms;
-    append_kernel<<<static_cast<unsigned>(grid), kAppendThreads, 0,
-                    static_cast<cudaStream_t>(stream)>>>(A, dev_status);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_pdl(append_kernel, dim3(static_cast<unsigned>(grid)), dim3(kAppendThreads), 0,
+                                  static_cast<cudaStream_t>(stream), A, dev_status));
 }
 
 extern "C" csa_status_t csa_paged_workspace_size(const csa_paged_layout_t *layout,

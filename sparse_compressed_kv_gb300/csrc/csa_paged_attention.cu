@@ -196,15 +196,6 @@ __device__ __forceinline__ constexpr uint32_t idesc_bf16() {
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Positions and unit counts are 64-bit; a 64-bit division costs a few hundred
-// cycles on the way to the first row, so those that fit take a 32-bit one.
-__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
-}
-__device__ __forceinline__ int64_t mod_pos(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) % static_cast<uint32_t>(b) : a % b;
-}
-
 // What token t attends: b < 0 for padding, n = near = 0 for a bad token.
 // `per` tokens a sequence is the guess by which the sequence's length is
 // loaded in the same round trip as its number.
@@ -212,10 +203,10 @@ __device__ __forceinline__ Rec token_rec(const PagedArgs &A, int t, int per, int
     Rec r{};
     r.t = t;
     const int g = min(t / per, A.L.num_seqs - 1);
-    r.b = A.L.tok_seq[t];
-    const int64_t pos = A.L.tok_pos[t];
-    int64_t n = A.L.row_len[g];
-    if (A.window > 0) r.first_res = A.L.swa_first_pos[g];
+    r.b = __ldcg(A.L.tok_seq + t);
+    const int64_t pos = __ldcg(A.L.tok_pos + t);
+    int64_t n = __ldcg(A.L.row_len + g);
+    if (A.window > 0) r.first_res = __ldcg(A.L.swa_first_pos + g);
     bad = 0;
     if (r.b == -1) return r;
     if (r.b < 0 || r.b >= A.L.num_seqs || pos < 0) {
@@ -224,8 +215,8 @@ __device__ __forceinline__ Rec token_rec(const PagedArgs &A, int t, int per, int
         return r;
     }
     if (r.b != g) {
-        n = A.L.row_len[r.b];
-        if (A.window > 0) r.first_res = A.L.swa_first_pos[r.b];
+        n = __ldcg(A.L.row_len + r.b);
+        if (A.window > 0) r.first_res = __ldcg(A.L.swa_first_pos + r.b);
     }
     const int64_t cap = static_cast<int64_t>(A.L.max_pages) * A.L.page_rows;
     if (n < 0) {
@@ -1159,6 +1150,20 @@ __global__ void __launch_bounds__(256) join_wide_kernel(const PagedArgs A) {
     }
 }
 
+template <auto kKernel>
+cudaError_t launch_one_join(const Launch &lc, const PagedArgs &A, dim3 grid, int threads) {
+    const cudaError_t e = prepare_kernel<kKernel>(0);
+    return e != cudaSuccess ? e : launch_pdl(kKernel, grid, dim3(threads), 0, lc.stream, A);
+}
+
+template <bool kBf16>
+cudaError_t launch_join(const Launch &lc, const PagedArgs &A, int entries, int groups) {
+    if (entries == 1) return launch_one_join<join_deep_kernel<8, kBf16>>(lc, A, dim3(1, groups * 64), 1024);
+    if (entries <= 12) return launch_one_join<join_deep_kernel<4, kBf16>>(lc, A, dim3(entries, groups * 64), 512);
+    const int share = entries * groups >= 64 ? 2 : 4;
+    return launch_one_join<join_wide_kernel<kBf16>>(lc, A, dim3(entries, groups * 4, share), 256);
+}
+
 int groups_of(const csa_params_t &p) { return (p.n_heads + kHG - 1) / kHG; }
 
 struct Ws {
@@ -1227,26 +1232,23 @@ cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L
     A.part_o = reinterpret_cast<float4 *>(wb + w.o);
     A.status = status;
     const int ctas = (lc.sm_count < kMaxCtas ? lc.sm_count : kMaxCtas) / groups;
-    auto kern = A.bf16_out ? paged_attention_kernel<1> : paged_attention_kernel<2>;
-    const size_t smem = A.bf16_out ? smem_bytes<1>() : smem_bytes<2>();
-    cudaError_t e = set_kernel_smem(kern, smem);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(ctas, groups), dim3(kThreads), smem, lc.stream, tq, tr, A);
+    cudaError_t e;
+    if (A.bf16_out) {
+        e = prepare_kernel<paged_attention_kernel<1>>(smem_bytes<1>());
+        if (e == cudaSuccess)
+            e = launch_pdl(paged_attention_kernel<1>, dim3(ctas, groups), dim3(kThreads), smem_bytes<1>(), lc.stream, tq, tr, A);
+    } else {
+        e = prepare_kernel<paged_attention_kernel<2>>(smem_bytes<2>());
+        if (e == cudaSuccess)
+            e = launch_pdl(paged_attention_kernel<2>, dim3(ctas, groups), dim3(kThreads), smem_bytes<2>(), lc.stream, tq, tr, A);
+    }
     if (e != cudaSuccess) return e;
     // no token can be cut: nothing to join
     const int64_t slots_max = (static_cast<int64_t>(L.max_pages) * L.page_rows + 7) / 8 * 8 + p.window;
     if (slots_max <= kCutAbove * kChunk) return cudaSuccess;
     const int entries = L.num_tokens < ctas ? L.num_tokens : ctas;
     // one long context is cut into many parts, a batch's tokens into few
-    if (entries == 1)
-        return launch_pdl(A.bf16_out ? join_deep_kernel<8, true> : join_deep_kernel<8, false>, dim3(1, groups * 64),
-                          dim3(1024), 0, lc.stream, A);
-    if (entries <= 12)
-        return launch_pdl(A.bf16_out ? join_deep_kernel<4, true> : join_deep_kernel<4, false>,
-                          dim3(entries, groups * 64), dim3(512), 0, lc.stream, A);
-    const int share = entries * groups >= 64 ? 2 : 4;
-    return launch_pdl(A.bf16_out ? join_wide_kernel<true> : join_wide_kernel<false>,
-                      dim3(entries, groups * 4, share), dim3(256), 0, lc.stream, A);
+    return A.bf16_out ? launch_join<true>(lc, A, entries, groups) : launch_join<false>(lc, A, entries, groups);
 }
 
 }  // namespace csa
