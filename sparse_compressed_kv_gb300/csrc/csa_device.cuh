@@ -101,15 +101,6 @@ __device__ __forceinline__ int64_t window_first(int64_t p, int window) {
     return f < 0 ? 0 : f;
 }
 
-// Positions are 64-bit; a 64-bit division costs a few hundred cycles, so those
-// that fit (both operands in 32 bits) take a 32-bit one.
-__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
-}
-__device__ __forceinline__ int64_t mod_pos(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) % static_cast<uint32_t>(b) : a % b;
-}
-
 __device__ __forceinline__ void raise_status(int32_t *st, int bits) {
     if (bits && st) atomicOr(st, bits);
 }

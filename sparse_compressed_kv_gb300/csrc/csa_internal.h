@@ -196,6 +196,31 @@ cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L
                                    int64_t page_stride, const void *q, const float *sinks,
                                    csa_type_t out_type, void *out, int32_t *status, void *ws);
 
+// Division of 32-bit numbers by a number known on the host: a high product, an
+// average and a shift instead of a division (T. Granlund, P. Montgomery,
+// "Division by invariant integers using multiplication", 1994).
+struct FastDiv {
+    uint32_t d, mul, s1, s2;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t div) : d(div) {
+        uint32_t l = 0;
+        while (l < 32 && (uint64_t(1) << l) < div) ++l;
+        mul = static_cast<uint32_t>(((((uint64_t(1) << l) - div) << 32) / div) + 1);
+        s1 = l < 1 ? l : 1;
+        s2 = l > 0 ? l - 1 : 0;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t div(uint32_t n) const {
+        const uint32_t t = __umulhi(mul, n);
+        return (t + ((n - t) >> s1)) >> s2;
+    }
+    __device__ __forceinline__ uint32_t mod(uint32_t n) const { return n - div(n) * d; }
+    // any non-negative number: 64-bit arithmetic where it does not fit
+    __device__ __forceinline__ int64_t div64(int64_t n) const { return (n >> 32) == 0 ? div(static_cast<uint32_t>(n)) : n / d; }
+    __device__ __forceinline__ int64_t mod64(int64_t n) const { return (n >> 32) == 0 ? mod(static_cast<uint32_t>(n)) : n % d; }
+#endif
+};
+
 // Launch helper: programmatic dependent launch on, so each kernel's prologue
 // may overlap the previous kernel's tail (kernels wait with griddepcontrol).
 template <typename... KArgs, typename... Args>

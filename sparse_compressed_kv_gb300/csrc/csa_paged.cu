@@ -13,239 +13,239 @@ namespace {
 
 // Four exclusive prefix sums over the requests (tokens, new blocks, pages
 // taken, pages given back) fix everything.  Every CTA makes the sums for itself
-// from the 12 bytes per request (no exchange between CTAs) and writes its share
-// of the outputs: the kernel is a chain of latencies (load, divide, scan,
-// store), not of bytes.  In a decode step, where every request brings a few
-// tokens, the thread that summed a request writes all of its entries; with
-// prompts among them each output entry is computed by itself, its request found
-// by bisection of the sums in shared memory.
-constexpr int kPlanThreads = 1024;
+// from the 12 bytes per request (no exchange between CTAs), keeps them in
+// shared memory and writes its share of the outputs.  The kernel is a chain of
+// latencies and of instructions, not of bytes: small CTAs, each thread summing
+// several requests, divisions by products, 32-bit sums.  In a decode step,
+// where every request brings a few tokens, the thread that has a request writes
+// all of its entries; with prompts among them each output entry is computed by
+// itself, its request found by bisection.
+constexpr int kPlanThreads = 256;
+constexpr int kPlanBatch = 4;     // requests a thread loads at a time
 constexpr int kPlanMaxSeqs = 8192;
 constexpr int64_t kPlanMaxLen = int64_t(1) << 48;
-constexpr int kPlanFew = 8;       // tokens a request, at most, for a thread to write them in turn
+constexpr uint32_t kPlanFew = 8;  // tokens a request, at most, for a thread to write them in turn
+
+struct PlanArgs {
+    csa_page_plan_t P;
+    FastDiv ratio, page_rows, swa_cap, num_pages;
+};
 
 struct Req {
-    int64_t len, end, old_rows, rows;
-    int64_t old_pages, pages;
-    int32_t add;      // new tokens
+    int64_t len, end, old_rows;
+    uint32_t add, new_rows;       // tokens and blocks that the step brings
+    int32_t old_pages, pages;     // (saturated: more than the table has is refused)
     bool over;
 };
 
-__device__ __forceinline__ Req plan_request(const csa_page_plan_t &P, int64_t len, int32_t nl) {
+__device__ __forceinline__ int32_t plan_pages(const PlanArgs &A, int64_t rows) {
+    const int64_t n = A.page_rows.div64(rows + A.P.page_rows - 1);
+    return n > INT32_MAX ? INT32_MAX : static_cast<int32_t>(n);
+}
+
+__device__ __forceinline__ Req plan_request(const PlanArgs &A, int64_t len, int32_t nl) {
     Req r;
     r.len = len;
     r.over = nl < 0;
     r.add = nl > 0 ? nl : 0;
     r.end = r.over ? 0 : len + r.add;
-    r.old_rows = div_pos(len, P.ratio);
-    r.rows = div_pos(r.end, P.ratio);
-    r.old_pages = div_pos(r.old_rows + P.page_rows - 1, P.page_rows);
-    r.pages = div_pos(r.rows + P.page_rows - 1, P.page_rows);
+    r.old_rows = A.ratio.div64(len);
+    // len = old_rows ratio + rest; the sum below fits 32 bits
+    r.new_rows = A.ratio.div(static_cast<uint32_t>(len - r.old_rows * A.P.ratio) + r.add);
+    r.old_pages = plan_pages(A, r.old_rows);
+    r.pages = plan_pages(A, r.old_rows + r.new_rows);
     return r;
 }
 
 struct Sums {
-    int64_t tok, row, need, rel;
+    uint32_t tok, row, need, rel;
 };
 
 __device__ __forceinline__ Sums operator+(const Sums &a, const Sums &b) {
     return {a.tok + b.tok, a.row + b.row, a.need + b.need, a.rel + b.rel};
 }
+__device__ __forceinline__ Sums operator-(const Sums &a, const Sums &b) {
+    return {a.tok - b.tok, a.row - b.row, a.need - b.need, a.rel - b.rel};
+}
 
 __device__ __forceinline__ Sums plan_sums(const Req &r) {
-    if (r.over) return {0, 0, 0, r.old_pages};
-    return {r.add, r.rows - r.old_rows, r.pages - r.old_pages, 0};
+    if (r.over) return {0, 0, 0, static_cast<uint32_t>(r.old_pages)};
+    return {r.add, r.new_rows, static_cast<uint32_t>(r.pages - r.old_pages), 0};
+}
+
+__device__ __forceinline__ Sums scan_warp(Sums v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sums u{__shfl_up_sync(0xffffffffu, v.tok, o), __shfl_up_sync(0xffffffffu, v.row, o),
+                     __shfl_up_sync(0xffffffffu, v.need, o), __shfl_up_sync(0xffffffffu, v.rel, o)};
+        if (lane >= o) v = v + u;
+    }
+    return v;
 }
 
 // The last request whose range starts at or before i (ranges of requests
 // without elements are empty, so the last one that starts there holds i).
-__device__ __forceinline__ int plan_find(const int32_t *off, int n, int32_t i) {
+template <uint32_t Sums::*kField>
+__device__ __forceinline__ int plan_find(const Sums *off, int n, uint32_t i) {
     int lo = 0, hi = n;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (off[mid] <= i) lo = mid;
+        if (off[mid].*kField <= i) lo = mid;
         else hi = mid;
     }
     return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const csa_page_plan_t P,
-                                                                 int32_t *status) {
-    extern __shared__ int32_t sm[];
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs A, int32_t *status) {
+    extern __shared__ Sums off[];                // [B] exclusive
+    const csa_page_plan_t &P = A.P;
     const int B = P.num_seqs;
-    int32_t *tok_off = sm, *row_off = sm + B, *need_off = sm + 2 * B, *rel_off = sm + 3 * B;
-    __shared__ Sums warp_sum[kPlanThreads / 32];
-    __shared__ int warp_bad[kPlanThreads / 32], warp_most[kPlanThreads / 32];
-    const int nthreads = blockDim.x, nwarps = nthreads >> 5;
+    constexpr int kWarps = kPlanThreads / 32;
+    __shared__ Sums warp_sum[kWarps];
+    __shared__ uint32_t warp_tok[kWarps], warp_rel[kWarps], warp_bad[kWarps], warp_most[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();      // (and no early start for what follows: it may read the maps before its own wait)
+    const int64_t head = P.free_pos[0], tail = P.free_pos[1], N = P.num_pages;
 
     // this thread's contiguous run of requests
-    const int per = (B + nthreads - 1) / nthreads;
+    const int per = (B + kPlanThreads - 1) / kPlanThreads;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    const int64_t head = P.free_pos[0], tail = P.free_pos[1], N = P.num_pages;
     Sums mine{0, 0, 0, 0};
-    int bad = 0, most = 0;
-    Req own{};
-    for (int b = b0; b < b1; ++b) {
-        const int64_t len = P.seq_len[b];
-        const int32_t nl = P.new_len[b];
-        if (len < 0 || len >= kPlanMaxLen || nl < -1) {
-            bad |= CSA_DEV_BAD_LENGTH;
-            continue;
-        }
-        own = plan_request(P, len, nl);
-        if (own.old_pages > P.max_pages || own.pages > P.max_pages) bad |= CSA_DEV_CAPACITY;
-        mine = mine + plan_sums(own);
-        most = max(most, own.add);
-    }
-    Sums incl = mine;
+    // Sums are 32-bit; whether one passes 2^31 (more than any capacity) shows in
+    // the sums of the upper halves of what is added: where those stay
+    // below 2^15, 8192 requests add less than 2^32.
+    uint32_t bad = 0, most = 0, tok_hi = 0, rel_hi = 0;
+    for (int b = b0; b < b1; b += kPlanBatch) {
+        int64_t len[kPlanBatch];
+        int32_t nl[kPlanBatch];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        Sums v;
-        v.tok = __shfl_up_sync(0xffffffffu, incl.tok, o);
-        v.row = __shfl_up_sync(0xffffffffu, incl.row, o);
-        v.need = __shfl_up_sync(0xffffffffu, incl.need, o);
-        v.rel = __shfl_up_sync(0xffffffffu, incl.rel, o);
-        if (lane >= o) incl = incl + v;
+        for (int k = 0; k < kPlanBatch; ++k) {
+            len[k] = b + k < b1 ? P.seq_len[b + k] : 0;
+            nl[k] = b + k < b1 ? P.new_len[b + k] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kPlanBatch; ++k) {
+            if (b + k >= b1) break;
+            off[b + k] = mine;
+            if (len[k] < 0 || len[k] >= kPlanMaxLen || nl[k] < -1) {
+                bad |= CSA_DEV_BAD_LENGTH;
+                continue;
+            }
+            const Req r = plan_request(A, len[k], nl[k]);
+            if (r.old_pages > P.max_pages || r.pages > P.max_pages) bad |= CSA_DEV_CAPACITY;
+            const Sums v = plan_sums(r);
+            mine = mine + v;
+            most = max(most, r.add);
+            tok_hi += v.tok >> 16;
+            rel_hi += v.rel >> 16;
+        }
     }
+    const Sums incl = scan_warp(mine, lane);
     bad = __reduce_or_sync(0xffffffffu, bad);
     most = __reduce_max_sync(0xffffffffu, most);
+    tok_hi = __reduce_add_sync(0xffffffffu, tok_hi);
+    rel_hi = __reduce_add_sync(0xffffffffu, rel_hi);
     if (lane == 31) {
         warp_sum[warp] = incl;
         warp_bad[warp] = bad;
         warp_most[warp] = most;
+        warp_tok[warp] = tok_hi;
+        warp_rel[warp] = rel_hi;
     }
     __syncthreads();
     Sums base{0, 0, 0, 0}, total{0, 0, 0, 0};
-    {
-        // each lane one warp's sums, scanned again by shuffles
-        Sums v{0, 0, 0, 0};
-        bad = most = 0;
-        if (lane < nwarps) {
-            v = warp_sum[lane];
-            bad = warp_bad[lane];
-            most = warp_most[lane];
-        }
-        bad = __reduce_or_sync(0xffffffffu, bad);
-        most = __reduce_max_sync(0xffffffffu, most);
-        Sums w = v;
+    bad = most = tok_hi = rel_hi = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            Sums u;
-            u.tok = __shfl_up_sync(0xffffffffu, w.tok, o);
-            u.row = __shfl_up_sync(0xffffffffu, w.row, o);
-            u.need = __shfl_up_sync(0xffffffffu, w.need, o);
-            u.rel = __shfl_up_sync(0xffffffffu, w.rel, o);
-            if (lane >= o) w = w + u;
-        }
-        total.tok = __shfl_sync(0xffffffffu, w.tok, 31);
-        total.row = __shfl_sync(0xffffffffu, w.row, 31);
-        total.need = __shfl_sync(0xffffffffu, w.need, 31);
-        total.rel = __shfl_sync(0xffffffffu, w.rel, 31);
-        base.tok = __shfl_sync(0xffffffffu, w.tok - v.tok, warp);
-        base.row = __shfl_sync(0xffffffffu, w.row - v.row, warp);
-        base.need = __shfl_sync(0xffffffffu, w.need - v.need, warp);
-        base.rel = __shfl_sync(0xffffffffu, w.rel - v.rel, warp);
+    for (int w = 0; w < kWarps; ++w) {
+        if (w == warp) base = total;
+        total = total + warp_sum[w];
+        bad |= warp_bad[w];
+        most = max(most, warp_most[w]);
+        tok_hi += warp_tok[w];
+        rel_hi += warp_rel[w];
     }
+    const bool wide = tok_hi >= 1u << 15;        // (blocks and pages are no more than tokens)
     if (head < 0 || tail < head || tail - head > N || tail >= kPlanMaxLen) bad |= CSA_DEV_BAD_LAYOUT;
-    else if (total.need > tail - head) bad |= CSA_DEV_CAPACITY;
-    else if (tail + total.rel - head > N) bad |= CSA_DEV_BAD_LAYOUT;   // more pages than the pool has
-    if (total.tok > P.tok_cap || total.row > P.row_cap) bad |= CSA_DEV_CAPACITY;
+    else if (wide || total.need > tail - head) bad |= CSA_DEV_CAPACITY;
+    else if (rel_hi >= 1u << 15 || tail + total.rel - head > N) bad |= CSA_DEV_BAD_LAYOUT;   // more pages than the pool has
+    if (wide || total.tok > P.tok_cap || total.row > P.row_cap) bad |= CSA_DEV_CAPACITY;
     const bool ok = bad == 0;
-    if (blockIdx.x == 0 && tid == 0) raise_status(status, bad);
-    // a step that is refused has no tokens, blocks or pages
-    Sums at{base.tok + incl.tok - mine.tok, base.row + incl.row - mine.row,
-            base.need + incl.need - mine.need, base.rel + incl.rel - mine.rel};
-    if (!ok) total = Sums{0, 0, 0, 0};
-    const bool few = ok && most <= kPlanFew;
-    const bool search = ok && (!few || total.rel > 0);
-    // place k of the ring (positions are below 2^48: their remainder once)
-    const int64_t h0 = mod_pos(ok ? head : 0, N), t0 = mod_pos(ok ? tail : 0, N);
-    auto ring = [&](int64_t base0, int64_t k) {
-        const int64_t i = base0 + k;                 // k < N: at most once around
+    if (blockIdx.x == 0 && tid == 0) raise_status(status, static_cast<int>(bad));
+    if (!ok) total = Sums{0, 0, 0, 0};           // no tokens, blocks or pages
+    const Sums front = base + incl - mine;
+    for (int b = b0; b < b1; ++b) off[b] = ok ? off[b] + front : Sums{0, 0, 0, 0};
+    __syncthreads();
+
+    // place k of the ring, k < N: at most once around
+    const int64_t h0 = ok ? A.num_pages.mod64(head) : 0, t0 = ok ? A.num_pages.mod64(tail) : 0;
+    auto ring = [&](int64_t from, uint32_t k) {
+        const int64_t i = from + k;
         return P.free_ring + (i >= N ? i - N : i);
     };
-    auto put_token = [&](int64_t i, int b, const Req &r, int64_t k) {
-        const int64_t pos = r.len + k;
+    auto put_token = [&](uint32_t i, int b, int64_t pos, int64_t end) {
         P.tok_seq[i] = b;
         P.tok_pos[i] = pos;
-        P.swa_slot[i] = pos >= r.end - P.swa_cap ? static_cast<int64_t>(b) * P.swa_cap + mod_pos(pos, P.swa_cap) : -1;
+        P.swa_slot[i] = pos >= end - P.swa_cap ? static_cast<int64_t>(b) * P.swa_cap + A.swa_cap.mod64(pos) : -1;
     };
-    // block k of the step's new ones of request b, whose new pages start at `need`
-    auto put_row = [&](int64_t i, int b, const Req &r, int64_t k, int64_t need) {
+    // new block k of request b, whose new pages start at place `need`
+    auto put_row = [&](uint32_t i, int b, const Req &r, uint32_t k, uint32_t need) {
         const int64_t g = r.old_rows + k;
-        const int64_t pg = div_pos(g, P.page_rows);
+        const int32_t pg = static_cast<int32_t>(A.page_rows.div64(g));     // < max_pages
         const int32_t page = pg < r.old_pages ? P.table[static_cast<int64_t>(b) * P.max_pages + pg]
                                               : *ring(h0, need + (pg - r.old_pages));
-        P.row_slot[i] = static_cast<int64_t>(page) * P.page_rows + (g - pg * P.page_rows);
+        P.row_slot[i] = static_cast<int64_t>(page) * P.page_rows + (g - static_cast<int64_t>(pg) * P.page_rows);
     };
-
-    // per request
-    for (int b = b0; b < b1; ++b) {
-        if (per > 1 && ok) own = plan_request(P, P.seq_len[b], P.new_len[b]);
-        const int64_t before = ok ? own.len : P.seq_len[b];
-        if (search) {
-            tok_off[b] = static_cast<int32_t>(at.tok);
-            row_off[b] = static_cast<int32_t>(at.row);
-            need_off[b] = static_cast<int32_t>(at.need);
-            rel_off[b] = static_cast<int32_t>(at.rel);
-        }
-        if (b % static_cast<int>(gridDim.x) == static_cast<int>(blockIdx.x)) {
-            P.tok_off[b] = ok ? at.tok : 0;
-            P.row_off[b] = ok ? at.row : 0;
-            const int64_t end = ok ? own.end : before;
-            P.seq_len_out[b] = end;
-            P.row_len[b] = end > 0 ? div_pos(end, P.ratio) : 0;
-            P.swa_first_pos[b] = end > P.swa_cap ? end - P.swa_cap : 0;
-            if (few && !own.over) {
-                for (int k = 0; k < own.add; ++k) put_token(at.tok + k, b, own, k);
-                for (int64_t k = 0; k < own.rows - own.old_rows; ++k) put_row(at.row + k, b, own, k, at.need);
-                for (int64_t k = 0; k < own.pages - own.old_pages; ++k)
-                    P.table[static_cast<int64_t>(b) * P.max_pages + own.old_pages + k] = *ring(h0, at.need + k);
-            }
-        }
-        if (ok) at = at + plan_sums(own);
+    const bool few = most <= kPlanFew;
+    const uint32_t step = gridDim.x * kPlanThreads, first = blockIdx.x * kPlanThreads + tid;
+    for (uint32_t b = first; b < static_cast<uint32_t>(B); b += step) {
+        const Sums at = off[b];
+        P.tok_off[b] = at.tok;
+        P.row_off[b] = at.row;
+        const int64_t len = P.seq_len[b];
+        Req r{};
+        if (ok) r = plan_request(A, len, P.new_len[b]);
+        const int64_t end = ok ? r.end : len;
+        P.seq_len_out[b] = end;
+        P.row_len[b] = ok ? (r.over ? 0 : r.old_rows + r.new_rows) : end > 0 ? end / P.ratio : 0;
+        P.swa_first_pos[b] = end > P.swa_cap ? end - P.swa_cap : 0;
+        if (!ok || !few || r.over) continue;
+        for (uint32_t k = 0; k < r.add; ++k) put_token(at.tok + k, b, len + k, end);
+        for (uint32_t k = 0; k < r.new_rows; ++k) put_row(at.row + k, b, r, k, at.need);
+        for (int32_t pg = r.old_pages; pg < r.pages; ++pg)
+            P.table[static_cast<int64_t>(b) * P.max_pages + pg] = *ring(h0, at.need + (pg - r.old_pages));
     }
-    const int64_t step = static_cast<int64_t>(gridDim.x) * nthreads;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * nthreads + tid;
     if (first == 0) {
         P.tok_off[B] = total.tok;
         P.row_off[B] = total.row;
         P.free_pos_out[0] = head + total.need;
         P.free_pos_out[1] = tail + total.rel;
     }
-    for (int64_t i = total.tok + first; i < P.tok_cap; i += step) {
+    if (!few) {
+        for (uint32_t i = first; i < total.tok; i += step) {
+            const int b = plan_find<&Sums::tok>(off, B, i);
+            const int64_t len = P.seq_len[b];
+            put_token(i, b, len + (i - off[b].tok), len + P.new_len[b]);
+        }
+        for (uint32_t i = first; i < total.row; i += step) {
+            const int b = plan_find<&Sums::row>(off, B, i);
+            put_row(i, b, plan_request(A, P.seq_len[b], P.new_len[b]), i - off[b].row, off[b].need);
+        }
+        for (uint32_t i = first; i < total.need; i += step) {
+            const int b = plan_find<&Sums::need>(off, B, i);
+            const int32_t pg = plan_pages(A, A.ratio.div64(P.seq_len[b])) + static_cast<int32_t>(i - off[b].need);
+            P.table[static_cast<int64_t>(b) * P.max_pages + pg] = *ring(h0, i);
+        }
+    }
+    for (uint32_t i = first; i < total.rel; i += step) {
+        const int b = plan_find<&Sums::rel>(off, B, i);
+        *ring(t0, i) = P.table[static_cast<int64_t>(b) * P.max_pages + (i - off[b].rel)];
+    }
+    for (int64_t i = static_cast<int64_t>(total.tok) + first; i < P.tok_cap; i += step) {
         P.tok_seq[i] = -1;
         P.tok_pos[i] = -1;
         P.swa_slot[i] = -1;
     }
-    for (int64_t i = total.row + first; i < P.row_cap; i += step) P.row_slot[i] = -1;
-    if (search) {
-        __syncthreads();
-        if (!few) {
-            for (int64_t i = first; i < total.tok; i += step) {
-                const int b = plan_find(tok_off, B, static_cast<int32_t>(i));
-                Req r;
-                r.len = P.seq_len[b];
-                r.end = r.len + P.new_len[b];
-                put_token(i, b, r, i - tok_off[b]);
-            }
-            for (int64_t i = first; i < total.row; i += step) {
-                const int b = plan_find(row_off, B, static_cast<int32_t>(i));
-                put_row(i, b, plan_request(P, P.seq_len[b], P.new_len[b]), i - row_off[b], need_off[b]);
-            }
-            for (int64_t i = first; i < total.need; i += step) {
-                const int b = plan_find(need_off, B, static_cast<int32_t>(i));
-                const int64_t pg = plan_request(P, P.seq_len[b], P.new_len[b]).old_pages + (i - need_off[b]);
-                P.table[static_cast<int64_t>(b) * P.max_pages + pg] = *ring(h0, i);
-            }
-        }
-        for (int64_t i = first; i < total.rel; i += step) {
-            const int b = plan_find(rel_off, B, static_cast<int32_t>(i));
-            *ring(t0, i) = P.table[static_cast<int64_t>(b) * P.max_pages + (i - rel_off[b])];
-        }
-    }
+    for (int64_t i = static_cast<int64_t>(total.row) + first; i < P.row_cap; i += step) P.row_slot[i] = -1;
     __threadfence();
 }
 
@@ -256,7 +256,8 @@ struct AppendJob {
     const int64_t *slots;
     char *cache;
     int64_t row_pitch, page_stride;
-    uint32_t pieces, page_rows, slot_end, row_bytes;   // 16-byte pieces a row; num_pages * page_rows
+    FastDiv pieces, page_rows;                         // 16-byte pieces a row
+    uint32_t slot_end, row_bytes;                      // slot_end: num_pages * page_rows
 };
 struct AppendArgs {
     AppendJob job[CSA_MAX_APPEND_JOBS];
@@ -295,8 +296,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
                 if (q < A.num_jobs && i >= A.start[q]) j[k] = q;
             const AppendJob &J = A.job[j[k]];
             const uint32_t e = static_cast<uint32_t>(i - A.start[j[k]]);
-            const uint32_t row = e / J.pieces;
-            c[k] = (e - row * J.pieces) * 16;
+            const uint32_t row = J.pieces.div(e);
+            c[k] = (e - row * J.pieces.d) * 16;
             slot[k] = J.slots[row];
             v[k] = __ldcs(reinterpret_cast<const uint4 *>(J.rows + row * J.row_pitch + c[k]));
         }
@@ -308,8 +309,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
                 bad = CSA_DEV_BAD_INDEX;
                 continue;
             }
-            const uint32_t s = static_cast<uint32_t>(slot[k]), page = s / J.page_rows;
-            const int64_t at = page * J.page_stride + (s - page * J.page_rows);
+            const uint32_t s = static_cast<uint32_t>(slot[k]), page = J.page_rows.div(s);
+            const int64_t at = page * J.page_stride + (s - page * J.page_rows.d);
             *reinterpret_cast<uint4 *>(J.cache + at * J.row_bytes + c[k]) = v[k];
         }
     }
@@ -372,15 +373,17 @@ extern "C" csa_status_t csa_page_plan(const csa_page_plan_t *plan, int32_t *dev_
     int sms = 0;
     csa_status_t st = current_device(&sms);
     if (st != CSA_OK) return st;
-    if (prepare_kernel<page_plan_kernel>(kPlanMaxSeqs * 16) != cudaSuccess) return CSA_ERR_CUDA;
-    const size_t smem = static_cast<size_t>(P.num_seqs) * 16;
-    const int threads = P.num_seqs <= 128 ? 128 : P.num_seqs <= 512 ? 512 : kPlanThreads;
+    if (prepare_kernel<page_plan_kernel>(kPlanMaxSeqs * sizeof(Sums)) != cudaSuccess) return CSA_ERR_CUDA;
+    const size_t smem = static_cast<size_t>(P.num_seqs) * sizeof(Sums);
+    // a request or two output entries a thread, one CTA an SM at most
     int64_t items = P.tok_cap > P.row_cap ? P.tok_cap : P.row_cap;
-    int64_t grid = (items + 2 * threads - 1) / (2 * threads);    // two entries a thread, one CTA an SM
-    if (grid < 1) grid = 1;
+    items = (items + 1) / 2 > P.num_seqs ? (items + 1) / 2 : P.num_seqs;
+    int64_t grid = (items + kPlanThreads - 1) / kPlanThreads;
     if (grid > sms) grid = sms;
-    return cuda_status(launch_pdl(page_plan_kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), smem,
-                                  static_cast<cudaStream_t>(stream), P, dev_status));
+    const PlanArgs A{P, FastDiv(P.ratio), FastDiv(P.page_rows), FastDiv(P.swa_cap),
+                     FastDiv(static_cast<uint32_t>(P.num_pages))};
+    return cuda_status(launch_pdl(page_plan_kernel, dim3(static_cast<unsigned>(grid)), dim3(kPlanThreads), smem,
+                                  static_cast<cudaStream_t>(stream), A, dev_status));
 }
 
 extern "C" csa_status_t csa_paged_append(const csa_append_job_t *jobs, int32_t num_jobs,
@@ -407,11 +410,11 @@ extern "C" csa_status_t csa_paged_append(const csa_append_job_t *jobs, int32_t n
         K.cache = static_cast<char *>(J.cache);
         K.row_pitch = J.row_pitch;
         K.page_stride = J.page_stride;
-        K.pieces = J.row_bytes / 16;
-        K.page_rows = J.page_rows;
+        K.pieces = FastDiv(J.row_bytes / 16);
+        K.page_rows = FastDiv(J.page_rows);
         K.slot_end = static_cast<uint32_t>(J.num_pages * J.page_rows);
         K.row_bytes = J.row_bytes;
-        A.start[A.num_jobs + 1] = A.start[A.num_jobs] + J.num_rows * K.pieces;
+        A.start[A.num_jobs + 1] = A.start[A.num_jobs] + J.num_rows * K.pieces.d;
         ++A.num_jobs;
     }
     if (A.num_jobs == 0) return CSA_OK;

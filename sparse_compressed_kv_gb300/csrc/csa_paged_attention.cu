@@ -63,6 +63,7 @@ struct PagedArgs {
     int32_t H, window, ratio, bf16_out;
     float scale_log2;
     int32_t total_rows;       // rows of the pool: the coordinate that reads as zeros
+    FastDiv page_div, ratio_div, swa_div;   // by page_rows, ratio, swa_cap
     int64_t num_pages, page_stride;
     const __nv_bfloat16 *cache;
     const float *sinks;
@@ -227,7 +228,7 @@ __device__ __forceinline__ Rec token_rec(const PagedArgs &A, int t, int per, int
         bad |= CSA_DEV_CAPACITY;
         n = cap;
     }
-    const int64_t seen = div_pos(pos, A.ratio);
+    const int64_t seen = A.ratio_div.div64(pos);
     r.n = static_cast<int32_t>(n < seen ? n : seen);
     if (A.window > 0) {
         r.first = window_first(pos, A.window);
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // its first table entry on its way while the roles start
         if (r.c0 * kChunk < r.n)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(A.L.table + static_cast<int64_t>(r.b) * A.L.max_pages +
-                                                          r.c0 * kChunk / A.L.page_rows));
+                                                          A.page_div.div(r.c0 * kChunk)));
         if (at == kMaxRec - 1 && !direct) {
             S.more = 1;
             S.s0 = s + chunk_cost(c);
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (k.i >= nrec) return e;
                 const int n = S.rec[k.i].n, j = k.c * kChunk + 16 * li + rl;
                 if (j < n) {
-                    const int pg = j / A.L.page_rows;
+                    const int pg = static_cast<int>(A.page_div.div(j));
                     e.in_page = j - pg * A.L.page_rows;
                     e.page = A.L.table[static_cast<int64_t>(S.rec[k.i].b) * A.L.max_pages + pg];
                     e.box = j + 8 <= n && e.in_page + 8 <= A.L.page_rows;
@@ -677,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (x < r.first_res) bad |= CSA_DEV_MISSING_SWA;
                     else
                         src = static_cast<const __nv_bfloat16 *>(A.L.swa_kv) +
-                              (static_cast<int64_t>(r.b) * A.L.swa_cap + mod_pos(x, A.L.swa_cap)) * kHD;
+                              (static_cast<int64_t>(r.b) * A.L.swa_cap + A.swa_div.mod64(x)) * kHD;
                 }
                 const uint32_t okm = __ballot_sync(0xffffffffu, src != nullptr) & 0xFFFFu;
                 const int32_t y1 = __shfl_sync(0xffffffffu, now.row, 8);
@@ -1222,6 +1223,9 @@ cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L
     A.bf16_out = out_type == CSA_BF16;
     A.scale_log2 = p.scale * kLog2e;
     A.total_rows = static_cast<int32_t>(total_rows);
+    A.page_div = FastDiv(L.page_rows);
+    A.ratio_div = FastDiv(p.ratio);
+    A.swa_div = FastDiv(L.swa_cap > 0 ? L.swa_cap : 1);
     A.num_pages = num_pages;
     A.page_stride = page_stride;
     A.cache = static_cast<const __nv_bfloat16 *>(cache);
