@@ -64,6 +64,7 @@ struct PagedArgs {
     float scale_log2;
     int32_t total_rows;       // rows of the pool: the coordinate that reads as zeros
     FastDiv page_div, ratio_div, swa_div;   // by page_rows, ratio, swa_cap
+    FastDiv split_div[3];
     int64_t num_pages, page_stride;
     const __nv_bfloat16 *cache;
     const float *sinks;
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Tokens are cut only where that shortens the longest CTA by more than
     // the partials and their join cost: otherwise CTA c takes token c (T <= G),
     // or the tokens that begin in its range.
-    const bool direct = T <= G && maxc <= U / G + kCutAbove;
+    const bool direct = T <= G && maxc <= static_cast<int>(A.split_div[0].div(U)) + kCutAbove;
     const bool snap = direct || (T > G && maxc <= kCutAbove);
     // few CTAs at work: 2 or 4 of them share a range, each with all of its
     // logits and weights and its share of the 512 columns
@@ -352,8 +353,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ndt = 4 >> dlog;                                    // 128-column tiles of this CTA
     const int dt0 = (static_cast<int>(blockIdx.x) & (dparts - 1)) * ndt;
     // range k begins at unit floor(k U / nsplit)
-    const int uq = U / nsplit, ur = U - uq * nsplit;
-    auto begin = [&](int k) { return k * uq + k * ur / nsplit; };
+    const bool full_split = nsplit == G >> dlog;                  // (otherwise a unit a range)
+    const FastDiv &sdiv = A.split_div[dlog];
+    const int uq = full_split ? static_cast<int>(sdiv.div(U)) : 1, ur = U - uq * nsplit;
+    auto begin = [&](int k) { return k * uq + (full_split ? static_cast<int>(sdiv.div(k * ur)) : 0); };
     int ua = 0, ub = split < T ? 1 : 0;
     if (!direct) {
         ua = split < nsplit ? begin(split) : U;
@@ -1236,6 +1239,7 @@ cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L
     A.part_o = reinterpret_cast<float4 *>(wb + w.o);
     A.status = status;
     const int ctas = (lc.sm_count < kMaxCtas ? lc.sm_count : kMaxCtas) / groups;
+    for (int i = 0; i < 3; ++i) A.split_div[i] = FastDiv(ctas >> i);
     cudaError_t e;
     if (A.bf16_out) {
         e = prepare_kernel<paged_attention_kernel<1>>(smem_bytes<1>());
