@@ -8,15 +8,18 @@
 // token's chunks for itself (the lengths are on the device only), takes an
 // equal range of them, and walks it as segments, one per token, through one
 // pipeline that does not drain between tokens:
-//   warps 0, 6..8  fetch a chunk's rows, 16 each: a group of 8 rows that lies
-//                  in one page is one TMA box (64 columns x 8 rows x 8 column
-//                  groups: 8 KiB whatever the page size), other groups
-//                  (page ends, the last rows, the window) go row by row with
-//                  16-byte cp.async, rows that do not exist as zeros
-//   warp 1         Q of the next segment;  S = Q . rows^T  (M = 64 heads,
-//                  N = 64 rows, K = 512), one chunk ahead of
-//   warp 9         O^T += rows^T . P^T  (M = 128 columns a tile, N = 64 heads)
-//   warps 2..5     softmax with a lazily raised maximum; a segment's epilogue
+//   warps 0..3    fetch a chunk's rows, 16 each: a group of 8 rows that lies
+//                 in one page is one TMA box (64 columns x 8 rows x 8 column
+//                 groups: 8 KiB whatever the page size), other groups (page
+//                 ends, the last rows, the window) go row by row with 16-byte
+//                 cp.async, rows that do not exist as zeros
+//   warps 4..7    softmax with a lazily raised maximum
+//   warps 8..11   warp 8: Q of the next segment; S = Q . rows^T (M = 64 heads,
+//                 N = 64 rows, K = 512), one chunk ahead of warp 9: O^T +=
+//                 rows^T . P^T (M = 128 columns a tile, N = 64 heads); all
+//                 four: a segment's epilogue, tile by tile, while the next
+//                 segment's rows, logits and weights are on their way (its
+//                 first O^T product takes each tile as it is drained)
 // A group's 8 KiB hold 8 column groups of 8 rows x 128 bytes (the swizzle
 // atom), so the same bytes are the K-major operand of S (row groups 8 KiB
 // apart) and the MN-major operand of O^T (column groups 1 KiB apart, row
@@ -37,8 +40,8 @@
 namespace csa {
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int kSmThreads = 128;                 // warps 2..5
+constexpr int kThreads = 384;
+constexpr int kSmThreads = 128;                 // warps 4..7; the epilogue's 8..11
 constexpr int kBarSm = 1;
 constexpr int kHG = 64;                         // heads per CTA
 constexpr int kChunk = 64;
@@ -92,13 +95,15 @@ struct Smem {
     uint64_t q_full, q_free;
     uint64_t full[kStages], empty[kStages][4];   // a stage is released 16 rows at a time
     uint64_t sfull[2], sfree[2];
-    uint64_t pfull, pfree, ofree;
+    uint64_t pfull, pfree;
+    uint64_t stretch[2], stretch_free[2];   // the factors of a stretch are written, used
+    uint64_t ofree[4];           // a tile of O^T is drained
     uint32_t tmem_holder;
     uint32_t maskw[kStages][4];
     uint32_t flag[2][4];
     float alpha[kHG];
-    alignas(16) float fin[kHG];
-    alignas(16) float flush[kHG];
+    alignas(16) float fin[2][kHG];     // of a stretch: factors of the output,
+    alignas(16) float flush[2][kHG];   // and of the partial so far
     int32_t nrec, more;
     int32_t t0, s0;
     int2 wsum[kThreads / 32];    // cost, most chunks of a token
@@ -285,12 +290,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&S.pfull, kSmThreads);
         mbar_init(&S.pfree, 1);
-        mbar_init(&S.ofree, kSmThreads);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.stretch[i], kSmThreads);
+            mbar_init(&S.stretch_free[i], kSmThreads);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&S.ofree[i], kSmThreads);
         mbar_fence_init();
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_rows);
     }
-    if (warp == 1) {
+    if (warp == 8) {
         tmem_alloc(&S.tmem_holder, kTmemCols);
         tmem_relinquish();
     }
@@ -495,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n_fetch = 0;                // chunks fetched
     uint32_t nq = 0, np = 0;             // chunks whose S / O^T product was issued
     uint32_t n_ql = 0;                   // Q loads issued
-    uint32_t n_of = 0;                   // sub-segments begun (O^T from zero)
-    uint32_t n_sm = 0;                   // chunks through the softmax
+    uint32_t n_sm = 0;                   // chunks through the softmax; whose O^T product was issued
+    uint32_t n_ep = 0;                   // stretches through the softmax, the epilogue
 
     for (;;) {
         __syncthreads();
@@ -506,31 +515,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool more = S.more != 0;
         if (nrec == 0) break;
 
-        if (warp == 1) {
-            // -------------------------------------------- S = Q . rows^T
-            // The whole warp keeps step and one elected thread issues: behind
-            // elect.sync the descriptors stay in uniform registers (a 64 x 64 x 16
-            // instruction every 33 cycles; behind `lane == 0`, every 54).
+        if (warp >= 8) {
+            // -------------------------------------------- products, epilogue
+            // Step j: warp 8 issues S of chunk j, warp 9 O^T of chunk j - 1, and
+            // all four drain O^T where that chunk ends a stretch.  A whole
+            // warp keeps step and one elected thread issues: behind elect.sync the
+            // descriptors stay in uniform registers (a 64 x 64 x 16 instruction
+            // every 33 cycles; behind `lane == 0`, every 54).
             constexpr uint32_t id_qk = idesc_bf16<kHG, kChunk, false>();
+            constexpr uint32_t id_pv = idesc_bf16<128, kHG, true>();
             const uint64_t q_desc = sw128_desc(smem_addr(sQ), 16, 1024);
             const uint64_t r_desc = sw128_desc(smem_addr(sRows), 16, kGroupBytes);
-            for (int i = 0; i < nrec; ++i) {
-                const int nch = S.rec[i].c1 - S.rec[i].c0;
-                if (nch <= 0) continue;
-                // the last product of the segment before is done with the buffer
-                if (n_ql > 0) mbar_wait(&S.q_free, (n_ql - 1) & 1u, A.status);
-                __syncwarp();
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&S.q_full, kQBytes);
-                    tma_load_4d(sQ, &tm_q, 0, h0, 0, S.rec[i].t, &S.q_full, policy_evict_normal());
+            const uint64_t a_desc = sw128_desc(smem_addr(sRows) + 2 * dt0 * 1024, 1024, kGroupBytes);
+            const uint64_t p_desc = sw128_desc(smem_addr(sP), 16, 1024);
+            const int dl = (warp & 3) * 32 + lane;   // column of a tile
+            const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+            const int hmax = min(kHG, H - h0);
+            // 16 rows at a time, each 16 rows' slice of the stage released when its
+            // products are done
+            auto pv = [&](auto ntile, uint64_t ad, int st) {
+#pragma unroll
+                for (int ks = 0; ks < kChunk / 16; ++ks) {
+#pragma unroll
+                    for (int dd = 0; dd < ntile; ++dd) {
+                        const uint64_t av = ad + off(2 * dd * 1024 + ks * 2 * kGroupBytes);
+                        const uint32_t d = tmem + kOCol + dd * kHG;
+                        umma_bf16(d, av, p_desc + off(ks * 32), id_pv, 1u);
+                        if (kTerms == 2) umma_bf16(d, av, p_desc + off(kPBytes + ks * 32), id_pv, 1u);
+                    }
+                    umma_commit(&S.empty[st][ks]);
                 }
-                __syncwarp();
-                mbar_wait(&S.q_full, n_ql & 1u, A.status);
-                ++n_ql;
-                for (int k = 0; k < nch; ++k, ++nq) {
+                umma_commit(&S.pfree);
+            };
+            int i = 0, k = 0, nch = 0, every = 1, z = 0;     // chunk j: k of segment i, z of a stretch
+            auto settle = [&]() {
+                while (i < nrec) {
+                    nch = S.rec[i].c1 - S.rec[i].c0;
+                    if (nch > 0) break;
+                    ++i;
+                }
+                k = z = 0;
+                if (i < nrec) every = flush_every<kFlush>(nch);
+            };
+            settle();
+            int bi = -1, bk = 0, bz = 0, bn = 0, be = 1;     // the chunk before it
+            for (;;) {
+                if (warp == 8 && i < nrec) {
+                    if (k == 0) {
+                        // the last product of the segment before is done with Q
+                        if (n_ql > 0) mbar_wait(&S.q_free, (n_ql - 1) & 1u, A.status);
+                        __syncwarp();
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&S.q_full, kQBytes);
+                            tma_load_4d(sQ, &tm_q, 0, h0, 0, S.rec[i].t, &S.q_full, policy_evict_normal());
+                        }
+                        __syncwarp();
+                        mbar_wait(&S.q_full, n_ql & 1u, A.status);
+                        ++n_ql;
+                    }
                     const int st = nq % kStages, sb = nq & 1u;
                     mbar_wait(&S.full[st], (nq / kStages) & 1u, A.status);
                     mbar_wait(&S.sfree[sb], ((nq >> 1) & 1u) ^ 1u, A.status);
+                    ++nq;
                     __syncwarp();
                     tc_fence_after();
                     if (elect_one()) {
@@ -547,56 +593,127 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                 }
-            }
-        } else if (warp == 9) {
-            // -------------------------------------------- O^T += rows^T . P^T
-            // 16 rows at a time, each 16 rows' slice of the stage released when
-            // its products are done
-            constexpr uint32_t id_pv = idesc_bf16<128, kHG, true>();
-            const uint64_t a_desc = sw128_desc(smem_addr(sRows) + 2 * dt0 * 1024, 1024, kGroupBytes);
-            const uint64_t p_desc = sw128_desc(smem_addr(sP), 16, 1024);
-            auto pv = [&](auto ntile, uint64_t ad, int st, bool zero) {
-#pragma unroll
-                for (int ks = 0; ks < kChunk / 16; ++ks) {
-#pragma unroll
-                    for (int dd = 0; dd < ntile; ++dd) {
-                        const uint64_t av = ad + off(2 * dd * 1024 + ks * 2 * kGroupBytes);
-                        const uint32_t d = tmem + kOCol + dd * kHG;
-                        umma_bf16(d, av, p_desc + off(ks * 32), id_pv, ks > 0 ? 1u : (zero ? 0u : 1u));
-                        if (kTerms == 2) umma_bf16(d, av, p_desc + off(kPBytes + ks * 32), id_pv, 1u);
-                    }
-                    umma_commit(&S.empty[st][ks]);
-                }
-                umma_commit(&S.pfree);
-            };
-            for (int i = 0; i < nrec; ++i) {
-                const int nch = S.rec[i].c1 - S.rec[i].c0, every = flush_every<kFlush>(nch);
-                for (int k = 0, z = 0; k < nch; ++k, ++np, z = z + 1 == every ? 0 : z + 1) {
+                if (warp == 9 && bi >= 0) {
                     const int st = np % kStages;
-                    const bool zero = z == 0;
                     mbar_wait(&S.pfull, np & 1u, A.status);
-                    if (zero) {
-                        if (n_of > 0) mbar_wait(&S.ofree, (n_of - 1) & 1u, A.status);
-                        ++n_of;
+                    ++np;
+                    const uint64_t ad = a_desc + off(st * kStageBytes);
+                    if (bz == 0) {
+                        // a stretch's first chunk, tile by tile as the stretch
+                        // before it leaves tensor memory
+                        for (int dd = 0; dd < ndt; ++dd) {
+                            if (n_ep > 0) mbar_wait(&S.ofree[dd], (n_ep - 1) & 1u, A.status);
+                            __syncwarp();
+                            tc_fence_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int ks = 0; ks < kChunk / 16; ++ks) {
+                                    const uint64_t av = ad + off(2 * dd * 1024 + ks * 2 * kGroupBytes);
+                                    const uint32_t d = tmem + kOCol + dd * kHG;
+                                    umma_bf16(d, av, p_desc + off(ks * 32), id_pv, ks > 0 ? 1u : 0u);
+                                    if (kTerms == 2) umma_bf16(d, av, p_desc + off(kPBytes + ks * 32), id_pv, 1u);
+                                }
+                                if (dd + 1 == ndt) {
+                                    for (int ks = 0; ks < 4; ++ks) umma_commit(&S.empty[st][ks]);
+                                    umma_commit(&S.pfree);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                    } else {
+                        __syncwarp();
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (ndt == 4) pv(std::integral_constant<int, 4>{}, ad, st);
+                            else if (ndt == 2) pv(std::integral_constant<int, 2>{}, ad, st);
+                            else pv(std::integral_constant<int, 1>{}, ad, st);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint64_t ad = a_desc + off(st * kStageBytes);
-                        if (ndt == 4) pv(std::integral_constant<int, 4>{}, ad, st, zero);
-                        else if (ndt == 2) pv(std::integral_constant<int, 2>{}, ad, st, zero);
-                        else pv(std::integral_constant<int, 1>{}, ad, st, zero);
+                }
+                if (bi >= 0) {
+                    ++n_sm;
+                    if (bk + 1 == bn || bz + 1 == be) {
+                        // ---- O^T into the partial, or the output
+                        const int t = S.rec[bi].t, flags = S.rec[bi].flags;
+                        const int64_t obase = (static_cast<int64_t>(t) * H + h0) * kHD;
+                        const int64_t pslot = static_cast<int64_t>(S.rec[bi].slot) * gridDim.y + hg;
+                        const int e = n_ep & 1u;
+                        const bool add = bk >= be;               // the partial holds earlier stretches
+                        const bool part = (flags & kRecPart) || bk + 1 < bn;
+                        mbar_wait(&S.stretch[e], (n_ep >> 1) & 1u, A.status);
+                        mbar_wait(&S.pfree, (n_sm - 1) & 1u, A.status);   // its last product
+                        ++n_ep;
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int dd = 0; dd < ndt; ++dd) {
+                            // one column per lane; a partial keeps four heads together,
+                            // so that a warp stores 512 contiguous bytes
+                            float4 *const pd = A.part_o + (pslot * 4 + dt0 + dd) * (16 * 128) + dl;
+#pragma unroll 1
+                            for (int hb = 0; hb < kHG; hb += 32) {
+                                if (hb >= hmax) break;
+                                uint32_t o[32];
+                                tmem_ld16_raw(tmem + lane_off + kOCol + dd * kHG + hb, *reinterpret_cast<uint32_t(*)[16]>(o));
+                                tmem_ld16_raw(tmem + lane_off + kOCol + dd * kHG + hb + 16,
+                                              *reinterpret_cast<uint32_t(*)[16]>(o + 16));
+                                float4 *const pq = pd + hb / 4 * 128;
+                                if (add) {
+                                    float4 old[8];
+#pragma unroll
+                                    for (int x = 0; x < 8; ++x) old[x] = pq[x * 128];
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int x = 0; x < 8; ++x) {
+                                        const float4 f = *reinterpret_cast<const float4 *>(S.flush[e] + hb + 4 * x);
+                                        o[4 * x] = __float_as_uint(fmaf(old[x].x, f.x, __uint_as_float(o[4 * x])));
+                                        o[4 * x + 1] = __float_as_uint(fmaf(old[x].y, f.y, __uint_as_float(o[4 * x + 1])));
+                                        o[4 * x + 2] = __float_as_uint(fmaf(old[x].z, f.z, __uint_as_float(o[4 * x + 2])));
+                                        o[4 * x + 3] = __float_as_uint(fmaf(old[x].w, f.w, __uint_as_float(o[4 * x + 3])));
+                                    }
+                                }
+                                tmem_wait_ld();
+                                if (hb + 32 >= hmax) {           // the tile is in registers
+                                    tc_fence_before();
+                                    mbar_arrive(&S.ofree[dd]);
+                                }
+                                if (part) {
+#pragma unroll
+                                    for (int x = 0; x < 8; ++x)
+                                        pq[x * 128] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                                                  __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+                                    continue;
+                                }
+                                const int64_t at = obase + hb * kHD + (dt0 + dd) * 128 + dl;
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) {
+                                    if (hb + x >= hmax) continue;
+                                    const float v = __uint_as_float(o[x]) * S.fin[e][hb + x];
+                                    if (kTerms == 1) static_cast<__nv_bfloat16 *>(A.out)[at + x * kHD] = __float2bfloat16(v);
+                                    else static_cast<float *>(A.out)[at + x * kHD] = v;
+                                }
+                            }
+                        }
+                        mbar_arrive(&S.stretch_free[e]);
+                        __syncwarp();
                     }
-                    __syncwarp();
+                }
+                if (i >= nrec) break;
+                bi = i, bk = k, bz = z, bn = nch, be = every;
+                z = z + 1 == every ? 0 : z + 1;
+                if (++k == nch) {
+                    ++i;
+                    settle();
                 }
             }
-        } else if (warp == 0 || warp >= 6) {
+        } else if (warp < 4) {
             // -------------------------------------------- row fetch
             // The warp walks the list's chunks, 16 rows of each.  Lane l (and
             // l + 16) looks after row l; three chunks ahead its page number is
             // on its way from the table, two ahead it is a row of the pool
             // whose bytes are on their way into L2, then it is copied.
-            const int li = warp == 0 ? 0 : warp - 5;
+            const int li = warp;
             const int rl = lane & 15;
             int bad = 0;
             struct Cursor {
@@ -736,29 +853,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             bad = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bad)));
             if (lane == 0 && lead) raise_status(A.status, bad);
         } else {
-            // -------------------------------------------- softmax, epilogue
+            // -------------------------------------------- softmax
             const int q = warp & 3;                  // TMEM lane quarter
             const int hl = q * 16 + (lane & 15);     // head of this lane (two lanes per head)
             const bool upper = lane >= 16;           // rows 32..63 of the chunk
             const bool hv = h0 + hl < H;
             const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
-            const int hmax = min(kHG, H - h0);
             for (int i = 0; i < nrec; ++i) {
-                const Rec r = S.rec[i];
-                const int nch = r.c1 - r.c0;
-                const int64_t obase = (static_cast<int64_t>(r.t) * H + h0) * kHD;
+                const int nch = S.rec[i].c1 - S.rec[i].c0;
                 if (nch <= 0) {
-                    if (r.flags & kRecZero) {
-                        for (int e = tid - 64; e < hmax * 128 * ndt; e += kSmThreads) {
-                            const int64_t at = obase + (e / (128 * ndt)) * kHD + dt0 * 128 + e % (128 * ndt);
-                            if (A.bf16_out) static_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16(0.f);
+                    if (S.rec[i].flags & kRecZero) {
+                        const int64_t obase = (static_cast<int64_t>(S.rec[i].t) * H + h0) * kHD;
+                        for (int x = tid - 128; x < min(kHG, H - h0) * 128 * ndt; x += kSmThreads) {
+                            const int64_t at = obase + (x / (128 * ndt)) * kHD + dt0 * 128 + x % (128 * ndt);
+                            if (kTerms == 1) static_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16(0.f);
                             else static_cast<float *>(A.out)[at] = 0.f;
                         }
                     }
                     continue;
                 }
+                const bool cut = S.rec[i].flags & kRecPart;
                 float m_ref = -INFINITY, l = 0.f, m_flush = -INFINITY;
-                const int64_t pslot = static_cast<int64_t>(r.slot) * gridDim.y + hg;
                 const int every = flush_every<kFlush>(nch);
                 for (int k = 0, z = 0; k < nch; ++k, ++n_sm, z = z + 1 == every ? 0 : z + 1) {
                     const int st = n_sm % kStages, sb = n_sm & 1u;
@@ -876,73 +991,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
                     const bool last = k + 1 == nch;
                     if (!last && z + 1 != every) continue;
-                    // ---- O^T into the partial, or the output
-                    const bool add = k >= every;        // the partial already holds earlier chunks
-                    const bool part = (r.flags & kRecPart) || !last;
+                    // the stretch's factors for the epilogue
+                    const int e = n_ep & 1u;
+                    mbar_wait(&S.stretch_free[e], ((n_ep >> 1) & 1u) ^ 1u, A.status);
+                    ++n_ep;
                     if (!upper) {
-                        S.flush[hl] = m_flush == -INFINITY ? 1.f : exp2f(m_flush - m_ref);
+                        S.flush[e][hl] = m_flush == -INFINITY ? 1.f : exp2f(m_flush - m_ref);
                         float f = 1.f;
-                        if (!part) {
-                            float z = l;
-                            if (A.sinks && hv && m_ref != -INFINITY) z += exp2f(A.sinks[h0 + hl] * kLog2e - m_ref);
-                            f = (z > 0.f && l > 0.f) ? 1.f / z : 0.f;
+                        if (last && !cut) {
+                            float zs = l;
+                            if (A.sinks && hv && m_ref != -INFINITY) zs += exp2f(A.sinks[h0 + hl] * kLog2e - m_ref);
+                            f = (zs > 0.f && l > 0.f) ? 1.f / zs : 0.f;
                         }
-                        S.fin[hl] = f;
+                        S.fin[e][hl] = f;
+                        if (last && cut && dt0 == 0)
+                            A.part_ml[(static_cast<int64_t>(S.rec[i].slot) * gridDim.y + hg) * kHG + hl] =
+                                make_float2(m_ref, l);
                     }
                     m_flush = m_ref;
-                    mbar_wait(&S.pfree, n_sm & 1u, A.status);
-                    named_bar_sync(kBarSm, kSmThreads);
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int dd = 0; dd < ndt; ++dd) {
-                        // one column per lane; a partial keeps four heads together, so
-                        // that a warp stores 512 contiguous bytes
-                        const int dl = q * 32 + lane;
-                        float4 *const pd = A.part_o + (pslot * 4 + dt0 + dd) * (16 * 128) + dl;
-#pragma unroll 1
-                        for (int hb = 0; hb < kHG; hb += 32) {
-                            if (hb >= hmax) break;
-                            uint32_t o[32];
-                            tmem_ld16_raw(tmem + lane_off + kOCol + dd * kHG + hb, *reinterpret_cast<uint32_t(*)[16]>(o));
-                            tmem_ld16_raw(tmem + lane_off + kOCol + dd * kHG + hb + 16,
-                                          *reinterpret_cast<uint32_t(*)[16]>(o + 16));
-                            float4 *const pq = pd + hb / 4 * 128;
-                            if (add) {
-                                float4 old[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) old[e] = pq[e * 128];
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const float4 f = *reinterpret_cast<const float4 *>(S.flush + hb + 4 * e);
-                                    o[4 * e] = __float_as_uint(fmaf(old[e].x, f.x, __uint_as_float(o[4 * e])));
-                                    o[4 * e + 1] = __float_as_uint(fmaf(old[e].y, f.y, __uint_as_float(o[4 * e + 1])));
-                                    o[4 * e + 2] = __float_as_uint(fmaf(old[e].z, f.z, __uint_as_float(o[4 * e + 2])));
-                                    o[4 * e + 3] = __float_as_uint(fmaf(old[e].w, f.w, __uint_as_float(o[4 * e + 3])));
-                                }
-                            }
-                            tmem_wait_ld();
-                            if (part) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    pq[e * 128] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                              __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-                                continue;
-                            }
-                            const int64_t at = obase + hb * kHD + (dt0 + dd) * 128 + dl;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                if (hb + e >= hmax) continue;
-                                const float v = __uint_as_float(o[e]) * S.fin[hb + e];
-                                if (kTerms == 1) static_cast<__nv_bfloat16 *>(A.out)[at + e * kHD] = __float2bfloat16(v);
-                                else static_cast<float *>(A.out)[at + e * kHD] = v;
-                            }
-                        }
-                    }
-                    tc_fence_before();
-                    mbar_arrive(&S.ofree);
-                    if (last && (r.flags & kRecPart) && !upper && dt0 == 0)
-                        A.part_ml[pslot * kHG + hl] = make_float2(m_ref, l);
+                    mbar_arrive(&S.stretch[e]);
                 }
             }
         }
@@ -956,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == 8) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
