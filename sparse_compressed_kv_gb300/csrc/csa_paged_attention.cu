@@ -777,7 +777,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&S.full[pending]);
                 pending = -1;
             };
-            const uint64_t pol = policy_evict_normal();
+            // rows are read once, or once by each of two groups of heads
+            const uint64_t pol = gridDim.y > 1 ? policy_evict_normal() : policy_evict_first();
             Cursor cur{0, S.rec[0].c0};
             settle(cur);
             Cursor far = cur;
