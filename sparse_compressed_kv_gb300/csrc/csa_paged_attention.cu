@@ -357,19 +357,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (direct) dlog = T * 4 <= G ? 2 : T * 2 <= G ? 1 : 0;
     else if (!snap && T <= G) dlog = U <= G / 4 ? 2 : U <= G ? 1 : 0;
     const int dparts = 1 << dlog;
-    const int nsplit = min(G >> dlog, U);
     const int split = static_cast<int>(blockIdx.x) >> dlog;
     const int ndt = 4 >> dlog;                                    // 128-column tiles of this CTA
     const int dt0 = (static_cast<int>(blockIdx.x) & (dparts - 1)) * ndt;
-    // range k begins at unit floor(k U / nsplit)
-    const bool full_split = nsplit == G >> dlog;                  // (otherwise a unit a range)
-    const FastDiv &sdiv = A.split_div[dlog];
-    const int uq = full_split ? static_cast<int>(sdiv.div(U)) : 1, ur = U - uq * nsplit;
-    auto begin = [&](int k) { return k * uq + (full_split ? static_cast<int>(sdiv.div(k * ur)) : 0); };
+    // equal ranges of `share` units, the last ones shorter or empty: as few parts
+    // as the longest range allows
+    const int share = static_cast<int>(A.split_div[dlog].div(U + (G >> dlog) - 1));
     int ua = 0, ub = split < T ? 1 : 0;
     if (!direct) {
-        ua = split < nsplit ? begin(split) : U;
-        ub = split < nsplit ? begin(split + 1) : U;
+        ua = min(split * share, U);
+        ub = min(ua + share, U);
     }
     const bool by_token = T <= G;
     const bool lead = hg == 0 && dt0 == 0;       // reports errors, writes the join's list
@@ -422,9 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!owner) r.slot = 2 * split;
             // the split that holds the token's last chunk
             if (owner && c > 0) {
-                const int u = s + c - 1;
-                int last = min(u / uq, nsplit - 1);      // at or behind it: ranges have uq or uq + 1 units
-                while (begin(last) > u) --last;
+                const int last = (s + c - 1) / share;
                 if (last > split) m = make_int2(r.slot, last - split + 1);
             }
             if (r.c1 - r.c0 < c) r.flags |= kRecPart;
