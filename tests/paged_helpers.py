@@ -151,11 +151,11 @@ class Paged:
         x = torch.arange(max(0, p - self.window + 1), p + 1) if self.window else j[:0]
         return torch.cat([held, self.swa_kv[b, x % self.swa_kv.shape[1]]]).double()
 
-    def reference(self, skip=lambda t: None):
+    def reference(self, skip=lambda t: None, tokens=None):
         """float64 [T, H, 512]; `skip(t)` names rows that token t does not see."""
         out = torch.full((len(self.tok_seq), self.heads, HD), float("nan"), dtype=torch.float64)
         for t, b in enumerate(self.tok_seq.tolist()):
-            if b < 0:
+            if b < 0 or (tokens is not None and t not in tokens):
                 continue
             rows, gone = self.rows_of(t), skip(t)
             if gone is not None:

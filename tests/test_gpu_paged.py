@@ -342,6 +342,111 @@ def test_attention_on_another_stream(cuda_device):
     assert status == 0 and torch.equal(a, b)
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_attention_random_shapes(cuda_device, seed):
+    # token counts around the number of CTAs, any page size, heads and window
+    rng = np.random.default_rng(100 + seed)
+    B = int(rng.choice([1, 2, 5, 40, 151, 152, 153, 170]))
+    new = int(rng.choice([1, 1, 2, 3]))
+    ratio = int(rng.choice([1, 4, 128]))
+    most = int(rng.choice([3, 70, 400, 1500])) if B < 100 else int(rng.choice([3, 70, 400]))
+    ctx = [int(rng.integers(0, most + 1)) * ratio + int(rng.integers(0, ratio)) for _ in range(B)]
+    p = H.Paged(seed, row_len=[(c + new) // ratio for c in ctx],
+                tokens=[(b, ctx[b] + i) for b in range(B) for i in range(new)], ratio=ratio,
+                page_rows=int(rng.choice([1, 2, 3, 8, 12, 16, 50, 64, 128])), gap=int(rng.choice([0, 8, 3])),
+                heads=int(rng.choice([1, 3, 8, 16, 33, 64, 100])) if B < 100 else 8,
+                window=int(rng.choice([0, 1, 20, 128])), sinks=bool(rng.integers(2)))
+    dtype = [F32, BF16][seed % 2]
+    got, status = p.run(cuda_device, dtype)
+    assert status == 0
+    tokens = sorted(set(rng.integers(0, B * new, 40).tolist()) | {0, B * new - 1})
+    H.check(got, p.reference(tokens=tokens), dtype, tokens)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_attention_thousands_of_tokens_and_one_long(cuda_device, dtype):
+    # so many short tokens that a CTA lists them in several turns, cut by a long one
+    long = 30000
+    tokens = [(0, 4 * (i % 13) + i % 4) for i in range(2500)] + [(1, 4 * long)] + \
+             [(2, i % 4) if i % 3 else (-1, -1) for i in range(2600)]
+    p = H.Paged(30, row_len=[12, long, 0], tokens=tokens, heads=8, page_rows=32, window=4, swa_cap=60)
+    p.swa_first_pos[1] = 4 * long - 50
+    got, status = p.run(cuda_device, dtype)
+    assert status == 0
+    check = [0, 1, 7, 51, 1234, 2499, 2500, 2502, 2503, 4000, 5098, 5099, 5100]
+    check = [t for t in check if tokens[t][0] >= 0]
+    H.check(got, p.reference(tokens=check), dtype, check)
+    pad = torch.tensor([b < 0 for b, _ in tokens])
+    assert (got.cpu()[pad] == 7).all() and not got.isnan().any()
+
+
+def test_attention_far_positions(cuda_device):
+    # positions past 2^32: their slots in the ring and their blocks
+    far = (1 << 33) + 12345
+    p = H.Paged(31, row_len=[90, 7], tokens=[(0, far), (1, far * 5)], heads=16, window=50)
+    got, status = p.run(cuda_device, F32)
+    assert status == 0
+    H.check(got, p.reference(), F32)
+
+
+def test_attention_shared_pages(cuda_device):
+    # a prefix that two requests share: the same pages in two rows of the table
+    p = H.Paged(32, row_len=[96, 96, 40], tokens=[(0, 400), (1, 390), (2, 170)], heads=32, page_rows=16)
+    p.table[1, :4] = p.table[0, :4]
+    p.table[2, :2] = p.table[0, 2:4]
+    got, status = p.run(cuda_device, BF16)
+    assert status == 0
+    H.check(got, p.reference(), BF16)
+
+
+def test_attention_two_streams_at_once(cuda_device):
+    dev = cuda_device
+    ps = [H.Paged(40 + i, row_len=[4000, 300 * i], tokens=[(0, 16000), (1, 1200 * i)], heads=64, page_rows=32)
+          for i in range(2)]
+    alone = [p.run(dev, F32)[0].clone() for p in ps]
+    args, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for p in ps:
+        layout = csa.PagedLayout(p.tok_seq.to(dev), p.tok_pos.to(dev), p.row_len.to(dev), p.table.to(dev),
+                                 32, p.swa_kv.to(dev), p.swa_first_pos.to(dev))
+        prm = csa.params(64, 1, 128, 4)
+        args.append((layout, prm, p.cache.to(dev), p.q.to(dev), torch.empty(2, 64, H.HD, device=dev),
+                     torch.zeros(1, dtype=torch.int32, device=dev), csa.paged_workspace(layout, prm)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, s in zip(args, streams):
+            csa.csa_paged_attention(*a, stream=s)
+    torch.cuda.synchronize()
+    for a, want in zip(args, alone):
+        assert int(a[5].item()) == 0 and torch.equal(a[4], want)
+
+
+def test_attention_replayed_with_other_lengths(cuda_device):
+    # captured once; lengths, tables and contents change between replays, from
+    # whole tokens a CTA to one token cut over all of them
+    dev = cuda_device
+    lens = [[3, 5], [6000, 0], [700, 900], [0, 0], [64, 6000]]
+    ps = [H.Paged(50 + i, row_len=n, tokens=[(0, 4 * n[0] + 1), (1, 4 * n[1] + 3)], heads=64, page_rows=32,
+                  max_pages=200, spare_pages=250 - sum(-(-x // 32) for x in n)) for i, n in enumerate(lens)]
+    bufs = [x.to(dev).clone() for x in (ps[0].tok_seq, ps[0].tok_pos, ps[0].row_len, ps[0].table,
+                                        ps[0].swa_kv, ps[0].swa_first_pos, ps[0].cache, ps[0].q)]
+    layout = csa.PagedLayout(*bufs[:4], 32, *bufs[4:6])
+    prm = csa.params(64, 1, 128, 4)
+    ws, out = csa.paged_workspace(layout, prm), torch.empty(2, 64, H.HD, device=dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    csa.csa_paged_attention(layout, prm, bufs[6], bufs[7], out, status, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        csa.csa_paged_attention(layout, prm, bufs[6], bufs[7], out, status, ws)
+    for p in ps:
+        for b, x in zip(bufs, (p.tok_seq, p.tok_pos, p.row_len, p.table, p.swa_kv, p.swa_first_pos, p.cache, p.q)):
+            b.copy_(x)
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        H.check(out, p.reference(), F32)
+
+
 # ---------------------------------------------------------------- as a serving loop
 
 class Server:
