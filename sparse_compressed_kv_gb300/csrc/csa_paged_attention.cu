@@ -1143,14 +1143,15 @@ __global__ void __launch_bounds__(128 * kDeepSub) join_deep_kernel(const PagedAr
             join_store<kBf16>(A, (static_cast<int64_t>(J.t) * A.H + h0 + i) * kHD + tile * 128 + col, o[i] * inv_z[i]);
 }
 
-// Few parts: a CTA takes 32 or 16 heads of a tile (gridDim.z of them share the
-// tile); a thread walks its half of the quads of its column, all parts of
-// two quads in flight.
+// Few parts: a CTA takes 16 heads of a tile (32 where tokens are many: fewer
+// waves of CTAs), a thread two quads of heads of its column at a time, the first
+// parts on their way before the weights are made.
 constexpr int kWidePer = 3;                      // parts in flight
+constexpr int kWideHeads = 32;                   // at most
 
 template <bool kBf16>
 __global__ void __launch_bounds__(256) join_wide_kernel(const PagedArgs A) {
-    __shared__ float4 wgt[kMaxCtas][kHG / 4];    // scaled by 1 / z
+    __shared__ float4 wgt[kMaxCtas][kWideHeads / 4];   // scaled by 1 / z
     pdl_wait();
     pdl_launch_dependents();
     const JoinEntry J = join_entry(A);
@@ -1158,41 +1159,53 @@ __global__ void __launch_bounds__(256) join_wide_kernel(const PagedArgs A) {
     if (ns <= 0) return;
     const int tid = threadIdx.x, col = tid & 127, half = tid >> 7;
     const int tile = blockIdx.y & 3, hg = blockIdx.y >> 2, groups = static_cast<int>(gridDim.y) >> 2;
-    const int h0 = hg * kHG, heads = min(kHG, A.H - h0);
-    const int quads = 16 / static_cast<int>(gridDim.z), q0 = quads * static_cast<int>(blockIdx.z);
-    if (4 * q0 >= heads) return;
-    if (tid >= 4 * q0 && tid < 4 * (q0 + quads)) {
-        const float2 *const ml = A.part_ml + hg * kHG + tid;
+    const int most = kHG / static_cast<int>(gridDim.z);
+    const int hb = most * static_cast<int>(blockIdx.z), h0 = hg * kHG + hb;   // first head
+    if (h0 >= A.H) return;
+    const int heads = min(most, A.H - h0);
+    const float4 *const po = A.part_o + tile * (16 * 128) + hb / 4 * 128 + col;
+    float4 v[kWidePer][2];
+    auto load = [&](int k0, int qd) {                    // quads qd, qd + 1
+#pragma unroll
+        for (int k = 0; k < kWidePer; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (k0 + k < ns) v[k][e] = __ldcg(po + (J.slot(k0 + k) * groups + hg) * (4 * 16 * 128) + (qd + e) * 128);
+    };
+    load(0, 2 * half);
+    if (tid < most) {
+        const float2 *const ml = A.part_ml + hg * kHG + hb + tid;
         const float sink = A.sinks && tid < heads ? A.sinks[h0 + tid] * kLog2e : -INFINITY;
-        float M = -INFINITY;
-#pragma unroll 4
-        for (int k = 0; k < ns; ++k) M = fmaxf(M, __ldcg(ml + J.slot(k) * groups * kHG).x);
+        constexpr int kNear = 6;                 // parts kept in registers
+        float2 x[kNear];
+#pragma unroll
+        for (int k = 0; k < kNear; ++k)
+            x[k] = k < ns ? __ldcg(ml + J.slot(k) * groups * kHG) : make_float2(-INFINITY, 0.f);
+        float M = x[0].x;
+#pragma unroll
+        for (int k = 1; k < kNear; ++k) M = fmaxf(M, x[k].x);
+        for (int k = kNear; k < ns; ++k) M = fmaxf(M, __ldcg(ml + J.slot(k) * groups * kHG).x);
         const float Mall = fmaxf(M, sink);
         float z = M != -INFINITY && sink != -INFINITY ? exp2f(sink - Mall) : 0.f;
-#pragma unroll 4
-        for (int k = 0; k < ns; ++k) {
-            const float2 x = __ldcg(ml + J.slot(k) * groups * kHG);
-            const float w = x.x == -INFINITY ? 0.f : exp2f(x.x - Mall);
+        auto put = [&](int k, float2 y) {
+            const float w = y.x == -INFINITY ? 0.f : exp2f(y.x - Mall);
             reinterpret_cast<float *>(wgt[k])[tid] = w;
-            z += w * x.y;
-        }
+            z += w * y.y;
+        };
+#pragma unroll
+        for (int k = 0; k < kNear; ++k)
+            if (k < ns) put(k, x[k]);
+        for (int k = kNear; k < ns; ++k) put(k, __ldcg(ml + J.slot(k) * groups * kHG));
         const float f = M != -INFINITY && z > 0.f ? 1.f / z : 0.f;
         for (int k = 0; k < ns; ++k) reinterpret_cast<float *>(wgt[k])[tid] *= f;
     }
     __syncthreads();
-    const float4 *const po = A.part_o + tile * (16 * 128) + col;
     const int64_t to = (static_cast<int64_t>(J.t) * A.H + h0) * kHD + tile * 128 + col;
 #pragma unroll 1
-    for (int qd = q0 + half * quads / 2; qd < q0 + (half + 1) * quads / 2; qd += 2) {
-        if (4 * qd >= heads) break;
+    for (int qd = 2 * half; 4 * qd < heads; qd += 4) {
         float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
         for (int k0 = 0; k0 < ns; k0 += kWidePer) {
-            float4 v[kWidePer][2];
-#pragma unroll
-            for (int k = 0; k < kWidePer; ++k)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (k0 + k < ns) v[k][e] = __ldcg(po + (J.slot(k0 + k) * groups + hg) * (4 * 16 * 128) + (qd + e) * 128);
+            if (k0 > 0 || qd >= 4) load(k0, qd);
 #pragma unroll
             for (int k = 0; k < kWidePer; ++k) {
                 if (k0 + k >= ns) break;
@@ -1208,11 +1221,12 @@ __global__ void __launch_bounds__(256) join_wide_kernel(const PagedArgs A) {
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int h = 4 * (qd + e);
             const float o[4] = {acc[e].x, acc[e].y, acc[e].z, acc[e].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (h + i < heads) join_store<kBf16>(A, to + static_cast<int64_t>(h + i) * kHD, o[i]);
+            for (int i = 0; i < 4; ++i) {
+                const int h = 4 * (qd + e) + i;
+                if (h < heads) join_store<kBf16>(A, to + static_cast<int64_t>(h) * kHD, o[i]);
+            }
         }
     }
 }
@@ -1227,7 +1241,7 @@ template <bool kBf16>
 cudaError_t launch_join(const Launch &lc, const PagedArgs &A, int entries, int groups) {
     if (entries == 1) return launch_one_join<join_deep_kernel<8, kBf16>>(lc, A, dim3(1, groups * 64), 1024);
     if (entries <= 12) return launch_one_join<join_deep_kernel<4, kBf16>>(lc, A, dim3(entries, groups * 64), 512);
-    const int share = entries * groups >= 64 ? 2 : 4;
+    const int share = entries * groups >= 96 ? kHG / kWideHeads : 2 * kHG / kWideHeads;
     return launch_one_join<join_wide_kernel<kBf16>>(lc, A, dim3(entries, groups * 4, share), 256);
 }
 
