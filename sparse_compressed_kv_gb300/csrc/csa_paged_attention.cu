@@ -680,6 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                   __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
                                     continue;
                                 }
+                                // (one column a lane: four a lane after an exchange among
+                                // lanes store wider, but cost the softmax its issue slots)
                                 const int64_t at = obase + hb * kHD + (dt0 + dd) * 128 + dl;
 #pragma unroll
                                 for (int x = 0; x < 32; ++x) {
@@ -1052,24 +1054,26 @@ __device__ __forceinline__ void join_store(const PagedArgs &A, int64_t at, float
     else static_cast<float *>(A.out)[at] = x;
 }
 
-// Many parts: a CTA takes four heads of one 128-column tile; eight (one token)
-// or four threads share a column's parts, eight loads of four heads each in
-// flight (issued before the weights are known), and meet in shared memory in
-// order.
+// Many parts: a CTA takes four heads of kCols columns; kDeepSub threads share a
+// column's parts, eight loads of four heads each in flight (issued before the
+// weights are known), and meet in shared memory in order.  One token: 32
+// columns, so that every SM reads; a few: a whole 128-column tile.
 constexpr int kDeepPer = 8;
 
-template <int kDeepSub, bool kBf16>
-__global__ void __launch_bounds__(128 * kDeepSub) join_deep_kernel(const PagedArgs A) {
+template <int kDeepSub, int kCols, bool kBf16>
+__global__ void __launch_bounds__(kCols * kDeepSub) join_deep_kernel(const PagedArgs A) {
     __shared__ float wgt[4][kMaxCtas];
     __shared__ float inv_z[4];
-    __shared__ float4 red[(kDeepSub - 1) * 128];
+    __shared__ float4 red[(kDeepSub - 1) * kCols];
     pdl_wait();
     pdl_launch_dependents();
     const JoinEntry J = join_entry(A);
     const int ns = J.ns;
     if (ns <= 0) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col = tid & 127, sub = tid >> 7;
+    static_assert(kCols * kDeepSub >= 128, "four warps make the weights");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = tid / kCols;
     const int quad = blockIdx.y & 15, tile = blockIdx.y >> 4 & 3, hg = blockIdx.y >> 6;
+    const int col = static_cast<int>(blockIdx.z) * kCols + tid % kCols;      // of the tile
     const int groups = static_cast<int>(gridDim.y) >> 6, h0 = hg * kHG + 4 * quad;
     if (h0 >= A.H) return;
     const float4 *const po = A.part_o + tile * (16 * 128) + quad * 128 + col;
@@ -1126,11 +1130,11 @@ __global__ void __launch_bounds__(128 * kDeepSub) join_deep_kernel(const PagedAr
             acc.w = fmaf(wgt[3][p], v[k].w, acc.w);
         }
     }
-    if (sub > 0) red[(sub - 1) * 128 + col] = acc;
+    if (sub > 0) red[(sub - 1) * kCols + tid % kCols] = acc;
     __syncthreads();
     if (sub > 0) return;
     for (int j = 0; j + 1 < kDeepSub; ++j) {
-        const float4 u = red[j * 128 + col];
+        const float4 u = red[j * kCols + tid];
         acc.x += u.x;
         acc.y += u.y;
         acc.z += u.z;
@@ -1239,8 +1243,8 @@ cudaError_t launch_one_join(const Launch &lc, const PagedArgs &A, dim3 grid, int
 
 template <bool kBf16>
 cudaError_t launch_join(const Launch &lc, const PagedArgs &A, int entries, int groups) {
-    if (entries == 1) return launch_one_join<join_deep_kernel<8, kBf16>>(lc, A, dim3(1, groups * 64), 1024);
-    if (entries <= 12) return launch_one_join<join_deep_kernel<4, kBf16>>(lc, A, dim3(entries, groups * 64), 512);
+    if (entries == 1) return launch_one_join<join_deep_kernel<16, 32, kBf16>>(lc, A, dim3(1, groups * 64, 4), 512);
+    if (entries <= 12) return launch_one_join<join_deep_kernel<4, 128, kBf16>>(lc, A, dim3(entries, groups * 64), 512);
     const int share = entries * groups >= 96 ? kHG / kWideHeads : 2 * kHG / kWideHeads;
     return launch_one_join<join_wide_kernel<kBf16>>(lc, A, dim3(entries, groups * 4, share), 256);
 }
