@@ -236,9 +236,18 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
             P.table[static_cast<int64_t>(b) * P.max_pages + pg] = *ring(h0, i);
         }
     }
-    for (uint32_t i = first; i < total.rel; i += step) {
-        const int b = plan_find<&Sums::rel>(off, B, i);
-        *ring(t0, i) = P.table[static_cast<int64_t>(b) * P.max_pages + (i - off[b].rel)];
+    for (uint32_t i0 = first; i0 < total.rel; i0 += kPlanBatch * step) {
+        int32_t page[kPlanBatch];
+#pragma unroll
+        for (int k = 0; k < kPlanBatch; ++k) {
+            const uint32_t i = i0 + k * step;
+            if (i >= total.rel) break;
+            const int b = plan_find<&Sums::rel>(off, B, i);
+            page[k] = P.table[static_cast<int64_t>(b) * P.max_pages + (i - off[b].rel)];
+        }
+#pragma unroll
+        for (int k = 0; k < kPlanBatch; ++k)
+            if (i0 + k * step < total.rel) *ring(t0, i0 + k * step) = page[k];
     }
     for (int64_t i = static_cast<int64_t>(total.tok) + first; i < P.tok_cap; i += step) {
         P.tok_seq[i] = -1;
@@ -375,10 +384,14 @@ extern "C" csa_status_t csa_page_plan(const csa_page_plan_t *plan, int32_t *dev_
     if (st != CSA_OK) return st;
     if (prepare_kernel<page_plan_kernel>(kPlanMaxSeqs * sizeof(Sums)) != cudaSuccess) return CSA_ERR_CUDA;
     const size_t smem = static_cast<size_t>(P.num_seqs) * sizeof(Sums);
-    // a request or two output entries a thread, one CTA an SM at most
+    // a request or two output entries a thread, one CTA an SM at most; and some
+    // for the pages that requests may give back (how many is on the device)
     int64_t items = P.tok_cap > P.row_cap ? P.tok_cap : P.row_cap;
     items = (items + 1) / 2 > P.num_seqs ? (items + 1) / 2 : P.num_seqs;
     int64_t grid = (items + kPlanThreads - 1) / kPlanThreads;
+    const int64_t held = static_cast<int64_t>(P.num_seqs) * P.max_pages;
+    const int64_t back = (held < P.num_pages ? held : P.num_pages) / (16 * kPlanThreads);
+    if (grid < back) grid = back;
     if (grid > sms) grid = sms;
     const PlanArgs A{P, FastDiv(P.ratio), FastDiv(P.page_rows), FastDiv(P.swa_cap),
                      FastDiv(static_cast<uint32_t>(P.num_pages))};
