@@ -95,7 +95,7 @@ struct Smem {
     uint64_t q_full, q_free;
     uint64_t full[kStages], empty[kStages][4];   // a stage is released 16 rows at a time
     uint64_t sfull[2], sfree[2];
-    uint64_t pfull, pfree;
+    uint64_t pfull[2], pfree;    // P's rows 0..15 and 32..47, then 16..31 and 48..63
     uint64_t stretch[2], stretch_free[2];   // the factors of a stretch are written, used
     uint64_t ofree[4];           // a tile of O^T is drained
     uint32_t tmem_holder;
@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&S.sfull[i], 1);
             mbar_init(&S.sfree[i], kSmThreads);
         }
-        mbar_init(&S.pfull, kSmThreads);
+        mbar_init(&S.pfull[0], kSmThreads);
+        mbar_init(&S.pfull[1], kSmThreads);
         mbar_init(&S.pfree, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.stretch[i], kSmThreads);
@@ -526,11 +527,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int dl = (warp & 3) * 32 + lane;   // column of a tile
             const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
             const int hmax = min(kHG, H - h0);
-            // 16 rows at a time, each 16 rows' slice of the stage released when its
-            // products are done
-            auto pv = [&](auto ntile, uint64_t ad, int st) {
+            // two slices of 16 rows, each released when its products are done
+            auto pv = [&](auto ntile, uint64_t ad, int st, int k0) {
 #pragma unroll
-                for (int ks = 0; ks < kChunk / 16; ++ks) {
+                for (int ks = k0; ks < kChunk / 16; ks += 2) {
 #pragma unroll
                     for (int dd = 0; dd < ntile; ++dd) {
                         const uint64_t av = ad + off(2 * dd * 1024 + ks * 2 * kGroupBytes);
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     umma_commit(&S.empty[st][ks]);
                 }
-                umma_commit(&S.pfree);
+                if (k0 == 1) umma_commit(&S.pfree);
             };
             int i = 0, k = 0, nch = 0, every = 1, z = 0;     // chunk j: k of segment i, z of a stretch
             auto settle = [&]() {
@@ -590,10 +590,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (warp == 9 && bi >= 0) {
                     const int st = np % kStages;
-                    mbar_wait(&S.pfull, np & 1u, A.status);
+                    const uint32_t pp = np & 1u;
+                    mbar_wait(&S.pfull[0], pp, A.status);
                     ++np;
                     const uint64_t ad = a_desc + off(st * kStageBytes);
                     if (bz == 0) {
+                        mbar_wait(&S.pfull[1], pp, A.status);
                         // a stretch's first chunk, tile by tile as the stretch
                         // before it leaves tensor memory
                         for (int dd = 0; dd < ndt; ++dd) {
@@ -616,14 +618,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __syncwarp();
                         }
                     } else {
-                        __syncwarp();
-                        tc_fence_after();
-                        if (elect_one()) {
-                            if (ndt == 4) pv(std::integral_constant<int, 4>{}, ad, st);
-                            else if (ndt == 2) pv(std::integral_constant<int, 2>{}, ad, st);
-                            else pv(std::integral_constant<int, 1>{}, ad, st);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            if (half == 1) mbar_wait(&S.pfull[1], pp, A.status);
+                            __syncwarp();
+                            tc_fence_after();
+                            if (elect_one()) {
+                                if (ndt == 4) pv(std::integral_constant<int, 4>{}, ad, st, half);
+                                else if (ndt == 2) pv(std::integral_constant<int, 2>{}, ad, st, half);
+                                else pv(std::integral_constant<int, 1>{}, ad, st, half);
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
                     }
                 }
                 if (bi >= 0) {
@@ -953,39 +959,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // hi + lo with lo the rounded rest
                     const float mr = m_ref == -INFINITY ? 0.f : m_ref;
                     float sq[2] = {0.f, 0.f};
-                    uint32_t phi[16], plo[kTerms == 2 ? 16 : 1];
+                    uint8_t *const pr = sP + hl * 128;
+                    // half of the lane's rows at a time: the first products
+                    // start under the second half's exponentials
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float p0 = fast_exp2(fmaf(x[j], xs, -mr));
-                        const float p1 = fast_exp2(fmaf(x[j + 1], xs, -mr));
-                        const uint32_t hi = pack_bf16x2(p0, p1);
-                        const float g0 = __uint_as_float(hi << 16), g1 = __uint_as_float(hi & 0xFFFF0000u);
-                        phi[j >> 1] = hi;
-                        if (kTerms == 2) {
-                            sq[(j >> 1) & 1] += p0 + p1;
-                            plo[kTerms == 2 ? (j >> 1) : 0] = pack_bf16x2(p0 - g0, p1 - g1);
-                        } else {
-                            sq[(j >> 1) & 1] += g0 + g1;
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t phi[8], plo[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const int j = 16 * half + 2 * u;
+                            const float p0 = fast_exp2(fmaf(x[j], xs, -mr));
+                            const float p1 = fast_exp2(fmaf(x[j + 1], xs, -mr));
+                            const uint32_t hi = pack_bf16x2(p0, p1);
+                            const float g0 = __uint_as_float(hi << 16), g1 = __uint_as_float(hi & 0xFFFF0000u);
+                            phi[u] = hi;
+                            if (kTerms == 2) {
+                                sq[u & 1] += p0 + p1;
+                                plo[u] = pack_bf16x2(p0 - g0, p1 - g1);
+                            } else {
+                                sq[u & 1] += g0 + g1;
+                            }
                         }
-                    }
-                    const float sum = sq[0] + sq[1];
-                    l += sum + __shfl_xor_sync(0xffffffffu, sum, 16);
-                    if (n_sm > 0) mbar_wait(&S.pfree, (n_sm - 1) & 1u, A.status);
-                    {
-                        uint8_t *pr = sP + hl * 128;
+                        if (half == 0 && n_sm > 0) mbar_wait(&S.pfree, (n_sm - 1) & 1u, A.status);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t sw = static_cast<uint32_t>((((upper ? 4 : 0) + e) ^ (hl & 7)) << 4);
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t sw = static_cast<uint32_t>((((upper ? 4 : 0) + 2 * half + e) ^ (hl & 7)) << 4);
                             *reinterpret_cast<uint4 *>(pr + sw) =
                                 make_uint4(phi[4 * e], phi[4 * e + 1], phi[4 * e + 2], phi[4 * e + 3]);
                             if (kTerms == 2)
                                 *reinterpret_cast<uint4 *>(pr + kPBytes + sw) =
-                                    make_uint4(plo[(4 * e) % (kTerms == 2 ? 16 : 1)], plo[(4 * e + 1) % (kTerms == 2 ? 16 : 1)],
-                                               plo[(4 * e + 2) % (kTerms == 2 ? 16 : 1)], plo[(4 * e + 3) % (kTerms == 2 ? 16 : 1)]);
+                                    make_uint4(plo[4 * e], plo[4 * e + 1], plo[4 * e + 2], plo[4 * e + 3]);
                         }
+                        fence_proxy_async_smem();
+                        mbar_arrive(&S.pfull[half]);
                     }
-                    fence_proxy_async_smem();
-                    mbar_arrive(&S.pfull);
+                    const float sum = sq[0] + sq[1];
+                    l += sum + __shfl_xor_sync(0xffffffffu, sum, 16);
 
                     const bool last = k + 1 == nch;
                     if (!last && z + 1 != every) continue;
