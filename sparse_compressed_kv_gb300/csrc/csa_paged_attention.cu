@@ -28,8 +28,16 @@
 // A segment that is a whole token writes the output; the parts of a token cut
 // between CTAs go to the workspace as (O, m, l) and a second kernel joins
 // them.  The accumulator of tcgen05 drops bits below its last place, so
-// sums of thousands of rows drift; at least every kFlush chunks O^T is added, rounded,
-// into the CTA's own f32 partial and starts again from zero.
+// sums of thousands of rows drift; at least every kFlush chunks O^T is added,
+// rounded, into the CTA's own f32 partial and starts again from zero.
+//
+// Bound by: DRAM where a CTA has tens of chunks (2,950 cycles a chunk against
+// 2,865 at the copy rate: 32 ragged contexts, 545 MB, 104 us; one million
+// tokens at ratio 4, 269 MB, 60 us), with two terms of P the shared memory's
+// reads (384 KB a chunk: 3,070 of 3,250 cycles); by its latency chain where it
+// has one or two (8,192 rows 13.9 us, 256 rows 8.9 us, join included).  Two
+// stages of 64 rows are what fits beside Q; smaller chunks pay the
+// instructions' floor of 26 to 33 cycles more often.
 #include <math.h>
 
 #include <type_traits>
@@ -349,11 +357,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Tokens are cut only where that shortens the longest CTA by more than
     // the partials and their join cost: otherwise CTA c takes token c (T <= G),
-    // or the tokens that begin in its range.
+    // or the tokens that begin in its range.  (4 chunks: at 12, 150 tokens of
+    // 250 to 500 rows gain, 41.3 -> 32.6 us, but 64 of 512 to 1,024 rows lose,
+    // 31.2 -> 39.2, and one of 600, 9.2 -> 23.4.)
     const bool direct = T <= G && maxc <= static_cast<int>(A.split_div[0].div(U)) + kCutAbove;
     const bool snap = direct || (T > G && maxc <= kCutAbove);
     // few CTAs at work: 2 or 4 of them share a range, each with all of its
-    // logits and weights and its share of the 512 columns
+    // logits and weights and its share of the 512 columns: the last products
+    // and the partial (32 bytes a cycle and SM) are that much shorter
     int dlog = 0;
     if (direct) dlog = T * 4 <= G ? 2 : T * 2 <= G ? 1 : 0;
     else if (!snap && T <= G) dlog = U <= G / 4 ? 2 : U <= G ? 1 : 0;
@@ -640,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int64_t obase = (static_cast<int64_t>(t) * H + h0) * kHD;
                         const int64_t pslot = static_cast<int64_t>(S.rec[bi].slot) * gridDim.y + hg;
                         const int e = n_ep & 1u;
+                        (void)CSA_CHECK(S.rec[bi].slot < 2 * G && t < T, A.status);
                         const bool add = bk >= be;               // the partial holds earlier stretches
                         const bool part = (flags & kRecPart) || bk + 1 < bn;
                         mbar_wait(&S.stretch[e], (n_ep >> 1) & 1u, A.status);
@@ -757,6 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (e.in_page >= 0) {
                     if (e.page < 0 || e.page >= A.num_pages) bad |= CSA_DEV_BAD_INDEX;
                     else p.row = static_cast<int32_t>(e.page * A.page_stride) + e.in_page;
+                    if (!CSA_CHECK(p.row < A.total_rows, A.status)) p.row = -1;
                 }
                 const uint32_t bx = __ballot_sync(0xffffffffu, e.box);
                 p.box = (bx & 1u) | (bx >> 7 & 2u);

@@ -581,3 +581,21 @@ def test_serving_loop_matches_the_packed_path(cuda_device):
 def test_serving_loop_captured(cuda_device):
     # two captured steps that share a workspace, replayed in turn
     serve(cuda_device, captured=True)
+
+
+def test_paged_calls_under_the_checked_build(cuda_device):
+    """The library with internal bounds checks: a failed one sets a status bit,
+    and every test wants the status it expects."""
+    import os
+    import subprocess
+    import sys
+
+    from sparse_compressed_kv_gb300 import build as B
+
+    B.build(checks=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider",
+                        os.path.join("tests", "test_gpu_paged.py"), "-k",
+                        "test_plan or test_append or random_shapes or bad_pages or thousands or serving"],
+                       cwd=root, env=dict(os.environ, CSA_CHECKS="1"), capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and " passed" in r.stdout, (r.stdout + r.stderr)[-3000:]
