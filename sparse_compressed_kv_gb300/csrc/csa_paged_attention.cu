@@ -61,6 +61,15 @@ constexpr int kPBytes = kHG * kChunk * 2;       // one bf16 term of P: 8 KiB
 constexpr int kSCol = 0;                        // two S buffers of 64 columns
 constexpr int kOCol = 128;                      // O^T: 4 tiles x 64 heads
 constexpr uint32_t kTmemCols = 512;
+// With two terms of P, the first two tiles take both from one reading of the
+// rows (N = 128: hi's sums, then lo's) into 64 columns each; tensor memory has
+// room for no more.
+template <int kTerms>
+constexpr int kWide = kTerms == 2 ? 2 : 0;
+template <int kTerms>
+__device__ __forceinline__ constexpr uint32_t o_col(int dd) {
+    return kOCol + kHG * (dd + (dd < kWide<kTerms> ? dd : kWide<kTerms>));
+}
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleAbove = 8.f;            // log2 units
 constexpr int kMaxRec = 128;                    // segments a CTA lists at a time
@@ -530,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // descriptors stay in uniform registers (a 64 x 64 x 16 instruction
             // every 33 cycles; behind `lane == 0`, every 54).
             constexpr uint32_t id_qk = idesc_bf16<kHG, kChunk, false>();
-            constexpr uint32_t id_pv = idesc_bf16<128, kHG, true>();
+            constexpr uint32_t id_pv = idesc_bf16<128, kHG, true>(), id_wide = idesc_bf16<128, 2 * kHG, true>();
             const uint64_t q_desc = sw128_desc(smem_addr(sQ), 16, 1024);
             const uint64_t r_desc = sw128_desc(smem_addr(sRows), 16, kGroupBytes);
             const uint64_t a_desc = sw128_desc(smem_addr(sRows) + 2 * dt0 * 1024, 1024, kGroupBytes);
@@ -539,16 +548,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
             const int hmax = min(kHG, H - h0);
             // two slices of 16 rows, each released when its products are done
+            auto product = [&](int dd, int ks, uint64_t ad, uint32_t acc) {
+                const uint64_t av = ad + off(2 * dd * 1024 + ks * 2 * kGroupBytes);
+                const uint32_t d = tmem + o_col<kTerms>(dd);
+                if (dd < kWide<kTerms>) {
+                    umma_bf16(d, av, p_desc + off(ks * 32), id_wide, acc);
+                } else {
+                    umma_bf16(d, av, p_desc + off(ks * 32), id_pv, acc);
+                    if (kTerms == 2) umma_bf16(d, av, p_desc + off(kPBytes + ks * 32), id_pv, 1u);
+                }
+            };
             auto pv = [&](auto ntile, uint64_t ad, int st, int k0) {
 #pragma unroll
                 for (int ks = k0; ks < kChunk / 16; ks += 2) {
 #pragma unroll
-                    for (int dd = 0; dd < ntile; ++dd) {
-                        const uint64_t av = ad + off(2 * dd * 1024 + ks * 2 * kGroupBytes);
-                        const uint32_t d = tmem + kOCol + dd * kHG;
-                        umma_bf16(d, av, p_desc + off(ks * 32), id_pv, 1u);
-                        if (kTerms == 2) umma_bf16(d, av, p_desc + off(kPBytes + ks * 32), id_pv, 1u);
-                    }
+                    for (int dd = 0; dd < ntile; ++dd) product(dd, ks, ad, 1u);
                     umma_commit(&S.empty[st][ks]);
                 }
                 if (k0 == 1) umma_commit(&S.pfree);
@@ -615,12 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc_fence_after();
                             if (elect_one()) {
 #pragma unroll
-                                for (int ks = 0; ks < kChunk / 16; ++ks) {
-                                    const uint64_t av = ad + off(2 * dd * 1024 + ks * 2 * kGroupBytes);
-                                    const uint32_t d = tmem + kOCol + dd * kHG;
-                                    umma_bf16(d, av, p_desc + off(ks * 32), id_pv, ks > 0 ? 1u : 0u);
-                                    if (kTerms == 2) umma_bf16(d, av, p_desc + off(kPBytes + ks * 32), id_pv, 1u);
-                                }
+                                for (int ks = 0; ks < kChunk / 16; ++ks) product(dd, ks, ad, ks > 0 ? 1u : 0u);
                                 if (dd + 1 == ndt) {
                                     for (int ks = 0; ks < 4; ++ks) umma_commit(&S.empty[st][ks]);
                                     umma_commit(&S.pfree);
@@ -668,10 +677,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int hb = 0; hb < kHG; hb += 32) {
                                 if (hb >= hmax) break;
                                 uint32_t o[32];
-                                tmem_ld16_raw(tmem + lane_off + kOCol + dd * kHG + hb, *reinterpret_cast<uint32_t(*)[16]>(o));
-                                tmem_ld16_raw(tmem + lane_off + kOCol + dd * kHG + hb + 16,
-                                              *reinterpret_cast<uint32_t(*)[16]>(o + 16));
+                                const uint32_t oc = tmem + lane_off + o_col<kTerms>(dd) + hb;
+                                tmem_ld16_raw(oc, *reinterpret_cast<uint32_t(*)[16]>(o));
+                                tmem_ld16_raw(oc + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
                                 float4 *const pq = pd + hb / 4 * 128;
+                                if (dd < kWide<kTerms>) {
+#pragma unroll
+                                    for (int y = 0; y < 32; y += 16) {
+                                        uint32_t lo[16];
+                                        tmem_ld16_raw(oc + kHG + y, lo);
+                                        tmem_wait_ld();
+#pragma unroll
+                                        for (int x = 0; x < 16; ++x)
+                                            o[x + y] = __float_as_uint(__uint_as_float(o[x + y]) + __uint_as_float(lo[x]));
+                                    }
+                                }
                                 if (add) {
                                     float4 old[8];
 #pragma unroll
@@ -951,18 +971,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         named_bar_sync(kBarSm, kSmThreads);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int dd = 0; dd < ndt; ++dd)
-#pragma unroll 1
-                            for (int hb = 0; hb < 4; ++hb) {
-                                uint32_t o[16];
-                                const uint32_t ta2 = tmem + lane_off + kOCol + dd * kHG + hb * 16;
-                                tmem_ld16_raw(ta2, o);
-                                tmem_wait_ld();
+                        for (int x = 0; x < static_cast<int>(o_col<kTerms>(ndt) - kOCol); x += 16) {
+                            uint32_t o[16];
+                            const uint32_t ta2 = tmem + lane_off + kOCol + x;
+                            tmem_ld16_raw(ta2, o);
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * S.alpha[hb * 16 + e]);
-                                tmem_st16(ta2, o);
-                            }
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * S.alpha[x % kHG + e]);
+                            tmem_st16(ta2, o);
+                        }
                         tmem_wait_st();
                         tc_fence_before();
                         named_bar_sync(kBarSm, kSmThreads);
