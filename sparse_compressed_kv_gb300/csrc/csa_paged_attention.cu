@@ -774,8 +774,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------- row fetch
             // The warp walks the list's chunks, 16 rows of each.  Lane l (and
             // l + 16) looks after row l; three chunks ahead its page number is
-            // on its way from the table, two ahead it is a row of the pool
-            // whose bytes are on their way into L2, then it is copied.
+            // on its way from the table, two ahead it is a row of the pool (a box's
+            // bytes then set out into L2), then it is copied.
             const int li = warp;
             const int rl = lane & 15;
             int bad = 0;
@@ -821,15 +821,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const uint32_t bx = __ballot_sync(0xffffffffu, e.box);
                 p.box = (bx & 1u) | (bx >> 7 & 2u);
-                if (ahead && lane < 16 && p.row >= 0) {
-                    if (!(p.box >> (lane >> 3) & 1u))
-                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                                         A.cache + static_cast<int64_t>(p.row) * kHD),
-                                     "r"(kHD * 2)
-                                     : "memory");
-                    else if ((lane & 7) == 0)
-                        tma_prefetch_l2_3d(&tm_rows, 0, p.row, 0);
-                }
+                // (boxes only: prefetches of single rows hold up the copies, pages of two
+                // rows 136 -> 155 us by bulk prefetch, 142 by lines)
+                if (ahead && lane < 16 && (lane & 7) == 0 && p.row >= 0 && (p.box >> (lane >> 3) & 1u))
+                    tma_prefetch_l2_3d(&tm_rows, 0, p.row, 0);
                 return p;
             };
             int pending = -1;                          // stage whose cp.async rows are in flight
