@@ -3,19 +3,19 @@
 //   l_j = scale q_h . row_j,   out_h = sum_j softmax_j(l [, sink]) row_j.
 //
 // A token's row slots are its visible compressed rows, padded to a multiple of
-// 8, then its window rows; 64 slots are a chunk.  One kernel of one CTA per SM
+// 8, then its window rows; 48 slots are a chunk.  One kernel of one CTA per SM
 // (per 64 heads) divides the chunks of all tokens: each CTA counts every
 // token's chunks for itself (the lengths are on the device only), takes an
 // equal range of them, and walks it as segments, one per token, through one
 // pipeline that does not drain between tokens:
-//   warps 0..3    fetch a chunk's rows, 16 each: a group of 8 rows that lies
+//   warps 0..2    fetch a chunk's rows, 16 each: a group of 8 rows that lies
 //                 in one page is one TMA box (64 columns x 8 rows x 8 column
 //                 groups: 8 KiB whatever the page size), other groups (page
 //                 ends, the last rows, the window) go row by row with 16-byte
 //                 cp.async, rows that do not exist as zeros
 //   warps 4..7    softmax with a lazily raised maximum
 //   warps 8..11   warp 8: Q of the next segment; S = Q . rows^T (M = 64 heads,
-//                 N = 64 rows, K = 512), one chunk ahead of warp 9: O^T +=
+//                 N = 48 rows, K = 512), one chunk ahead of warp 9: O^T +=
 //                 rows^T . P^T (M = 128 columns a tile, N = 64 heads); all
 //                 four: a segment's epilogue, tile by tile, while the next
 //                 segment's rows, logits and weights are on their way (its
@@ -31,13 +31,18 @@
 // sums of thousands of rows drift; at least every kFlush chunks O^T is added,
 // rounded, into the CTA's own f32 partial and starts again from zero.
 //
-// Bound by: DRAM where a CTA has tens of chunks (2,950 cycles a chunk against
-// 2,865 at the copy rate: 32 ragged contexts, 545 MB, 104 us; one million
-// tokens at ratio 4, 269 MB, 60 us), with two terms of P the shared memory's
-// reads (384 KB a chunk: 3,070 of 3,250 cycles); by its latency chain where it
-// has one or two (8,192 rows 13.9 us, 256 rows 8.9 us, join included).  Two
-// stages of 64 rows are what fits beside Q; smaller chunks pay the
-// instructions' floor of 26 to 33 cycles more often.
+// Bound by: DRAM where a CTA has tens of chunks (32 ragged contexts, 545 MB,
+// 103 us; one million tokens at ratio 4, 269 MB, 58 us); with two terms of P
+// the products and the turn of a stage (2,070 cycles a chunk); by its latency
+// chain where a CTA has one or two (8,192 rows 14.8 us, 256 rows 9.1 us, join
+// included).  A stage's turn (released, copied, logits, weights, products) takes
+// 5,500 cycles, so the stages set the pace: three of 48 rows instead of two of
+// 64, what fits beside Q, take 2,760 cycles per 64 rows instead of 3,780 with
+// two terms and 2,840 instead of 3,130 with one (128-head drafts 82.5 -> 76.7
+// us, 256 tokens of 1K rows 72.6 -> 68.1; one token of 8,192 rows, two rounds
+// before and three now, 14.0 -> 14.8), and need no prefetch into L2 (with it: 105
+// instead of 103 us).  Chunks of 32 rows would pay the instructions' floor of 26 to
+// 33 cycles twice as often.
 #include <math.h>
 
 #include <type_traits>
@@ -52,13 +57,14 @@ constexpr int kThreads = 384;
 constexpr int kSmThreads = 128;                 // warps 4..7; the epilogue's 8..11
 constexpr int kBarSm = 1;
 constexpr int kHG = 64;                         // heads per CTA
-constexpr int kChunk = 64;
+constexpr int kChunk = 48;
+constexpr int kSlices = kChunk / 16;            // of 16 rows: one K step of O^T each
 constexpr int kQBytes = kHG * kHD * 2;          // 64 KiB
 constexpr int kGroupBytes = 8 * kHD * 2;        // 8 rows: 8 KiB
-constexpr int kStageBytes = 8 * kGroupBytes;    // 64 KiB
-constexpr int kStages = 2;
-constexpr int kPBytes = kHG * kChunk * 2;       // one bf16 term of P: 8 KiB
-constexpr int kOutBytes = 2048;                 // of an epilogue warp: 32 columns x 32 heads in bf16
+constexpr int kStageBytes = kChunk / 8 * kGroupBytes;   // 48 KiB
+constexpr int kStages = 3;
+constexpr int kPBytes = kHG * kChunk * 2;       // one bf16 term of P: 6 KiB
+constexpr int kOutBytes = 1024;                 // of an epilogue warp: 32 columns x 16 heads in bf16
 template <int kTerms>
 constexpr int kStagedBytes = kTerms == 1 ? 4 * kOutBytes : 0;
 constexpr int kSCol = 0;                        // two S buffers of 64 columns
@@ -75,11 +81,12 @@ __device__ __forceinline__ constexpr uint32_t o_col(int dd) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleAbove = 8.f;            // log2 units
-constexpr int kMaxRec = 128;                    // segments a CTA lists at a time
+constexpr int kMaxRec = 64;                     // segments a CTA lists at a time
 constexpr int kMaxCtas = 152;                   // CTAs of the grid at most (sizes the workspace)
-constexpr int kSegCost = 2;                     // a segment's epilogue, in chunks
-constexpr int kCutAbove = 4;                    // chunks a token may exceed the mean before tokens are cut
-constexpr int kFlushF32 = 40, kFlushBf16 = 512; // chunks between roundings of the accumulator, at most
+constexpr int kSegCost = 4;                     // a segment's epilogue, in chunks (3: 128 contexts of 512 rows 30.3
+                                                // us instead of 29.3; 2: 128-head drafts 82.5 instead of 76.5)
+constexpr int kCutAbove = 5;                    // chunks a token may exceed the mean before tokens are cut
+constexpr int kFlushF32 = 53, kFlushBf16 = 682; // chunks between roundings of the accumulator, at most
 
 struct PagedArgs {
     csa_paged_layout_t L;
@@ -113,13 +120,13 @@ constexpr int kRecZero = 2;   // a token without rows: zeros
 
 struct Smem {
     uint64_t q_full, q_free;
-    uint64_t full[kStages], empty[kStages][4];   // a stage is released 16 rows at a time
+    uint64_t full[kStages], empty[kStages][kSlices];   // a stage is released 16 rows at a time
     uint64_t sfull[2], sfree[2];
-    uint64_t pfull[2], pfree;    // P's rows 0..15 and 32..47, then 16..31 and 48..63
+    uint64_t pfull[2], pfree;    // P's rows 0..15 and 32..47, then 16..31
     uint64_t stretch[2], stretch_free[2];   // the factors of a stretch are written, used
     uint64_t ofree[4];           // a tile of O^T is drained
     uint32_t tmem_holder;
-    uint32_t maskw[kStages][4];
+    uint32_t maskw[kStages][kSlices];
     uint32_t flag[2][4];
     float alpha[kHG];
     alignas(16) float fin[2][kHG];     // of a stretch: factors of the output,
@@ -157,13 +164,6 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, int
         : "memory");
 }
 
-__device__ __forceinline__ void tma_prefetch_l2_3d(const CUtensorMap *m, int32_t x, int32_t y, int32_t z) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(m)),
-                 "r"(x), "r"(y), "r"(z)
-                 : "memory");
-}
-
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
                                             int32_t z, int32_t w, uint64_t *bar, uint64_t policy) {
     asm volatile(
@@ -185,7 +185,7 @@ __device__ __forceinline__ void tmem_ld16_raw(uint32_t taddr, uint32_t (&r)[16])
 }
 
 // threads 0..15: lanes 0..15 of the quarter, columns c ..; threads 16..31: the
-// same lanes, columns c + 32 ..
+// same lanes, columns c + 32 .. (16 of them) and c + 8 .. (8)
 __device__ __forceinline__ void tmem_ld16x2_raw(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
@@ -193,6 +193,13 @@ __device__ __forceinline__ void tmem_ld16x2_raw(uint32_t taddr, uint32_t (&r)[16
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
           "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld8x2_raw(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8], 8;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
         : "r"(taddr));
 }
 
@@ -211,6 +218,12 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uin
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(2u) << 61;
     return d;
+}
+
+// Unswizzled K-major operand: atoms of 8 rows x 16 bytes, 128 contiguous bytes
+// each, `lbo` apart along K and `sbo` along the rows.
+__device__ __forceinline__ uint64_t atom_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return sw128_desc(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7u) << 61);
 }
 
 // a byte offset as a step of a descriptor's start-address field (every shared
@@ -286,12 +299,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     paged_attention_kernel(const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_rows, const PagedArgs A) {
     constexpr int kFlush = kTerms == 2 ? kFlushF32 : kFlushBf16;
+    constexpr int kPieceBytes = kTerms * kHG * 16;       // 8 rows of P
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem<1024>(smem_raw);
     uint8_t *sQ = smem;
-    uint8_t *sRows = sQ + kQBytes;                       // [stage][8 groups][8 col groups][8 rows][128 B]
-    uint8_t *sP = sRows + kStages * kStageBytes;         // [term][64 heads][128 B]
-    uint8_t *sOut = sP + kTerms * kPBytes;               // [epilogue warp][32 heads][32 columns], bf16 output
+    uint8_t *sRows = sQ + kQBytes;                       // [stage][6 groups][8 col groups][8 rows][128 B]
+    uint8_t *sP = sRows + kStages * kStageBytes;         // [8 rows of the chunk][term][64 heads][16 B]
+    uint8_t *sOut = sP + kTerms * kPBytes;               // [epilogue warp][16 heads][32 columns], bf16 output
     Smem &S = *reinterpret_cast<Smem *>(sOut + kStagedBytes<kTerms>);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -302,8 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&S.q_full, 1);
         mbar_init(&S.q_free, 1);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&S.full[i], 4);
-            for (int k = 0; k < 4; ++k) mbar_init(&S.empty[i][k], 1);
+            mbar_init(&S.full[i], kSlices);
+            for (int k = 0; k < kSlices; ++k) mbar_init(&S.empty[i][k], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.sfull[i], 1);
@@ -370,17 +384,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Tokens are cut only where that shortens the longest CTA by more than
     // the partials and their join cost: otherwise CTA c takes token c (T <= G),
-    // or the tokens that begin in its range.  (4 chunks: at 12, 150 tokens of
-    // 250 to 500 rows gain, 41.3 -> 32.6 us, but 64 of 512 to 1,024 rows lose,
-    // 31.2 -> 39.2, and one of 600, 9.2 -> 23.4.)
+    // or the tokens that begin in its range.  (240 rows; 192 and 336 measure the
+    // same within 0.5%.  At 768, 150 tokens of 250 to 500 rows gained, 41.3 ->
+    // 32.6 us, but 64 of 512 to 1,024 rows lost, 31.2 -> 39.2, and one of 600,
+    // 9.2 -> 23.4, all with chunks of 64 rows.)
     const bool direct = T <= G && maxc <= static_cast<int>(A.split_div[0].div(U)) + kCutAbove;
     const bool snap = direct || (T > G && maxc <= kCutAbove);
     // few CTAs at work: 2 or 4 of them share a range, each with all of its
     // logits and weights and its share of the 512 columns: the last products
-    // and the partial (32 bytes a cycle and SM) are that much shorter
+    // and the partial (32 bytes a cycle and SM) are that much shorter (8,192
+    // rows, three chunks for two CTAs 14.8 us, two for one 15.3)
     int dlog = 0;
     if (direct) dlog = T * 4 <= G ? 2 : T * 2 <= G ? 1 : 0;
-    else if (!snap && T <= G) dlog = U <= G / 4 ? 2 : U <= G ? 1 : 0;
+    else if (!snap && T <= G) dlog = U <= G / 4 ? 2 : 3 * U <= 4 * G ? 1 : 0;
     const int dparts = 1 << dlog;
     const int split = static_cast<int>(blockIdx.x) >> dlog;
     const int ndt = 4 >> dlog;                                    // 128-column tiles of this CTA
@@ -547,24 +563,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t q_desc = sw128_desc(smem_addr(sQ), 16, 1024);
             const uint64_t r_desc = sw128_desc(smem_addr(sRows), 16, kGroupBytes);
             const uint64_t a_desc = sw128_desc(smem_addr(sRows) + 2 * dt0 * 1024, 1024, kGroupBytes);
-            const uint64_t p_desc = sw128_desc(smem_addr(sP), 16, 1024);
+            const uint64_t p_desc = atom_desc(smem_addr(sP), kPieceBytes, 128);
             const int dl = (warp & 3) * 32 + lane;   // column of a tile
             const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
             const int hmax = min(kHG, H - h0);
-            // two slices of 16 rows, each released when its products are done
+            // slices of 16 rows (0 and 2, then 1), each released when its products are done
             auto product = [&](int dd, int ks, uint64_t ad, uint32_t acc) {
                 const uint64_t av = ad + off(2 * dd * 1024 + ks * 2 * kGroupBytes);
                 const uint32_t d = tmem + o_col<kTerms>(dd);
+                const uint64_t pd = p_desc + off(2 * ks * kPieceBytes);
                 if (dd < kWide<kTerms>) {
-                    umma_bf16(d, av, p_desc + off(ks * 32), id_wide, acc);
+                    umma_bf16(d, av, pd, id_wide, acc);
                 } else {
-                    umma_bf16(d, av, p_desc + off(ks * 32), id_pv, acc);
-                    if (kTerms == 2) umma_bf16(d, av, p_desc + off(kPBytes + ks * 32), id_pv, 1u);
+                    umma_bf16(d, av, pd, id_pv, acc);
+                    if (kTerms == 2) umma_bf16(d, av, pd + off(kHG * 16), id_pv, 1u);
                 }
             };
             auto pv = [&](auto ntile, uint64_t ad, int st, int k0) {
 #pragma unroll
-                for (int ks = k0; ks < kChunk / 16; ks += 2) {
+                for (int ks = k0; ks < kSlices; ks += 2) {
 #pragma unroll
                     for (int dd = 0; dd < ntile; ++dd) product(dd, ks, ad, 1u);
                     umma_commit(&S.empty[st][ks]);
@@ -605,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     if (elect_one()) {
                         const uint64_t rd = r_desc + off(st * kStageBytes);
-                        const uint32_t d = tmem + kSCol + sb * kChunk;
+                        const uint32_t d = tmem + kSCol + sb * 64;
 #pragma unroll
                         for (int kk = 0; kk < 32; ++kk) {
                             const uint32_t cg = kk >> 2, ko = (kk & 3) * 32;
@@ -633,9 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tc_fence_after();
                             if (elect_one()) {
 #pragma unroll
-                                for (int ks = 0; ks < kChunk / 16; ++ks) product(dd, ks, ad, ks > 0 ? 1u : 0u);
+                                for (int ks = 0; ks < kSlices; ++ks) product(dd, ks, ad, ks > 0 ? 1u : 0u);
                                 if (dd + 1 == ndt) {
-                                    for (int ks = 0; ks < 4; ++ks) umma_commit(&S.empty[st][ks]);
+                                    for (int ks = 0; ks < kSlices; ++ks) umma_commit(&S.empty[st][ks]);
                                     umma_commit(&S.pfree);
                                 }
                             }
@@ -741,14 +758,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         reinterpret_cast<__nv_bfloat16 *>(sOut + (warp & 3) * kOutBytes);
                                     __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(A.out) + at +
                                                                (lane >> 2) * kHD + (warp & 3) * 32 + (lane & 3) * 8;
-                                    __syncwarp();
 #pragma unroll
-                                    for (int x = 0; x < 32; ++x) stage[x * 32 + lane] = __float2bfloat16(__uint_as_float(o[x]));
-                                    __syncwarp();
+                                    for (int y = 0; y < 32; y += 16) {
+                                        __syncwarp();
 #pragma unroll
-                                    for (int x = 0; x < 32; x += 8) {
-                                        const uint4 v = reinterpret_cast<const uint4 *>(stage)[x * 4 + lane];
-                                        if (hb + x + (lane >> 2) < hmax) *reinterpret_cast<uint4 *>(dst + x * kHD) = v;
+                                        for (int x = 0; x < 16; ++x)
+                                            stage[x * 32 + lane] = __float2bfloat16(__uint_as_float(o[x + y]));
+                                        __syncwarp();
+#pragma unroll
+                                        for (int x = 0; x < 16; x += 8) {
+                                            const uint4 v = reinterpret_cast<const uint4 *>(stage)[x * 4 + lane];
+                                            if (hb + x + y + (lane >> 2) < hmax) *reinterpret_cast<uint4 *>(dst + (x + y) * kHD) = v;
+                                        }
                                     }
                                 } else {
                                     // a column a lane (16 bytes a lane: 83.8 -> 84.6 us for 128-head drafts)
@@ -770,12 +791,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     settle();
                 }
             }
-        } else if (warp < 4) {
+        } else if (warp < kSlices) {
             // -------------------------------------------- row fetch
             // The warp walks the list's chunks, 16 rows of each.  Lane l (and
-            // l + 16) looks after row l; three chunks ahead its page number is
-            // on its way from the table, two ahead it is a row of the pool (a box's
-            // bytes then set out into L2), then it is copied.
+            // l + 16) looks after row l; three chunks before it is copied its page
+            // number is on its way from the table, two before it is a row of
+            // the pool.
             const int li = warp;
             const int rl = lane & 15;
             int bad = 0;
@@ -812,7 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int32_t row;                           // row of the pool, or -1
                 uint32_t box;                          // bit g: group g of 8 rows is one box
             };
-            auto place = [&](const Entry &e, bool ahead) {
+            auto place = [&](const Entry &e) {
                 Place p{-1, 0};
                 if (e.in_page >= 0) {
                     if (e.page < 0 || e.page >= A.num_pages) bad |= CSA_DEV_BAD_INDEX;
@@ -821,10 +842,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const uint32_t bx = __ballot_sync(0xffffffffu, e.box);
                 p.box = (bx & 1u) | (bx >> 7 & 2u);
-                // (boxes only: prefetches of single rows hold up the copies, pages of two
-                // rows 136 -> 155 us by bulk prefetch, 142 by lines)
-                if (ahead && lane < 16 && (lane & 7) == 0 && p.row >= 0 && (p.box >> (lane >> 3) & 1u))
-                    tma_prefetch_l2_3d(&tm_rows, 0, p.row, 0);
                 return p;
             };
             int pending = -1;                          // stage whose cp.async rows are in flight
@@ -846,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Entry e1 = look_up(far);
             advance(far);
             Entry ahead = look_up(far);
-            Place now = place(e0, false), next = place(e1, false);
+            Place now = place(e0), next = place(e1);
             while (cur.i < nrec) {
                 const Rec &r = S.rec[cur.i];
                 const int j0 = cur.c * kChunk + 16 * li, wslot = rec_window_slot(r);
@@ -900,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // the queue moves up
                 now = next;
-                next = place(ahead, true);
+                next = place(ahead);
                 advance(far);
                 ahead = look_up(far);
                 advance(cur);
@@ -912,11 +929,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (pending >= 0) land(false);
             bad = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bad)));
             if (lane == 0 && lead) raise_status(A.status, bad);
-        } else {
+        } else if (warp >= 4) {
             // -------------------------------------------- softmax
             const int q = warp & 3;                  // TMEM lane quarter
             const int hl = q * 16 + (lane & 15);     // head of this lane (two lanes per head)
-            const bool upper = lane >= 16;           // rows 32..63 of the chunk
+            const bool upper = lane >= 16;           // rows 32..47 and 24..31 of the chunk, others 0..23
             const bool hv = h0 + hl < H;
             const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
             for (int i = 0; i < nrec; ++i) {
@@ -939,34 +956,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int st = n_sm % kStages, sb = n_sm & 1u;
                     mbar_wait(&S.sfull[sb], (n_sm >> 1) & 1u, A.status);
                     tc_fence_after();
-                    uint32_t sr[2][16];
-                    tmem_ld16x2_raw(tmem + lane_off + kSCol + sb * kChunk, sr[0]);
-                    tmem_ld16x2_raw(tmem + lane_off + kSCol + sb * kChunk + 16, sr[1]);
+                    uint32_t sr[16], sr2[8];
+                    tmem_ld16x2_raw(tmem + lane_off + kSCol + sb * 64, sr);
+                    tmem_ld8x2_raw(tmem + lane_off + kSCol + sb * 64 + 16, sr2);
                     tmem_wait_ld();
                     tc_fence_before();
                     mbar_arrive(&S.sfree[sb]);
                     mbar_wait(&S.full[st], (n_sm / kStages) & 1u, A.status);   // orders the mask words
-                    uint64_t msk = 0;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) msk |= static_cast<uint64_t>(S.maskw[st][w]) << (16 * w);
+                    const uint32_t mw[kSlices] = {S.maskw[st][0], S.maskw[st][1], S.maskw[st][2]};
                     // Every row real and a scale >= 0: the maximum of the raw
                     // logits, the scale in the exponent's fma.  Otherwise
                     // scaled logits, rows that do not exist at -inf.
-                    float x[32];
+                    float x[24];
                     float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     float xs = 1.f;
-                    if (msk == ~0ull && A.scale_log2 >= 0.f) {
+                    if ((mw[0] & mw[1] & mw[2]) == 0xFFFFu && A.scale_log2 >= 0.f) {
                         xs = A.scale_log2;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            x[j] = __uint_as_float(sr[j >> 4][j & 15]);
+                        for (int j = 0; j < 24; ++j) {
+                            x[j] = __uint_as_float(j < 16 ? sr[j & 15] : sr2[j & 7]);
                             mq[j & 3] = fmaxf(mq[j & 3], x[j]);
                         }
                     } else {
-                        const uint32_t mh = static_cast<uint32_t>(msk >> (upper ? 32 : 0));
+                        const uint32_t mh = (upper ? mw[2] : mw[0]) | (mw[1] >> (upper ? 8 : 0) & 0xFFu) << 16;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const uint32_t v = sr[j >> 4][j & 15];
+                        for (int j = 0; j < 24; ++j) {
+                            const uint32_t v = j < 16 ? sr[j & 15] : sr2[j & 7];
                             x[j] = ((mh >> j) & 1u) ? __uint_as_float(v) * A.scale_log2 : -INFINITY;
                             mq[j & 3] = fmaxf(mq[j & 3], x[j]);
                         }
@@ -1013,14 +1028,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // hi + lo with lo the rounded rest
                     const float mr = m_ref == -INFINITY ? 0.f : m_ref;
                     float sq[2] = {0.f, 0.f};
-                    uint8_t *const pr = sP + hl * 128;
-                    // half of the lane's rows at a time: the first products
-                    // start under the second half's exponentials
+                    uint8_t *const pr = sP + hl * 16;
+                    // two thirds of the lane's rows, then the rest: the first products
+                    // start under the rest's exponentials
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         uint32_t phi[8], plo[8];
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
+                        for (int u = 0; u < (half == 0 ? 8 : 4); ++u) {
                             const int j = 16 * half + 2 * u;
                             const float p0 = fast_exp2(fmaf(x[j], xs, -mr));
                             const float p1 = fast_exp2(fmaf(x[j + 1], xs, -mr));
@@ -1036,12 +1051,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (half == 0 && n_sm > 0) mbar_wait(&S.pfree, (n_sm - 1) & 1u, A.status);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t sw = static_cast<uint32_t>((((upper ? 4 : 0) + 2 * half + e) ^ (hl & 7)) << 4);
-                            *reinterpret_cast<uint4 *>(pr + sw) =
-                                make_uint4(phi[4 * e], phi[4 * e + 1], phi[4 * e + 2], phi[4 * e + 3]);
+                        for (int e = 0; e < (half == 0 ? 2 : 1); ++e) {
+                            const int piece = half == 0 ? (upper ? 4 : 0) + e : (upper ? 3 : 2);
+                            uint8_t *const at = pr + piece * kPieceBytes;
+                            *reinterpret_cast<uint4 *>(at) = make_uint4(phi[4 * e], phi[4 * e + 1], phi[4 * e + 2], phi[4 * e + 3]);
                             if (kTerms == 2)
-                                *reinterpret_cast<uint4 *>(pr + kPBytes + sw) =
+                                *reinterpret_cast<uint4 *>(at + kHG * 16) =
                                     make_uint4(plo[4 * e], plo[4 * e + 1], plo[4 * e + 2], plo[4 * e + 3]);
                         }
                         fence_proxy_async_smem();
@@ -1308,7 +1323,7 @@ template <bool kBf16>
 cudaError_t launch_join(const Launch &lc, const PagedArgs &A, int entries, int groups, int64_t slots_max) {
     // one token: 8 threads a column up to 32 parts (600 rows: 9.0 us the whole call
     // against 10.2 with 16), 16 beyond (8,192 rows: 13.9 against 15.0 us)
-    if (entries == 1 && slots_max <= 32 * kChunk)
+    if (entries == 1 && slots_max <= 2048)
         return launch_one_join<join_deep_kernel<8, 32, kBf16>>(lc, A, dim3(1, groups * 64, 4), 256);
     if (entries == 1) return launch_one_join<join_deep_kernel<16, 32, kBf16>>(lc, A, dim3(1, groups * 64, 4), 512);
     if (entries <= 12) return launch_one_join<join_deep_kernel<4, 128, kBf16>>(lc, A, dim3(entries, groups * 64), 512);
