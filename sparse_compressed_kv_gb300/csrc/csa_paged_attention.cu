@@ -1321,8 +1321,8 @@ cudaError_t launch_one_join(const Launch &lc, const PagedArgs &A, dim3 grid, int
 
 template <bool kBf16>
 cudaError_t launch_join(const Launch &lc, const PagedArgs &A, int entries, int groups, int64_t slots_max) {
-    // one token: 8 threads a column up to 32 parts (600 rows: 9.0 us the whole call
-    // against 10.2 with 16), 16 beyond (8,192 rows: 13.9 against 15.0 us)
+    // one token: 8 threads a column for few parts (600 rows: 1.2 us less than with
+    // 16), 16 beyond (8,192 rows: 1.1 us less than with 8)
     if (entries == 1 && slots_max <= 2048)
         return launch_one_join<join_deep_kernel<8, 32, kBf16>>(lc, A, dim3(1, groups * 64, 4), 256);
     if (entries == 1) return launch_one_join<join_deep_kernel<16, 32, kBf16>>(lc, A, dim3(1, groups * 64, 4), 512);
