@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // rows, three chunks for two CTAs 14.8 us, two for one 15.3)
     int dlog = 0;
     if (direct) dlog = T * 4 <= G ? 2 : T * 2 <= G ? 1 : 0;
-    else if (!snap && T <= G) dlog = U <= G / 4 ? 2 : 3 * U <= 4 * G ? 1 : 0;
+    else if (!snap && T <= G) dlog = U <= G / 4 ? 2 : U <= G + G / 3 ? 1 : 0;
     const int dparts = 1 << dlog;
     const int split = static_cast<int>(blockIdx.x) >> dlog;
     const int ndt = 4 >> dlog;                                    // 128-column tiles of this CTA
