@@ -333,6 +333,88 @@ def test_attention_long_rows_in_one_cta(cuda_device):
             assert (out[t].double() - ref).norm() <= H.REL[dtype] * ref.norm()
 
 
+@pytest.mark.parametrize("T,n", [
+    (100, 640),      # a whole token a CTA
+    (60, 400),       # two CTAs a token, half of the columns each
+    (30, 300),       # four
+    (1, 20000),      # one token over all CTAs, three chunks each
+    (160, 3000),     # long stretches, rounded into the partial on the way
+], ids=str)
+def test_attention_rising_maximum(cuda_device, T, n):
+    # rows in steps of 48 whose logits rise by more than the rescaling's threshold,
+    # so that what a CTA has accumulated is rescaled, and still counts
+    dev = cuda_device
+    g = torch.Generator(device=dev).manual_seed(T)
+    rows = torch.randn(n, H.HD, device=dev, generator=g)
+    rows = (rows * (2 + 2.2 * (torch.arange(n, device=dev) % 144 // 48))[:, None]).to(BF16)
+    pages = -(-n // 16)
+    table = torch.randperm(pages, device=dev, generator=g).int()[None]
+    cache = torch.full((pages, 16, H.HD), float("nan"), device=dev, dtype=BF16)
+    j = torch.arange(n, device=dev)
+    cache[table[0, j // 16].long(), j % 16] = rows
+    q = torch.randn(T, 64, H.HD, device=dev, generator=g).to(BF16)
+    layout = csa.PagedLayout(torch.zeros(T, dtype=torch.int32, device=dev),
+                             torch.full((T,), 4 * n, dtype=torch.int64, device=dev),
+                             torch.tensor([n], device=dev), table, 16)
+    prm = csa.params(64, 1, 0, 4)
+    ws = csa.paged_workspace(layout, prm)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    for dtype in (F32, BF16):
+        out = torch.empty(T, 64, H.HD, device=dev, dtype=dtype)
+        csa.csa_paged_attention(layout, prm, cache, q, out, status, ws)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        for t in range(0, T, max(1, T // 12)):
+            l = prm.scale * q[t].double() @ rows.double().T
+            assert 20 < float(l.max()) < 40
+            ref = torch.softmax(l, 1) @ rows.double()
+            # a weight's relative error is its logit's absolute error: 32
+            # accumulation steps of 2^-23 of at most 40, in weights and their sum
+            tol = H.REL[dtype] + 2 * 40 * 32 * 2 ** -23
+            err = (out[t].double() - ref).norm(dim=1) / ref.norm(dim=1)
+            assert float(err.max()) <= tol, f"token {t}: off by {float(err.max()):.3e}"
+
+
+@pytest.mark.parametrize("long", [150, 3000], ids=["whole", "cut"])
+def test_attention_more_tokens_than_a_cta_lists(cuda_device, long):
+    # mostly padding, so that one CTA's range holds more than a hundred tokens; real
+    # ones and ones without rows among them, and one long enough to be cut
+    dev, T, heads = cuda_device, 8192, 65
+    g = torch.Generator(device=dev).manual_seed(long)
+    n = [150, long]
+    pages = [-(-x // 16) for x in n]
+    table = torch.full((2, max(pages)), -1, dtype=torch.int32, device=dev)
+    table[0, :pages[0]] = torch.arange(pages[0], device=dev)
+    table[1, :pages[1]] = pages[0] + torch.arange(pages[1], device=dev)
+    cache = torch.randn(sum(pages), 16, H.HD, device=dev, generator=g).to(BF16)
+    q = torch.randn(T, heads, H.HD, device=dev, generator=g).to(BF16)
+    i = torch.arange(T)
+    seq, pos = torch.full((T,), -1, dtype=torch.int32), torch.full((T,), -1, dtype=torch.int64)
+    real, empty = i % 41 == 7, i % 64 == 3
+    seq[real | empty] = 0
+    pos[real] = 4 * (i[real] % 150 + 1)
+    pos[empty] = 3
+    seq[5000], pos[5000] = 1, 4 * long
+    layout = csa.PagedLayout(seq.to(dev), pos.to(dev), torch.tensor(n, device=dev), table, 16)
+    prm = csa.params(heads, 1, 0, 4)
+    ws = csa.paged_workspace(layout, prm)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    held = [cache[table[b, :pages[b]].long()].reshape(-1, H.HD)[:n[b]].double() for b in range(2)]
+    for dtype in (F32, BF16):
+        out = torch.full((T, heads, H.HD), 7.5, device=dev, dtype=dtype)
+        csa.csa_paged_attention(layout, prm, cache, q, out, status, ws)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        assert bool((out[(seq < 0).to(dev)] == 7.5).all())
+        for t in (seq >= 0).nonzero()[:, 0].tolist():
+            rows = held[int(seq[t])][:int(pos[t]) // 4]
+            if len(rows) == 0:
+                assert bool((out[t] == 0).all())
+                continue
+            ref = torch.softmax(prm.scale * q[t].double() @ rows.T, 1) @ rows
+            assert (out[t].double() - ref).norm() <= H.REL[dtype] * ref.norm(), t
+
+
 def test_attention_on_another_stream(cuda_device):
     p = H.Paged(12, row_len=[500, 300], tokens=[(0, 2000), (1, 1200)], heads=64)
     a, _ = p.run(cuda_device, BF16)
