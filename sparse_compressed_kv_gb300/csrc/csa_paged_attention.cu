@@ -771,6 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                             if (hb + x + y + (lane >> 2) < hmax) *reinterpret_cast<uint4 *>(dst + (x + y) * kHD) = v;
                                         }
                                     }
+                                    __syncwarp();                // (some lanes stored, some did not)
                                 } else {
                                     // a column a lane (16 bytes a lane: 83.8 -> 84.6 us for 128-head drafts)
 #pragma unroll
@@ -954,7 +955,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int every = flush_every<kFlush>(nch);
                 for (int k = 0, z = 0; k < nch; ++k, ++n_sm, z = z + 1 == every ? 0 : z + 1) {
                     const int st = n_sm % kStages, sb = n_sm & 1u;
+                    // (a wait's lanes may leave it at different polls; what is
+                    // .aligned below, tensor memory and barriers, wants the warp whole)
                     mbar_wait(&S.sfull[sb], (n_sm >> 1) & 1u, A.status);
+                    __syncwarp();
                     tc_fence_after();
                     uint32_t sr[16], sr2[8];
                     tmem_ld16x2_raw(tmem + lane_off + kSCol + sb * 64, sr);
@@ -1001,11 +1005,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else if (m_ref == -INFINITY) {
                         m_ref = mc;
                     }
+                    __syncwarp();
                     named_bar_sync(kBarSm, kSmThreads);
                     const bool any = (S.flag[sb][0] | S.flag[sb][1] | S.flag[sb][2] | S.flag[sb][3]) != 0;
                     if (any && z != 0) {
                         if (!upper) S.alpha[hl] = alpha;
                         mbar_wait(&S.pfree, (n_sm - 1) & 1u, A.status);   // the product before this one
+                        __syncwarp();
                         named_bar_sync(kBarSm, kSmThreads);
                         tc_fence_after();
 #pragma unroll 1
