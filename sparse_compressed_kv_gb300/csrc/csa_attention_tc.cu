@@ -487,7 +487,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < nch; ++i) {
             const int st = i & 1;
             const uint32_t ph = static_cast<uint32_t>(i >> 1) & 1u;
+            // (a wait's lanes may leave it at different polls; what is .aligned
+            // below, tensor memory and barriers, wants the warp whole)
             mbar_wait(&S.sfull[st], ph, A.status);
+            __syncwarp();
             tc_fence_after();
             // S of the M = 64 product sits in lanes 0..15 of the quarter: the
             // two-access load gives lanes 0..15 columns c.. to threads 0..15
@@ -542,12 +545,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             } else if (m_ref == -INFINITY) {
                 m_ref = mc;
             }
+            __syncwarp();
             named_bar_sync(kBarSm, kSmThreads);
             const bool any = (S.flag[st][0] | S.flag[st][1] | S.flag[st][2] | S.flag[st][3]) != 0;
             if (any) {
                 if (!upper) S.alpha[hl] = alpha;
                 // PV of the previous chunk must have landed in O^T
                 mbar_wait(&S.pfree[st ^ 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, A.status);
+                __syncwarp();
                 named_bar_sync(kBarSm, kSmThreads);
                 tc_fence_after();
 #pragma unroll 1
@@ -618,6 +623,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             S.fin[hl] = f;
         }
         if (nch > 0) mbar_wait(&S.odone, 0, A.status);
+        __syncwarp();
         named_bar_sync(kBarSm, kSmThreads);
         tc_fence_after();
         const bool part = A.splits > 1 || A.raw;
