@@ -387,12 +387,35 @@ def _device_stream(fn: str, index: int, stream=None) -> int:
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
 
 
-def _ptr(t, index: int) -> int:
+def _ptr(t, index: int, contiguous=True) -> int:
     if not t.is_cuda or t.get_device() != index:
         raise ValueError(f"tensor must live on cuda:{index}")
-    if not t.is_contiguous():
+    if contiguous and not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
     return t.data_ptr()
+
+
+def _page_stride(cache, page_rows: int) -> int:
+    """Rows from a page to the next of a cache [num_pages, rows, *row], which
+    is a whole pool or one layer's part of a pool that several share
+    (pool[:, first:first + page_rows]): the rows of a page are dense, the pages
+    any whole number of rows apart."""
+    rows = int(cache.shape[1])
+    if rows < page_rows:
+        raise ValueError(f"a page of cache holds {rows} rows, not {page_rows}")
+    if cache.is_contiguous():
+        return rows
+    want, width = [], 1
+    for n in reversed(cache.shape[1:]):
+        want.insert(0, width)
+        width *= int(n)
+    row = width // max(rows, 1)
+    dense = all(n == 1 or s == w for n, s, w in zip(cache.shape[1:], cache.stride()[1:], want))
+    apart = cache.stride(0) if cache.shape[0] > 1 else width
+    if not dense or row == 0 or apart % row or apart < width:
+        raise ValueError("cache must have dense pages, a whole number of rows apart, got shape "
+                         f"{tuple(cache.shape)} and stride {cache.stride()}")
+    return apart // row
 
 
 class PagePlan:
@@ -433,15 +456,17 @@ def csa_page_plan(plan: PagePlan, dev_status, stream=None):
 
 class AppendJob:
     """Rows [n, ...] (dense within a row, any pitch) to slots [n] of a cache
-    [num_pages, page_stride, ...] whose rows have the same bytes."""
+    [num_pages, at least page_rows, ...] whose rows have the same bytes: a
+    whole pool, or one layer's part of it (pool[:, first:first + page_rows])."""
 
     def __init__(self, rows, slots, cache, page_rows: int):
         n = int(rows.shape[0])
         if cache.dim() < 2 or cache.dtype != rows.dtype or cache.shape[2:] != rows.shape[1:]:
-            raise ValueError(f"cache must be {rows.dtype} [num_pages, page_stride, "
+            raise ValueError(f"cache must be {rows.dtype} [num_pages, rows of a page, "
                              f"*{tuple(rows.shape[1:])}], got {cache.dtype} {tuple(cache.shape)}")
         if n and not rows[0].is_contiguous():
             raise ValueError("a row must be contiguous")
+        apart = _page_stride(cache, page_rows)
         size = rows.element_size()
         width = size * (rows[0].numel() if n else cache[0, 0].numel())
         pitch = rows.stride(0) * size if n > 1 else width
@@ -450,7 +475,7 @@ class AppendJob:
             rows=_arg("rows", rows, rows.dtype, contiguous=False),
             slots=_arg("slots", slots, torch.int64, (n,)), num_rows=n, row_pitch=pitch,
             row_bytes=width, page_rows=page_rows, num_pages=int(cache.shape[0]),
-            page_stride=int(cache.shape[1]), cache=_arg("cache", cache, cache.dtype))
+            page_stride=apart, cache=_arg("cache", cache, cache.dtype, contiguous=False))
 
 
 class AppendJobs:
@@ -509,8 +534,9 @@ def paged_workspace(layout: PagedLayout, prm: csa_params_t, device=None) -> torc
 
 def csa_paged_attention(layout: PagedLayout, prm: csa_params_t, cache, q, out, dev_status, ws,
                         sinks=None, stream=None):
-    """cache bf16 [num_pages, page_stride, 512], q bf16 [T, H, 512], out f32 or
-    bf16 [T, H, 512]."""
+    """cache bf16 [num_pages, at least page_rows, 512] (a whole pool, or one
+    layer's part of it, as for AppendJob), q bf16 [T, H, 512], out f32 or bf16
+    [T, H, 512]."""
     dev = layout.device
     s = _device_stream("csa_paged_attention", dev, stream)
     if cache.dtype != torch.bfloat16 or q.dtype != torch.bfloat16:
@@ -521,10 +547,11 @@ def csa_paged_attention(layout: PagedLayout, prm: csa_params_t, cache, q, out, d
     if q.shape != shape or out.shape != shape:
         raise ValueError(f"q and out must have shape {shape}")
     if cache.dim() != 3 or cache.shape[2] != prm.hd:
-        raise ValueError(f"cache must have shape (num_pages, page_stride, {prm.hd})")
+        raise ValueError(f"cache must have shape (num_pages, rows of a page, {prm.hd})")
     if sinks is not None and (sinks.dtype != torch.float32 or sinks.shape != (prm.n_heads,)):
         raise ValueError(f"sinks must be float32 [{prm.n_heads}]")
     _check("csa_paged_attention", load().csa_paged_attention(
-        layout.ref, ctypes.byref(prm), _ptr(cache, dev), cache.shape[0], cache.shape[1], _ptr(q, dev),
+        layout.ref, ctypes.byref(prm), _ptr(cache, dev, contiguous=False), cache.shape[0],
+        cache.shape[1] if cache.is_contiguous() else _page_stride(cache, layout.c.page_rows), _ptr(q, dev),
         None if sinks is None else _ptr(sinks, dev), 1 if out.dtype == torch.bfloat16 else 0,
         _ptr(out, dev), _ptr(dev_status, dev), _ptr(ws, dev), ws.numel(), s))

@@ -26,3 +26,97 @@ def test_attention_head_counts_inside_a_group(cuda_device, heads, dtype):
     H.check(got, p.reference(tokens=tokens), dtype, tokens)
     again, _ = p.run(cuda_device, dtype)
     assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("width,page_rows,gap", [(1024, 16, 0), (80, 3, 2)])
+def test_append_to_one_layer_of_interleaved_pages(cuda_device, width, page_rows, gap):
+    dev, pages, P, layers = cuda_device, 9, page_rows, 3
+    g = torch.Generator(device=dev).manual_seed(width)
+    pool = torch.randint(0, 256, (pages, layers * P + gap, width), dtype=torch.uint8, device=dev, generator=g)
+    want, jobs, status = pool.clone(), [], torch.zeros(1, dtype=torch.int32, device=dev)
+    for k in (0, 2):                # the layer between them, and the gap, stay as they are
+        n = 2 * pages * P // 3
+        rows = torch.randint(0, 256, (n, width), dtype=torch.uint8, device=dev, generator=g)
+        slots = torch.randperm(pages * P, device=dev, generator=g)[:n]
+        jobs.append(csa.AppendJob(rows, slots, pool[:, k * P:(k + 1) * P], P))
+        want[slots // P, k * P + slots % P] = rows
+    csa.csa_paged_append(csa.AppendJobs(jobs), status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and torch.equal(pool, want)
+
+
+@pytest.mark.parametrize("page_rows", [16, 6])
+def test_attention_over_one_layer_of_interleaved_pages(cuda_device, page_rows):
+    # three layers' rows under the same page numbers; each call sees its own
+    dev, P, layers = cuda_device, page_rows, 3
+    ps = [H.Paged(60 + k, row_len=[210, 77], tokens=[(0, 850), (1, 320)], heads=24, page_rows=P, window=40)
+          for k in range(layers)]
+    pages = ps[0].cache.shape[0]
+    pool = torch.full((pages, layers * P, H.HD), float("nan"), dtype=BF16, device=dev)
+    for k, p in enumerate(ps):
+        for b, n in enumerate([210, 77]):                   # one table for all layers
+            j = torch.arange(n)
+            pool[ps[0].table[b, j // P].long(), k * P + j % P] = p.cache[p.table[b, j // P].long(), j % P].to(dev)
+    for k, p in enumerate(ps):
+        layout = csa.PagedLayout(p.tok_seq.to(dev), p.tok_pos.to(dev), p.row_len.to(dev), ps[0].table.to(dev), P,
+                                 p.swa_kv.to(dev), p.swa_first_pos.to(dev))
+        prm = csa.params(24, 1, 40, 4)
+        out, status = torch.empty(2, 24, H.HD, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+        csa.csa_paged_attention(layout, prm, pool[:, k * P:(k + 1) * P], p.q.to(dev), out, status,
+                                csa.paged_workspace(layout, prm))
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        H.check(out, p.reference(), F32)
+
+
+def test_serving_step_over_two_layers_of_interleaved_pages(cuda_device):
+    # one plan a step for both layers; each layer's rows appended to and read from
+    # its own half of every page
+    dev, P, heads, ratio, cap, steps = cuda_device, 5, 16, 4, 24, [17, 1, 1, 30, 1, 4, 1]
+    pages, tok_cap, row_cap = 20, 32, 10
+    i64 = lambda *x: torch.zeros(*x, dtype=torch.int64, device=dev)
+    seq, pos = [i64(1), i64(1)], [torch.tensor([0, pages], device=dev), i64(2)]
+    new_len = torch.zeros(1, dtype=torch.int32, device=dev)
+    table = torch.full((1, 8), -1, dtype=torch.int32, device=dev)
+    ring = torch.randperm(pages, device=dev).int()
+    row_len, first, tok_off, row_off = i64(1), i64(1), i64(2), i64(2)
+    tok_seq = torch.zeros(tok_cap, dtype=torch.int32, device=dev)
+    tok_pos, swa_slot, row_slot = i64(tok_cap), i64(tok_cap), i64(row_cap)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    plans = [csa.PagePlan(ratio=ratio, page_rows=P, swa_cap=cap, seq_len=seq[k], new_len=new_len, table=table,
+                          free_ring=ring, free_pos=pos[k], seq_len_out=seq[1 - k], row_len=row_len,
+                          swa_first_pos=first, free_pos_out=pos[1 - k], tok_off=tok_off, row_off=row_off,
+                          tok_seq=tok_seq, tok_pos=tok_pos, swa_slot=swa_slot, row_slot=row_slot) for k in (0, 1)]
+    pool = torch.full((pages, 2 * P, H.HD), float("nan"), dtype=BF16, device=dev)
+    prm = csa.params(heads, 1, 16, ratio)
+    parts = [pool[:, :P], pool[:, P:]]
+    swa = [torch.zeros(1, cap, H.HD, dtype=BF16, device=dev) for _ in parts]
+    held = [[], []]
+    win = [[], []]
+    for i, n in enumerate(steps):
+        g = torch.Generator(device=dev).manual_seed(i)
+        randn = lambda *x: torch.randn(*x, device=dev, generator=g).to(BF16)
+        new_len.fill_(n)
+        csa.csa_page_plan(plans[i % 2], status)
+        T = sum(steps[:i + 1])
+        for k, cache in enumerate(parts):
+            rows, near, q = randn(row_cap, H.HD), randn(tok_cap, H.HD), randn(tok_cap, heads, H.HD)
+            csa.csa_paged_append(csa.AppendJobs([csa.AppendJob(rows, row_slot, cache, P),
+                                                 csa.AppendJob(near, swa_slot, swa[k], cap)]), status)
+            layout = csa.PagedLayout(tok_seq, tok_pos, row_len, table, P, swa[k], first)
+            out = torch.full((tok_cap, heads, H.HD), 7.0, device=dev)
+            csa.csa_paged_attention(layout, prm, cache, q, out, status, csa.paged_workspace(layout, prm))
+            held[k] += list(rows[:T // ratio - (T - n) // ratio].double())
+            win[k] += list(near[:n].double())
+            torch.cuda.synchronize()
+            # the last token alone: older ones of a long step may have lost their window
+            p = T - 1
+            every = torch.stack(held[k][:p // ratio] + win[k][max(0, p - 15):p + 1])
+            ref = torch.softmax(prm.scale * q[n - 1].double() @ every.T, 1) @ every
+            assert (out[n - 1].double() - ref).norm() <= H.REL[F32] * ref.norm()
+            assert (out[n:] == 7).all()
+        # (the ring holds the newest 24 positions: a step of 30 tokens pushes out what
+        # the first of them would see)
+        lost = max(0, T - n - 15) < max(0, T - cap)
+        assert int(status.item()) == (csa.DEV_MISSING_SWA if lost else 0)
+        status.zero_()
