@@ -410,7 +410,9 @@ csa_status_t csa_topk_noalloc(const csa_layout_t *layout, const csa_params_t *pa
  *     tok_off[b + 1] - 1, its new blocks row_off[b] .. row_off[b + 1] - 1
  *     (the first of them is block floor(seq_len[b] / ratio)).
  *   seq_len_out, row_len, swa_first_pos [B], free_pos_out [2]: after the
- *     step.  They are separate from the inputs (a loop swaps the two).
+ *     step (a loop swaps seq_len and free_pos with their _out).
+ * What the call writes, table and free_ring among it, shares memory with no
+ * other array of the call, else CSA_ERR_INVALID_ARGUMENT.
  * A step that cannot be done is refused as a whole: too few free pages, a
  * request with more than max_pages pages, more than tok_cap tokens or
  * row_cap blocks set CSA_DEV_CAPACITY; a negative or absurd (2^48) length

@@ -334,6 +334,26 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int64_t k2G = int64_t(1) << 31;
 
+struct Range {
+    const void *p;
+    int64_t bytes;
+};
+
+// Whether one of the first `written` arrays shares memory with any other array.
+template <int kN>
+bool overlapping(const Range (&r)[kN], int written) {
+    for (int i = 0; i < written; ++i) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(r[i].p);
+        if (!r[i].p || r[i].bytes <= 0) continue;
+        for (int j = i + 1; j < kN; ++j) {
+            const uintptr_t b = reinterpret_cast<uintptr_t>(r[j].p);
+            if (!r[j].p || r[j].bytes <= 0) continue;
+            if (a < b + r[j].bytes && b < a + r[i].bytes) return true;
+        }
+    }
+    return false;
+}
+
 csa_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
 
 csa_status_t check_paged(const csa_paged_layout_t *L, const csa_params_t *p) {
@@ -380,9 +400,16 @@ extern "C" csa_status_t csa_page_plan(const csa_page_plan_t *plan, int32_t *dev_
     const void *const narrow[] = {P.new_len, P.table, P.free_ring, P.tok_seq, dev_status};
     for (const void *p : narrow)
         if (p && !aligned(p, 4)) return CSA_ERR_INVALID_ARGUMENT;
-    // every CTA reads the inputs while others write the outputs
-    if (P.seq_len_out == P.seq_len || P.row_len == P.seq_len || P.free_pos_out == P.free_pos)
-        return CSA_ERR_INVALID_ARGUMENT;
+    // every CTA reads the inputs, some of them again for each output, while
+    // others write: what is written shares memory with nothing else
+    const int64_t B = P.num_seqs;
+    const Range arrays[] = {{P.table, B * P.max_pages * 4}, {P.free_ring, P.num_pages * 4},
+                            {P.seq_len_out, B * 8}, {P.row_len, B * 8}, {P.swa_first_pos, B * 8},
+                            {P.free_pos_out, 16}, {P.tok_off, (B + 1) * 8}, {P.row_off, (B + 1) * 8},
+                            {P.tok_seq, P.tok_cap * 4}, {P.tok_pos, P.tok_cap * 8},
+                            {P.swa_slot, P.tok_cap * 8}, {P.row_slot, P.row_cap * 8}, {dev_status, 4},
+                            {P.seq_len, B * 8}, {P.new_len, B * 4}, {P.free_pos, 16}};
+    if (overlapping(arrays, 13)) return CSA_ERR_INVALID_ARGUMENT;
     int sms = 0;
     csa_status_t st = current_device(&sms);
     if (st != CSA_OK) return st;

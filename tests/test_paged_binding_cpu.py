@@ -1,9 +1,21 @@
-"""The paged caches' binding on the CPU: which tensors it takes, and what it
-makes of their strides."""
+"""The paged caches on the CPU: which tensors the binding takes, what it makes of
+their strides, and which arrays the C entry points refuse to share memory."""
+import ctypes
+
 import pytest
 import torch
 
+from sparse_compressed_kv_gb300 import build as B
 from sparse_compressed_kv_gb300 import csa
+
+INVALID = 1
+PTR = 4096
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return csa.load()
 
 
 def test_page_stride_of_a_pool_and_its_parts():
@@ -41,3 +53,39 @@ def test_append_job_takes_a_part_of_a_pool():
         csa.AppendJob(torch.zeros(2, 8), i64, pool[:, 4:8], 5)
     with pytest.raises(ValueError, match="page"):
         csa.AppendJob(torch.zeros(2, 8), i64, pool[:, ::2], 4)
+
+
+def _plan_at(lib, **at):
+    """A small plan whose arrays lie apart, but for those named in `at`."""
+    sizes = dict(seq_len=32, new_len=16, table=128, free_ring=128, free_pos=16, seq_len_out=32, row_len=32,
+                 swa_first_pos=32, free_pos_out=16, tok_off=40, row_off=40, tok_seq=32, tok_pos=64, swa_slot=64,
+                 row_slot=32, status=4)
+    ptr = {n: PTR + 256 * i for i, n in enumerate(sizes)}
+    ptr.update({n: ptr[o] + d for n, (o, d) in at.items()})
+    status = ptr.pop("status")
+    p = csa.csa_page_plan_t(num_seqs=4, ratio=4, page_rows=16, max_pages=8, num_pages=32, tok_cap=8, row_cap=4,
+                            swa_cap=128, **ptr)
+    return lib.csa_page_plan(ctypes.byref(p), status, None)
+
+
+WRITTEN = ("table", "free_ring", "seq_len_out", "row_len", "swa_first_pos", "free_pos_out", "tok_off", "row_off",
+           "tok_seq", "tok_pos", "swa_slot", "row_slot", "status")
+
+
+@pytest.mark.parametrize("name", WRITTEN)
+def test_plan_refuses_outputs_over_other_arrays(lib, name):
+    # every CTA reads the inputs while others write the outputs: the same array, or
+    # one that begins inside another
+    for other in ("seq_len", "new_len", "free_pos") + tuple(n for n in WRITTEN if n != name):
+        assert _plan_at(lib, **{name: (other, 0)}) == INVALID, other
+        assert _plan_at(lib, **{name: (other, 8 if other != "status" else 0)}) == INVALID, other
+
+
+def test_plan_takes_arrays_that_only_touch(lib):
+    # (CSA_ERR_CUDA or _UNSUPPORTED: the checks are through, and this machine has no GPU)
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are not real")
+    assert _plan_at(lib) not in (0, INVALID)
+    assert _plan_at(lib, row_len=("seq_len_out", 32), tok_pos=("tok_seq", 32)) not in (0, INVALID)
+    # the inputs may share memory with each other
+    assert _plan_at(lib, new_len=("seq_len", 0)) not in (0, INVALID)
