@@ -494,6 +494,9 @@ csa_status_t csa_paged_append(const csa_append_job_t *jobs /* (host) */, int32_t
  *     rest of the pool may hold anything, NaN included.
  *   q bf16 [T, n_heads, hd], sinks f32 [n_heads] (nullable), out f32 or bf16
  *     [T, n_heads, hd] by out_type.
+ * out, the workspace and the status word share memory with nothing else that
+ * the call takes (a bf16 output does not replace its queries), else
+ * CSA_ERR_INVALID_ARGUMENT; nor with the cache's rows, which is not checked.
  * n_heads is any number from 1 to 128, page_rows any number from 1 (pages of
  * a multiple of 8 rows are copied 8 rows at a time, others row by row);
  * n_ih, ihd and top_k of params are not used.  Rows times weights are summed

@@ -511,6 +511,16 @@ extern "C" csa_status_t csa_paged_attention(const csa_paged_layout_t *layout,
     const size_t want = paged_attention_workspace(L, *params);
     if (want > 0 && (!ws || ws_bytes < want)) return CSA_ERR_WORKSPACE;
     if (ws && !aligned(ws, 256)) return CSA_ERR_INVALID_ARGUMENT;
+    // several CTAs read a token's query, each at its own time, and write their
+    // columns of the output
+    const int64_t T = L.num_tokens, B = L.num_seqs, W = params->window > 0 ? 1 : 0;
+    const int64_t vals = T * params->n_heads * kHD;
+    const Range arrays[] = {{out, vals * (out_type == CSA_BF16 ? 2 : 4)}, {ws, static_cast<int64_t>(want)},
+                            {dev_status, 4}, {q, vals * 2}, {sinks, int64_t(4) * params->n_heads},
+                            {L.tok_seq, T * 4}, {L.tok_pos, T * 8}, {L.row_len, B * 8},
+                            {L.table, B * L.max_pages * 4}, {L.swa_kv, W * B * L.swa_cap * kHD * 2},
+                            {L.swa_first_pos, W * B * 8}};
+    if (overlapping(arrays, 3)) return CSA_ERR_INVALID_ARGUMENT;
     int sms = 0;
     st = current_device(&sms);
     if (st != CSA_OK) return st;

@@ -89,3 +89,43 @@ def test_plan_takes_arrays_that_only_touch(lib):
     assert _plan_at(lib, row_len=("seq_len_out", 32), tok_pos=("tok_seq", 32)) not in (0, INVALID)
     # the inputs may share memory with each other
     assert _plan_at(lib, new_len=("seq_len", 0)) not in (0, INVALID)
+
+
+ATTENTION = dict(out=2 * 3 * 16 * 512, ws=0, status=4, q=2 * 3 * 16 * 512, sinks=64, tok_seq=12, tok_pos=24,
+                 row_len=16, table=64, swa_kv=2 * 128 * 1024, swa_first_pos=16)
+
+
+def _attend_at(lib, window=128, **at):
+    """A small bf16 attention whose arrays lie apart, but for those named in `at`."""
+    P = csa.params(16, 1, window)
+    size = ctypes.c_size_t(0)
+    L = csa.csa_paged_layout_t(num_seqs=2, num_tokens=3, page_rows=16, max_pages=8, swa_cap=128)
+    assert lib.csa_paged_workspace_size(ctypes.byref(L), ctypes.byref(P), ctypes.byref(size)) == 0
+    ptr, end = {}, 4096
+    for n, bytes_ in dict(ATTENTION, ws=size.value).items():
+        ptr[n] = end
+        end += -(-bytes_ // 256) * 256 + 256
+    ptr.update({n: ptr[o] + d for n, (o, d) in at.items()})
+    for n in ("tok_seq", "tok_pos", "row_len", "table", "swa_kv", "swa_first_pos"):
+        setattr(L, n, ptr[n])
+    return lib.csa_paged_attention(ctypes.byref(L), ctypes.byref(P), end, 16, 16, ptr["q"], ptr["sinks"], 1,
+                                   ptr["out"], ptr["status"], ptr["ws"], size.value, None)
+
+
+@pytest.mark.parametrize("name", ["out", "ws", "status"])
+def test_attention_refuses_outputs_over_other_arrays(lib, name):
+    for other in ATTENTION:
+        if other == name:
+            continue
+        assert _attend_at(lib, **{name: (other, 0)}) == INVALID, other
+        if ATTENTION[other] > 256:      # one that begins inside another
+            assert _attend_at(lib, **{name: (other, 256)}) == INVALID, other
+
+
+def test_attention_takes_arrays_that_only_touch(lib):
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are not real")
+    assert _attend_at(lib) not in (0, INVALID)
+    assert _attend_at(lib, sinks=("out", ATTENTION["out"])) not in (0, INVALID)
+    # without a window the ring is not used, wherever it is said to be
+    assert _attend_at(lib, window=0, swa_kv=("out", 0)) not in (0, INVALID)
