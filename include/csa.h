@@ -419,6 +419,9 @@ csa_status_t csa_topk_noalloc(const csa_layout_t *layout, const csa_params_t *pa
  * sets CSA_DEV_BAD_LENGTH; ring positions that do not fit the pool set
  * CSA_DEV_BAD_LAYOUT.  table and free_ring then stay as they were, the maps
  * are all -1, the offsets 0 and the lengths those from before the step.
+ * A page number outside the pool, in a request's part of the table or among the
+ * free pages, sets CSA_DEV_BAD_INDEX where the step meets it: its new blocks
+ * get slot -1 (csa_paged_append skips them), the number itself moves on as it is.
  * Pages, window and lengths are counted per (ratio, page_rows): layers of
  * another ratio have a table and a plan of their own.  num_seqs <= 8192,
  * num_pages * page_rows, tok_cap and row_cap below 2^31, else

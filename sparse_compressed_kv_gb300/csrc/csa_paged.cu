@@ -189,6 +189,13 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
         P.tok_pos[i] = pos;
         P.swa_slot[i] = pos >= end - P.swa_cap ? static_cast<int64_t>(b) * P.swa_cap + A.swa_cap.mod64(pos) : -1;
     };
+    // a page number that the table or the ring should not hold
+    int wrong = 0;
+    auto known = [&](int32_t page) {
+        const bool ok = page >= 0 && page < N;
+        if (!ok) wrong = CSA_DEV_BAD_INDEX;
+        return ok;
+    };
     // new block k of request b, whose new pages start at place `need`
     auto put_row = [&](uint32_t i, int b, const Req &r, uint32_t k, uint32_t need) {
         const int64_t g = r.old_rows + k;
@@ -196,7 +203,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
         if (!CSA_CHECK(pg >= 0 && pg < P.max_pages && pg < r.pages, status)) return;
         const int32_t page = pg < r.old_pages ? P.table[static_cast<int64_t>(b) * P.max_pages + pg]
                                               : *ring(h0, need + (pg - r.old_pages));
-        P.row_slot[i] = static_cast<int64_t>(page) * P.page_rows + (g - static_cast<int64_t>(pg) * P.page_rows);
+        P.row_slot[i] = known(page) ? static_cast<int64_t>(page) * P.page_rows + (g - static_cast<int64_t>(pg) * P.page_rows)
+                                    : -1;
     };
     const bool few = most <= kPlanFew;
     const uint32_t step = gridDim.x * kPlanThreads, first = blockIdx.x * kPlanThreads + tid;
@@ -250,8 +258,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
             page[k] = P.table[static_cast<int64_t>(b) * P.max_pages + (i - off[b].rel)];
         }
 #pragma unroll
-        for (int k = 0; k < kPlanBatch; ++k)
-            if (i0 + k * step < total.rel) *ring(t0, i0 + k * step) = page[k];
+        for (int k = 0; k < kPlanBatch; ++k) {
+            if (i0 + k * step >= total.rel) break;
+            (void)known(page[k]);
+            *ring(t0, i0 + k * step) = page[k];
+        }
     }
     for (int64_t i = static_cast<int64_t>(total.tok) + first; i < P.tok_cap; i += step) {
         P.tok_seq[i] = -1;
@@ -259,6 +270,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
         P.swa_slot[i] = -1;
     }
     for (int64_t i = static_cast<int64_t>(total.row) + first; i < P.row_cap; i += step) P.row_slot[i] = -1;
+    raise_status(status, wrong);
     __threadfence();
 }
 

@@ -120,3 +120,47 @@ def test_serving_step_over_two_layers_of_interleaved_pages(cuda_device):
         lost = max(0, T - n - 15) < max(0, T - cap)
         assert int(status.item()) == (csa.DEV_MISSING_SWA if lost else 0)
         status.zero_()
+
+
+def run_plan(device, *, ratio, page_rows, swa_cap, **case):
+    t = H.plan_tensors(device, **case)
+    status = torch.zeros(1, dtype=torch.int32, device=device)
+    csa.csa_page_plan(csa.PagePlan(ratio=ratio, page_rows=page_rows, swa_cap=swa_cap, **t), status)
+    torch.cuda.synchronize()
+    want, bad = H.plan_reference(ratio=ratio, page_rows=page_rows, swa_cap=swa_cap, **case)
+    return {k: t[k].tolist() for k in want}, int(status.item()), want, bad
+
+
+@pytest.mark.parametrize("number", [-1, 9, 1 << 30, -(1 << 31)])
+@pytest.mark.parametrize("new", [6, 30], ids=["few", "many"])
+@pytest.mark.parametrize("where", ["old", "ring", "given-back"])
+def test_plan_page_numbers_outside_the_pool(cuda_device, where, new, number):
+    # request 0 holds 9 blocks in pages 0, 1, 2 (of 4 rows; the last holds one) and
+    # brings some; request 1 ends and gives back pages 3 and 4
+    table = [[0, 1, 2] + [-1] * 5, [3, 4] + [-1] * 6]
+    ring = [5, 6, 7, 8] + [-1] * 5
+    if where == "old":
+        table[0][2] = number
+    elif where == "ring":
+        ring[0] = number
+    else:
+        table[1][1] = number
+    case = dict(ratio=2, page_rows=4, swa_cap=8, seq_len=[18, 16], new_len=[new, -1], table=table, free_ring=ring,
+                free_pos=[0, 4], tok_cap=45, row_cap=25)
+    if where == "ring":
+        case["new_len"][0] = new = max(new, 8)          # reaches the ring's first page
+    got, status, want, bad = run_plan(cuda_device, **case)
+    assert bad == 0 and status == csa.DEV_BAD_INDEX
+    # the rows of that page have no slot; all else is as always, the number among it
+    want["row_slot"] = [s if 0 <= s < 9 * 4 else -1 for s in want["row_slot"]]
+    assert (-1 in want["row_slot"][:new // 2]) == (where != "given-back")
+    assert got == want
+
+
+def test_plan_leaves_other_numbers_alone(cuda_device):
+    # a full old page, a table behind the request's pages and a ring behind the free
+    # ones may hold anything
+    case = dict(ratio=2, page_rows=4, swa_cap=8, seq_len=[16, 0], new_len=[4, 0], table=[[99, -5, -6], [77, -1, 55]],
+                free_ring=[5, 1, -9, 1 << 30, 66, 7], free_pos=[0, 2], tok_cap=6, row_cap=4)
+    got, status, want, bad = run_plan(cuda_device, **case)
+    assert status == bad == 0 and got == want
