@@ -419,6 +419,14 @@ csa_status_t csa_topk_noalloc(const csa_layout_t *layout, const csa_params_t *pa
  * sets CSA_DEV_BAD_LENGTH; ring positions that do not fit the pool set
  * CSA_DEV_BAD_LAYOUT.  table and free_ring then stay as they were, the maps
  * are all -1, the offsets 0 and the lengths those from before the step.
+ * A page has one owner: the plan counts no holders.  The attention reads a
+ * page through any number of table rows, so requests may share the full pages
+ * of a common prefix (not a page that is still being filled: each would write
+ * its rows there).  But new_len = -1 gives every page of the request back,
+ * shared or not, and the ring would hand it out while others read it, or twice
+ * when they end.  A request that shares pages is ended by the caller instead:
+ * its seq_len set to 0, and those of its pages that no other request holds
+ * written behind the end of the ring (free_pos[1] moved on by as many).
  * A page number outside the pool, in a request's part of the table or among the
  * free pages, sets CSA_DEV_BAD_INDEX where the step meets it: its new blocks
  * get slot -1 (csa_paged_append skips them), the number itself moves on as it is.

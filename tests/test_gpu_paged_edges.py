@@ -164,3 +164,26 @@ def test_plan_leaves_other_numbers_alone(cuda_device):
                 free_ring=[5, 1, -9, 1 << 30, 66, 7], free_pos=[0, 2], tok_cap=6, row_cap=4)
     got, status, want, bad = run_plan(cuda_device, **case)
     assert status == bad == 0 and got == want
+
+
+def test_plan_with_a_shared_prefix(cuda_device):
+    # two requests share the full pages 0 and 1; one of them ends as the header says:
+    # by the caller, who puts back what the other does not hold
+    step = dict(ratio=1, page_rows=2, swa_cap=4, tok_cap=4, row_cap=4)
+    table, ring, N = [[0, 1, 2, -1], [0, 1, 3, -1]], [4, 5, 6, 7, -1, -1, -1, -1], 8
+    got, status, want, bad = run_plan(cuda_device, seq_len=[6, 5], new_len=[1, 2], table=table, free_ring=ring,
+                                      free_pos=[0, 4], **step)
+    assert status == bad == 0 and got == want
+    assert len(set(got["row_slot"][:3])) == 3 and got["table"] == [[0, 1, 2, 4], [0, 1, 3, 5]]
+    head, tail = got["free_pos_out"]
+    ring, own = got["free_ring"], [3, 5]
+    for page in own:
+        ring[tail % N] = page
+        tail += 1
+    got, status, want, bad = run_plan(cuda_device, seq_len=[got["seq_len_out"][0], 0], new_len=[1, 3],
+                                      table=got["table"], free_ring=ring, free_pos=[head, tail], **step)
+    assert status == bad == 0 and got == want
+    head, tail = got["free_pos_out"]
+    held = got["table"][0][:4] + got["table"][1][:2]
+    free = [got["free_ring"][x % N] for x in range(head, tail)]
+    assert sorted(held + free) == list(range(N))
