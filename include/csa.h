@@ -79,8 +79,8 @@ typedef enum {
  * The library's kernels may read tok_seq, tok_pos, comp_off and
  * swa_first_pos as soon as they start, while a preceding kernel that allows
  * programmatic dependent launch may still run: these arrays must not be
- * written by such a kernel (the library's own kernels never write them; a
- * copy, or a kernel without that launch attribute, completes before the
+ * written by such a kernel (of the library's own, csa_page_plan alone writes
+ * them, and it does not allow that launch; a copy, or a kernel without that launch attribute, completes before the
  * next one starts).  Everything else a call reads (queries, weights, keys,
  * rows, the window ring) is read only after the preceding kernel has
  * finished. */
@@ -499,7 +499,12 @@ csa_status_t csa_paged_append(const csa_append_job_t *jobs /* (host) */, int32_t
  *   swa_kv / swa_first_pos may be NULL).
  * The layout's arrays have the meaning that csa_page_plan gives them; a
  * token with tok_seq = -1 is padding and its output is left as it was.  A
- * token without any row gets zeros, with or without a sink.
+ * token without any row gets zeros, with or without a sink; so does one with
+ * another tok_seq outside [0, B) or a negative tok_pos (CSA_DEV_BAD_LAYOUT).
+ * A window position that the ring has lost (below swa_first_pos) sets
+ * CSA_DEV_MISSING_SWA and is skipped: where a sequence brings n tokens in a
+ * step, all appended before the call, its ring needs swa_cap >= window + n - 1
+ * for the first of them to see its whole window.
  *   cache bf16, num_pages pages of page_rows rows of hd values, page_stride
  *     rows apart; only the rows named above are read into the result: the
  *     rest of the pool may hold anything, NaN included.
@@ -537,7 +542,7 @@ typedef struct {
     const int64_t *row_len;       /* [B] compressed rows held */
     const int32_t *table;         /* [B, max_pages] */
     const void *swa_kv;           /* bf16 [B, swa_cap, hd] */
-    int32_t swa_cap;              /* (host) >= window */
+    int32_t swa_cap;              /* (host) >= window; >= window + n - 1 for n tokens a step */
     const int64_t *swa_first_pos; /* [B] */
 } csa_paged_layout_t;
 

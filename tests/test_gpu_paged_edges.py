@@ -187,3 +187,17 @@ def test_plan_with_a_shared_prefix(cuda_device):
     held = got["table"][0][:4] + got["table"][1][:2]
     free = [got["free_ring"][x % N] for x in range(head, tail)]
     assert sorted(held + free) == list(range(N))
+
+
+@pytest.mark.parametrize("n", [1, 4, 40])
+def test_attention_ring_for_several_tokens_a_step(cuda_device, n):
+    # window + n - 1 slots hold every window of a step; one less loses a row of the first
+    W, end = 20, 500 + n
+    tokens = [(0, 500 + i) for i in range(n)]
+    for cap, want in ((W + n - 1, 0), (W + n - 2, csa.DEV_MISSING_SWA)):
+        if cap < W:
+            continue
+        p = H.Paged(70 + n, row_len=[end // 4], tokens=tokens, heads=16, window=W, swa_cap=cap)
+        got, status = p.run(cuda_device, F32)
+        assert status == want
+        H.check(got, p.reference(lambda t: {(500 + t) // 4} if want and t == 0 else None), F32)
