@@ -384,7 +384,11 @@ def _device_stream(fn: str, index: int, stream=None) -> int:
     torch.cuda.current_stream's object alone would cost three.)"""
     if index != torch.cuda.current_device():
         raise ValueError(f"{fn}: tensors live on cuda:{index}, not on the current device")
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device_index != index:
+        raise ValueError(f"{fn}: the stream belongs to cuda:{stream.device_index}, not cuda:{index}")
+    return stream.cuda_stream
 
 
 def _ptr(t, index: int, contiguous=True) -> int:
@@ -482,7 +486,12 @@ class AppendJobs:
     """Up to four AppendJob for one launch."""
 
     def __init__(self, jobs):
-        self.jobs, self.device = list(jobs), jobs[0].device
+        self.jobs = list(jobs)
+        if not 1 <= len(self.jobs) <= MAX_APPEND_JOBS:
+            raise ValueError(f"1 to {MAX_APPEND_JOBS} jobs, got {len(self.jobs)}")
+        self.device = self.jobs[0].device
+        if any(j.device != self.device for j in self.jobs):
+            raise ValueError(f"jobs on devices {[j.device for j in self.jobs]}: one call runs on one")
         self.c = (csa_append_job_t * len(self.jobs))(*[j.c for j in self.jobs])
 
 
@@ -507,6 +516,8 @@ class PagedLayout:
             if swa_kv.dim() != 3 or swa_kv.shape[0] != B or swa_kv.shape[2] != 512:
                 raise ValueError(f"swa_kv must have shape ({B}, swa_cap, 512), "
                                  f"got {tuple(swa_kv.shape)}")
+            if swa_first_pos is None:
+                raise ValueError("swa_kv needs swa_first_pos")
             ring = dict(swa_kv=_arg("swa_kv", swa_kv, torch.bfloat16), swa_cap=int(swa_kv.shape[1]),
                         swa_first_pos=_arg("swa_first_pos", swa_first_pos, torch.int64, (B,)))
         self.tensors = (tok_seq, tok_pos, row_len, table, swa_kv, swa_first_pos)

@@ -129,3 +129,34 @@ def test_attention_takes_arrays_that_only_touch(lib):
     assert _attend_at(lib, sinks=("out", ATTENTION["out"])) not in (0, INVALID)
     # without a window the ring is not used, wherever it is said to be
     assert _attend_at(lib, window=0, swa_kv=("out", 0)) not in (0, INVALID)
+
+
+def test_binding_refuses_a_ring_without_its_first_positions():
+    i32, i64 = torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int64)
+    with pytest.raises(ValueError, match="swa_first_pos"):
+        csa.PagedLayout(i32, i64, i64, torch.zeros(1, 1, dtype=torch.int32), 16,
+                        swa_kv=torch.zeros(1, 128, 512, dtype=torch.bfloat16))
+
+
+class _Job:
+    def __init__(self, device):
+        self.device, self.c = device, csa.csa_append_job_t()
+
+
+def test_binding_refuses_jobs_that_are_not_one_call():
+    assert csa.AppendJobs(iter([_Job(0), _Job(0)])).device == 0
+    for jobs in ([], [_Job(0)] * 5, [_Job(0), _Job(1)]):
+        with pytest.raises(ValueError, match="job"):
+            csa.AppendJobs(jobs)
+
+
+def test_binding_refuses_a_stream_of_another_device(monkeypatch):
+    class Stream:
+        def __init__(self, index):
+            self.device_index, self.cuda_stream = index, 77
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert csa._device_stream("f", 0, Stream(0)) == 77
+    with pytest.raises(ValueError, match="stream"):
+        csa._device_stream("f", 0, Stream(1))
+    with pytest.raises(ValueError, match="current device"):
+        csa._device_stream("f", 1, Stream(1))
