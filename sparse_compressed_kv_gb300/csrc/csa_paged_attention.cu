@@ -1082,8 +1082,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float f = 1.f;
                         if (last && !cut) {
                             float zs = l;
-                            if (A.sinks && hv && m_ref != -INFINITY) zs += exp2f(A.sinks[h0 + hl] * kLog2e - m_ref);
-                            f = (zs > 0.f && l > 0.f) ? 1.f / zs : 0.f;
+                            if (A.sinks && hv) zs += exp2f(A.sinks[h0 + hl] * kLog2e - m_ref);
+                            f = m_ref == -INFINITY ? 0.f : 1.f / zs;     // (a sink of NaN: NaN)
                         }
                         S.fin[e][hl] = f;
                         if (last && cut && dt0 == 0)
@@ -1131,6 +1131,10 @@ __device__ __forceinline__ JoinEntry join_entry(const PagedArgs &A) {
     if (A.L.num_tokens > static_cast<int>(gridDim.x)) e.t = A.meta[gridDim.x + blockIdx.x].x;
     return e;
 }
+
+// The sink's term 2^(sink - M) of a sum scaled to M >= sink (log2 units): 1 where
+// it is the maximum, an infinite one too; NaN stays NaN.
+__device__ __forceinline__ float sink_term(float sink, float M) { return sink == M ? 1.f : exp2f(sink - M); }
 
 template <bool kBf16>
 __device__ __forceinline__ void join_store(const PagedArgs &A, int64_t at, float x) {
@@ -1195,8 +1199,8 @@ __global__ void __launch_bounds__(kCols * kDeepSub) join_deep_kernel(const Paged
         for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (lane == 0) {
             const bool some = M != -INFINITY;
-            if (some && sink != -INFINITY) z += exp2f(sink - Mall);
-            inv_z[warp] = some && z > 0.f ? 1.f / z : 0.f;
+            if (some) z += sink_term(sink, Mall);
+            inv_z[warp] = some ? 1.f / z : 0.f;
         }
     }
     __syncthreads();
@@ -1274,7 +1278,7 @@ __global__ void __launch_bounds__(256) join_wide_kernel(const PagedArgs A) {
         for (int k = 1; k < kNear; ++k) M = fmaxf(M, x[k].x);
         for (int k = kNear; k < ns; ++k) M = fmaxf(M, __ldcg(ml + J.slot(k) * groups * kHG).x);
         const float Mall = fmaxf(M, sink);
-        float z = M != -INFINITY && sink != -INFINITY ? exp2f(sink - Mall) : 0.f;
+        float z = M != -INFINITY ? sink_term(sink, Mall) : 0.f;
         auto put = [&](int k, float2 y) {
             const float w = y.x == -INFINITY ? 0.f : exp2f(y.x - Mall);
             reinterpret_cast<float *>(wgt[k])[tid] = w;
@@ -1284,7 +1288,7 @@ __global__ void __launch_bounds__(256) join_wide_kernel(const PagedArgs A) {
         for (int k = 0; k < kNear; ++k)
             if (k < ns) put(k, x[k]);
         for (int k = kNear; k < ns; ++k) put(k, __ldcg(ml + J.slot(k) * groups * kHG));
-        const float f = M != -INFINITY && z > 0.f ? 1.f / z : 0.f;
+        const float f = M != -INFINITY ? 1.f / z : 0.f;
         for (int k = 0; k < ns; ++k) reinterpret_cast<float *>(wgt[k])[tid] *= f;
     }
     __syncthreads();

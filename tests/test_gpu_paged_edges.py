@@ -201,3 +201,25 @@ def test_attention_ring_for_several_tokens_a_step(cuda_device, n):
         got, status = p.run(cuda_device, F32)
         assert status == want
         H.check(got, p.reference(lambda t: {(500 + t) // 4} if want and t == 0 else None), F32)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("row_len,tokens", [
+    ([300], [(0, 1200)]),                                    # whole tokens
+    ([20000], [(0, 80000)]),                                 # one token in many parts
+    ([3000] * 14, [(b, 12000) for b in range(14)]),          # many tokens in a few parts
+    ([9000] * 3, [(b, 36000) for b in range(3)]),            # a few tokens in many parts
+], ids=["whole", "one", "many", "few"])
+def test_attention_sinks_of_any_value(cuda_device, row_len, tokens, dtype):
+    p = H.Paged(80, row_len=row_len, tokens=tokens, heads=9, page_rows=64, sinks=True)
+    p.sinks[:] = torch.tensor([0.0, float("nan"), float("inf"), -float("inf"), 30.0, 80.0, -80.0, -1e30, 1e30])
+    got, status = p.run(cuda_device, dtype)
+    assert status == 0
+    got, ref = got.double().cpu(), p.reference()
+    assert got[:, 1].isnan().all() and ref[:, 1].isnan().all()
+    for h in (2, 8):
+        assert (got[:, h] == 0).all() and (ref[:, h] == 0).all()
+    # the sink's logit has one rounding of its own, 2^-24 of 80 times log2 e or less
+    for h in (0, 3, 4, 5, 6, 7):
+        err = (got[:, h] - ref[:, h]).norm(dim=1)
+        assert (err <= (H.REL[dtype] + 2 * 80 * 2 ** -23) * ref[:, h].norm(dim=1)).all(), h
