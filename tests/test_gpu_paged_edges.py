@@ -223,3 +223,158 @@ def test_attention_sinks_of_any_value(cuda_device, row_len, tokens, dtype):
     for h in (0, 3, 4, 5, 6, 7):
         err = (got[:, h] - ref[:, h]).norm(dim=1)
         assert (err <= (H.REL[dtype] + 2 * 80 * 2 ** -23) * ref[:, h].norm(dim=1)).all(), h
+
+
+# ---------------------------------------------------------------- long loops, wide sums
+
+def test_append_of_more_pieces_than_a_pass_of_the_grid(cuda_device):
+    # 1.25 M pieces of 16 bytes are one pass; the second pass begins inside a pair
+    dev, P = cuda_device, 16
+    g = torch.Generator(device=dev).manual_seed(1)
+    jobs, caches, wants = [], [], []
+    for n, width in ((9000, 80), (25000, 1024), (30000, 256)):
+        rows = torch.randint(0, 256, (n, width), dtype=torch.uint8, device=dev, generator=g)
+        pages = -(-n // P) + 3
+        slots = torch.randperm(pages * P, device=dev, generator=g)[:n]
+        slots[torch.rand(n, device=dev, generator=g) < 0.1] = -1
+        cache = torch.randint(0, 256, (pages, P + 1, width), dtype=torch.uint8, device=dev, generator=g)
+        want, keep = cache.clone(), slots >= 0
+        want[slots[keep] // P, slots[keep] % P] = rows[keep]
+        jobs.append(csa.AppendJob(rows, slots, cache, P))
+        caches.append(cache)
+        wants.append(want)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    csa.csa_paged_append(csa.AppendJobs(jobs), status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for c, w in zip(caches, wants):
+        assert torch.equal(c, w)
+
+
+def test_plan_gives_back_more_pages_than_a_pass_of_the_grid(cuda_device):
+    seq_len = [60000, 5, 70001, 50000]
+    table, ring, pos = H.pool(90, seq_len, ratio=1, page_rows=1, max_pages=70010, extra=40, head=123456)
+    got, status, want, bad = run_plan(cuda_device, ratio=1, page_rows=1, swa_cap=16, seq_len=seq_len,
+                                      new_len=[-1, 9, -1, -1], table=table, free_ring=ring, free_pos=pos, tok_cap=12,
+                                      row_cap=12)
+    assert status == bad == 0 and got == want
+
+
+@pytest.mark.parametrize("B,new", [(3, [(1 << 31) - 1, (1 << 31) - 1, 7]), (8192, [1 << 19] * 8192)], ids=["few", "many"])
+def test_plan_refuses_token_sums_past_32_bits(cuda_device, B, new):
+    # the sum is 5 or 0 in 32 bits, what the maps would hold; blocks and pages are few
+    assert sum(new) % (1 << 32) in (0, 5) and sum(new) >= 1 << 32
+    table = [[-1, -1] for _ in range(B)]
+    got, status, want, bad = run_plan(cuda_device, ratio=1 << 30, page_rows=1, swa_cap=16, seq_len=[0] * B, new_len=new,
+                                      table=table, free_ring=[0, 1, 2, 3], free_pos=[0, 4], tok_cap=14, row_cap=4)
+    assert status == bad == csa.DEV_CAPACITY and got == want
+    assert got["seq_len_out"] == [0] * B and got["tok_seq"] == [-1] * 14
+
+
+def test_plan_refuses_sums_of_given_back_pages_past_32_bits(cuda_device):
+    # 8192 requests that hold 2^19 pages each: 0 in 32 bits.  (The table is 17 GB that
+    # nothing reads, since the step is refused.)
+    dev, B, n = cuda_device, 8192, 1 << 19
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB")
+    t = H.plan_tensors(dev, seq_len=[n] * B, new_len=[-1] * B, table=[[0]] * B, free_ring=[3, 2, 1, 0], free_pos=[1, 2],
+                       tok_cap=3, row_cap=2)
+    t["table"] = torch.empty(B, n, dtype=torch.int32, device=dev)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    csa.csa_page_plan(csa.PagePlan(ratio=1, page_rows=1, swa_cap=16, **t), status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == csa.DEV_BAD_LAYOUT
+    assert t["free_ring"].tolist() == [3, 2, 1, 0] and t["free_pos_out"].tolist() == [1, 2]
+    assert (t["seq_len_out"] == n).all() and (t["row_len"] == n).all() and (t["tok_seq"] == -1).all()
+    assert (t["tok_off"] == 0).all() and (t["row_off"] == 0).all() and (t["row_slot"] == -1).all()
+
+
+# ---------------------------------------------------------------- every weight by itself
+
+@pytest.mark.parametrize("T,n,heads", [(1, 512, 64), (40, 512, 64), (100, 512, 128), (330, 512, 64), (160, 4096, 64)], ids=str)
+def test_attention_weights_element_by_element(cuda_device, T, n, heads):
+    # Rows with one value each, so that an f32 output's column is the sum of n / 512
+    # weights: a term of a weight that is lost in some tile, slice of rows or head
+    # shows as 2^-8.  Relative bounds: two bf16 terms 2^-16; the logit (at most 6: a
+    # product by the scale, a difference, 2^-24 of 9 each) and exp2 together 2^-20;
+    # each sum of the denominator and of up to 16 terms a column, the partials and
+    # the quotient, half a step to a step (2^-23) each: 40 of them.
+    dev = cuda_device
+    g = torch.Generator(device=dev).manual_seed(T + n)
+    column = torch.cat([torch.randperm(H.HD, device=dev, generator=g) for _ in range(n // H.HD)])
+    pages = n // 16
+    table = torch.randperm(pages, device=dev, generator=g).int()[None]
+    rows = torch.zeros(n, H.HD, dtype=BF16, device=dev)
+    rows[torch.arange(n, device=dev), column] = 8.0
+    cache = torch.empty(pages, 16, H.HD, dtype=BF16, device=dev)
+    j = torch.arange(n, device=dev)
+    cache[table[0, j // 16].long(), j % 16] = rows
+    q = torch.randn(T, heads, H.HD, device=dev, generator=g).clamp_(-5.9, 5.9).to(BF16)
+    layout = csa.PagedLayout(torch.zeros(T, dtype=torch.int32, device=dev),
+                             torch.full((T,), 4 * n, dtype=torch.int64, device=dev), torch.tensor([n], device=dev),
+                             table, 16)
+    prm = csa.params(heads, 1, 0, 4, scale=0.125)
+    out, status = torch.empty(T, heads, H.HD, device=dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    csa.csa_paged_attention(layout, prm, cache, q, out, status, csa.paged_workspace(layout, prm))
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    l = q.double()[:, :, column]
+    assert float(l.abs().max()) < 6
+    w = torch.softmax(l, 2)
+    ref = torch.zeros(T, heads, H.HD, dtype=torch.float64, device=dev).index_add_(2, column, 8 * w)
+    err = ((out.double() - ref).abs() / ref).max()
+    assert float(err) <= 2 ** -16 + 2 ** -20 + 40 * 2 ** -23, f"off by {float(err):.3e}"
+
+
+# ---------------------------------------------------------------- prompts
+
+@pytest.mark.parametrize("T,ctx,ratio,heads,dtype", [
+    (700, 20000, 4, 64, F32), (1500, 6000, 4, 128, BF16), (4096, 30000, 128, 64, F32), (8192, 0, 4, 16, BF16),
+    (8192, 1, 128, 8, F32),
+], ids=str)
+def test_attention_of_a_prompt_chunk(cuda_device, T, ctx, ratio, heads, dtype):
+    # one request's chunk: every token sees the rows before it and its own window
+    dev, P, W = cuda_device, 64, 128
+    n, cap = (ctx + T) // ratio, W + T - 1
+    g = torch.Generator(device=dev).manual_seed(T + ctx)
+    pages = max(1, -(-n // P))
+    table = torch.randperm(pages, device=dev, generator=g).int()[None]
+    cache = torch.full((pages, P, H.HD), float("nan"), dtype=BF16, device=dev)
+    rows = torch.randn(n, H.HD, device=dev, generator=g).to(BF16)
+    j = torch.arange(n, device=dev)
+    cache[table[0, j // P].long(), j % P] = rows
+    ring = torch.randn(1, cap, H.HD, device=dev, generator=g).to(BF16)
+    q = torch.randn(T, heads, H.HD, device=dev, generator=g).to(BF16)
+    layout = csa.PagedLayout(torch.zeros(T, dtype=torch.int32, device=dev), ctx + torch.arange(T, device=dev),
+                             torch.tensor([n], device=dev), table, P, ring,
+                             torch.tensor([max(0, ctx + T - cap)], device=dev))
+    prm = csa.params(heads, 1, W, ratio)
+    out = torch.full((T, heads, H.HD), float("nan"), device=dev, dtype=dtype)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    csa.csa_paged_attention(layout, prm, cache, q, out, status, csa.paged_workspace(layout, prm))
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and bool(out.isfinite().all())
+    for t in sorted({0, 1, 127, 128, T - 1} | set(range(0, T, T // 23))):
+        p = ctx + t
+        x = torch.arange(max(0, p - W + 1), p + 1, device=dev)
+        every = torch.cat([rows[:p // ratio], ring[0, x % cap]]).double()
+        ref = torch.softmax(prm.scale * q[t].double() @ every.T, 1) @ every
+        assert (out[t].double() - ref).norm() <= H.REL[dtype] * ref.norm(), t
+
+
+def test_these_calls_under_the_checked_build(cuda_device):
+    """The library with internal bounds checks: a failed one sets a status bit, and
+    every test wants the status it expects."""
+    import os
+    import subprocess
+    import sys
+
+    from sparse_compressed_kv_gb300 import build as B
+
+    B.build(checks=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider",
+                        os.path.join("tests", "test_gpu_paged_edges.py"), "-k",
+                        "head_counts or interleaved or numbers or pieces or gives_back or prompt or element"],
+                       cwd=root, env=dict(os.environ, CSA_CHECKS="1"), capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and " passed" in r.stdout, (r.stdout + r.stderr)[-3000:]
