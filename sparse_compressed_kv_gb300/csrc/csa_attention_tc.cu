@@ -69,8 +69,6 @@ constexpr int kPBytes = kHG * kChunk * 2;      // 8 KiB: one bf16 term of P
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 0;                       // S buffers: columns 0 .. 127
 constexpr int kOCol = 128;                     // O^T: up to 4 tiles x 64 heads
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleAbove = 8.f;           // log2 units
 
 struct TcParams {
     RowSource R;
@@ -171,58 +169,6 @@ __device__ __forceinline__ void tc_token_finish(const RowSource &R, int t, TcTok
     if (R.no_selected) ns = 0;
     k.nsel = ns;
     k.wslot = (ns + 3) & ~3;
-}
-
-__device__ __forceinline__ void tmem_ld16_raw(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
-// 16 lanes x 16 columns twice: threads 0..15 read lanes 0..15 of the quarter
-// at columns c..c+15, threads 16..31 the same lanes at columns c+32..c+47
-__device__ __forceinline__ void tmem_ld16x2_raw(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16], 32;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
-// 2^x with the hardware's approximate exponential (relative error about
-// 2^-22, far below the bf16 terms P is stored in); 2^-inf = 0.
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-
-// Shared-memory descriptor with explicit leading / stride byte offsets
-// (128-byte swizzle).  K-major: the stride is the step between 8-row groups.
-// MN-major: the leading offset is the step between 64-element column boxes,
-// the stride the step between 8-row groups of the K dimension.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-    d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(2u) << 61;
-    return d;
-}
-
-// kind::f16, bf16 x bf16 -> f32, M x N, A transposed (MN-major) or not.
-template <int M, int N, bool kTransA>
-__device__ __forceinline__ constexpr uint32_t idesc_bf16() {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((kTransA ? 1u : 0u) << 15) |
-           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // kDT: 128-column tiles of the output this CTA owns (4: all 512 columns;

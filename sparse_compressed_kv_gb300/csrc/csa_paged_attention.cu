@@ -79,8 +79,6 @@ template <int kTerms>
 __device__ __forceinline__ constexpr uint32_t o_col(int dd) {
     return kOCol + kHG * (dd + (dd < kWide<kTerms> ? dd : kWide<kTerms>));
 }
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleAbove = 8.f;            // log2 units
 constexpr int kMaxRec = 64;                     // segments a CTA lists at a time
 constexpr int kMaxCtas = 152;                   // CTAs of the grid at most (sizes the workspace)
 constexpr int kSegCost = 4;                     // a segment's epilogue, in chunks (3: 128 contexts of 512 rows 30.3
@@ -174,50 +172,13 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *m, int
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16_raw(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
-// threads 0..15: lanes 0..15 of the quarter, columns c ..; threads 16..31: the
-// same lanes, columns c + 32 .. (16 of them) and c + 8 .. (8)
-__device__ __forceinline__ void tmem_ld16x2_raw(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16], 32;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
+// tmem_ld16x2_raw's lanes, at columns c .. and c + 8 .. (8 each)
 __device__ __forceinline__ void tmem_ld8x2_raw(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8], 8;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7])
         : "r"(taddr));
-}
-
-// 2^x, relative error about 2^-22; 2^-inf = 0
-__device__ __forceinline__ float fast_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-    d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-    d |= static_cast<uint64_t>(1u) << 46;
-    d |= static_cast<uint64_t>(2u) << 61;
-    return d;
 }
 
 // Unswizzled K-major operand: atoms of 8 rows x 16 bytes, 128 contiguous bytes
@@ -229,12 +190,6 @@ __device__ __forceinline__ uint64_t atom_desc(uint32_t saddr, uint32_t lbo, uint
 // a byte offset as a step of a descriptor's start-address field (every shared
 // address is below 256 KiB, so the field never carries)
 __device__ __forceinline__ constexpr uint64_t off(uint32_t bytes) { return bytes >> 4; }
-
-template <int M, int N, bool kTransA>
-__device__ __forceinline__ constexpr uint32_t idesc_bf16() {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((kTransA ? 1u : 0u) << 15) |
-           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
 
 // What token t attends: b < 0 for padding, n = near = 0 for a bad token.
 // `per` tokens a sequence is the guess by which the sequence's length is
