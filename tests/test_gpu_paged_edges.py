@@ -362,6 +362,77 @@ def test_attention_of_a_prompt_chunk(cuda_device, T, ctx, ratio, heads, dtype):
         assert (out[t].double() - ref).norm() <= H.REL[dtype] * ref.norm(), t
 
 
+# ---------------------------------------------------------------- nothing to do, or next to it
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 5, 151, 152, 153, 400, 8192])
+def test_attention_of_padding_alone(cuda_device, T, dtype):
+    p = H.Paged(100, row_len=[300, 0], tokens=[(-1, -1)] * T, heads=3, page_rows=8)
+    got, status = p.run(cuda_device, dtype)
+    assert status == 0 and (got == 7).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 60, 152, 153, 400, 2000])
+def test_attention_of_tokens_without_rows(cuda_device, T, dtype):
+    p = H.Paged(101, row_len=[300, 0], tokens=[(t % 2, 3) for t in range(T)], heads=66, page_rows=8, window=0,
+                sinks=True)
+    got, status = p.run(cuda_device, dtype)
+    assert status == 0 and (got == 0).all()
+
+
+def test_attention_without_tokens(cuda_device):
+    p = H.Paged(102, row_len=[30], tokens=[], heads=3, page_rows=8)
+    got, status = p.run(cuda_device, F32)
+    assert status == 0 and got.numel() == 0
+
+
+@pytest.mark.parametrize("page_rows", [1, 2, 8])
+def test_attention_over_a_pool_of_one_page(cuda_device, page_rows):
+    p = H.Paged(103, row_len=[page_rows], tokens=[(0, 4 * page_rows + 1)], heads=2, page_rows=page_rows, spare_pages=0,
+                window=3)
+    assert p.cache.shape[0] == 1
+    got, status = p.run(cuda_device, F32)
+    assert status == 0
+    H.check(got, p.reference(), F32)
+
+
+def test_a_refused_step_leaves_everything(cuda_device):
+    # too few free pages: the maps are empty, so the append writes nothing and the
+    # attention leaves its output, captured or not
+    dev, P = cuda_device, 4
+    t = H.plan_tensors(dev, seq_len=[6, 2], new_len=[30, 1], table=[[0] + [-1] * 9, [-1] * 10],
+                       free_ring=[1, 2, -1], free_pos=[0, 2], tok_cap=40, row_cap=20)
+    plan = csa.PagePlan(ratio=2, page_rows=P, swa_cap=16, **t)
+    pool = torch.full((3, P, H.HD), float("nan"), dtype=BF16, device=dev)
+    ring = torch.full((2, 16, H.HD), float("nan"), dtype=BF16, device=dev)
+    jobs = csa.AppendJobs([csa.AppendJob(torch.ones(20, H.HD, dtype=BF16, device=dev), t["row_slot"], pool, P),
+                           csa.AppendJob(torch.ones(40, H.HD, dtype=BF16, device=dev), t["swa_slot"], ring, 16)])
+    layout = csa.PagedLayout(t["tok_seq"], t["tok_pos"], t["row_len"], t["table"], P, ring, t["swa_first_pos"])
+    prm = csa.params(5, 1, 8, 2)
+    q = torch.randn(40, 5, H.HD, device=dev).to(BF16)
+    out, ws = torch.full((40, 5, H.HD), 7.0, device=dev), csa.paged_workspace(layout, prm)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def step():
+        csa.csa_page_plan(plan, status)
+        csa.csa_paged_append(jobs, status)
+        csa.csa_paged_attention(layout, prm, pool, q, out, status, ws)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for again in (lambda: None, g.replay):
+        again()
+        torch.cuda.synchronize()
+        assert int(status.item()) == csa.DEV_CAPACITY
+        assert pool.isnan().all() and ring.isnan().all() and (out == 7).all()
+        assert t["seq_len_out"].tolist() == [6, 2] and t["free_ring"].tolist() == [1, 2, -1]
+        status.zero_()
+
+
 def test_these_calls_under_the_checked_build(cuda_device):
     """The library with internal bounds checks: a failed one sets a status bit, and
     every test wants the status it expects."""
