@@ -66,11 +66,16 @@ typedef enum {
 } csa_status_t;
 
 /* Bits OR-ed into *dev_status by the kernels. */
-#define CSA_DEV_BAD_INDEX   0x01  /* idx outside [0, n_vis) for a selected slot */
+#define CSA_DEV_BAD_INDEX   0x01  /* idx outside [0, n_vis) for a selected slot; a page
+                                     or slot outside its pool */
 #define CSA_DEV_MISSING_SWA 0x02  /* a window position below swa_first_pos */
-#define CSA_DEV_BAD_LAYOUT  0x04  /* tok_seq outside [0,B), tok_pos < 0, bad comp_off */
-#define CSA_DEV_CAPACITY    0x08  /* a sequence holds more blocks than max_comp_rows */
-#define CSA_DEV_BAD_LENGTH  0x10  /* kv_len outside [0, top_k + window] */
+#define CSA_DEV_BAD_LAYOUT  0x04  /* tok_seq outside [0,B), tok_pos < 0, bad comp_off,
+                                     ring positions that do not fit the pool */
+#define CSA_DEV_CAPACITY    0x08  /* a sequence holds more blocks than max_comp_rows
+                                     (or its table has room for); a plan's step
+                                     needs more than there is */
+#define CSA_DEV_BAD_LENGTH  0x10  /* kv_len outside [0, top_k + window]; a plan's
+                                     length outside [0, 2^48), a negative row_len */
 #define CSA_DEV_TIMEOUT     0x20  /* a bounded wait inside a kernel gave up */
 #define CSA_DEV_CHECK       0x40  /* libcsa_checks.so only: an index inside the library
                                      left its array; the access was skipped */
@@ -518,6 +523,11 @@ csa_status_t csa_paged_append(const csa_append_job_t *jobs /* (host) */, int32_t
  * n_ih, ihd and top_k of params are not used.  Rows times weights are summed
  * in f32; for an f32 output the weights enter as two bf16 terms (relative
  * 2^-16), for a bf16 output as one (2^-8, as the output itself is rounded).
+ * The sums are the tensor cores', which drop what lies below the last place of
+ * the running sum; every 2,544 rows at most (f32 output; 32,736 for bf16) they
+ * are added, rounded, to a sum in f32.  For random rows an f32 output is off by
+ * 1e-6 to 4e-6 from float64 (relative, 2-norm), a bf16 output by 1.7e-3 to 2.2e-3
+ * (rounding the exact value to bf16: 1.7e-3).
  * A table entry outside the pool sets CSA_DEV_BAD_INDEX and its rows are
  * skipped; row_len above max_pages * page_rows sets CSA_DEV_CAPACITY and is
  * cut there; a negative one sets CSA_DEV_BAD_LENGTH (read as 0).

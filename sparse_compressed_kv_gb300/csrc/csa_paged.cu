@@ -19,9 +19,9 @@ namespace {
 // several requests, divisions by products, 32-bit sums.  In a decode step,
 // where every request brings a few tokens, the thread that has a request writes
 // all of its entries; with prompts among them each output entry is computed by
-// itself, its request found by bisection.  32 requests 3.9 us, 1,024 requests
-// 5.9 us, 256 requests with 77K tokens of prompts 6.8 us (an empty launch in a
-// stream takes about 2).
+// itself, its request found by bisection.  Replayed from a graph 32 requests take
+// 3.9 us, 1,024 requests 5.9, 256 requests with 77K tokens of prompts 6.9 (an
+// empty launch about 2); called in a stream 4.3, 5.8 and 6.8.
 constexpr int kPlanThreads = 256;
 constexpr int kPlanBatch = 4;     // requests a thread loads at a time
 constexpr int kPlanMaxSeqs = 8192;
@@ -293,8 +293,9 @@ struct AppendArgs {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendPer = 4;     // pieces a thread has in flight
 
-// A plain copy: bound by DRAM when large (354 MB in 58.4 us: 89% of the copy
-// rate), by two round trips when small (2.2 us).  The 16-byte pieces of all pairs are one index range; a
+// A plain copy: bound by DRAM when large (354 MB in 57.9 us: 90% of the copy
+// rate), by two round trips when small (2.2 us replayed from a graph, 4.1 called
+// in a stream).  The 16-byte pieces of all pairs are one index range; a
 // thread loads four pieces and their slots before it stores the first.
 // Index arithmetic is 32-bit inside a pair: in 64 bits its divisions, four a
 // piece, took longer than the copy (79.8 us).

@@ -31,11 +31,11 @@
 // sums of thousands of rows drift; at least every kFlush chunks O^T is added,
 // rounded, into the CTA's own f32 partial and starts again from zero.
 //
-// Bound by: DRAM where a CTA has tens of chunks (32 ragged contexts, 545 MB,
+// Bound by (times replayed from a graph): DRAM where a CTA has tens of chunks (32 ragged contexts, 545 MB,
 // 103 us; one million tokens at ratio 4, 269 MB, 58 us); with two terms of P
 // the products and the turn of a stage (2,070 cycles a chunk); by its latency
 // chain where a CTA has one or two (8,192 rows 14.8 us, 256 rows 9.1 us, join
-// included).  A stage's turn (released, copied, logits, weights, products) takes
+// included; called in a stream 14.6 and 9.5).  A stage's turn (released, copied, logits, weights, products) takes
 // 5,500 cycles, so the stages set the pace: three of 48 rows instead of two of
 // 64, what fits beside Q, take 2,760 cycles per 64 rows instead of 3,780 with
 // two terms and 2,840 instead of 3,130 with one (128-head drafts 82.5 -> 76.7
@@ -339,10 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Tokens are cut only where that shortens the longest CTA by more than
     // the partials and their join cost: otherwise CTA c takes token c (T <= G),
-    // or the tokens that begin in its range.  (240 rows; 192 and 336 measure the
-    // same within 0.5%.  At 768, 150 tokens of 250 to 500 rows gained, 41.3 ->
-    // 32.6 us, but 64 of 512 to 1,024 rows lost, 31.2 -> 39.2, and one of 600,
-    // 9.2 -> 23.4, all with chunks of 64 rows.)
+    // or the tokens that begin in its range.  (240 rows; 2 and 3 chunks measure
+    // the same within 0.5%.  At 8 chunks 64 tokens of 512 rows gain, 27.6 -> 26.4
+    // us, and one of 256 rows loses, 9.4 -> 15.4.  At 16, 150 tokens of 250 to 500
+    // rows gain, 30.8 -> 26.6 us, and 64 of 512 rows, 27.6 -> 23.4, but 64 of 512
+    // to 1,024 rows lose, 27.9 -> 34.3, 128 of 32 to 1,024 rows, 31.4 -> 46.3, and
+    // one of 600, 9.0 -> 22.8.)
     const bool direct = T <= G && maxc <= static_cast<int>(A.split_div[0].div(U)) + kCutAbove;
     const bool snap = direct || (T > G && maxc <= kCutAbove);
     // few CTAs at work: 2 or 4 of them share a range, each with all of its
@@ -510,9 +512,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------- products, epilogue
             // Step j: warp 8 issues S of chunk j, warp 9 O^T of chunk j - 1, and
             // all four drain O^T where that chunk ends a stretch.  A whole
-            // warp keeps step and one elected thread issues: behind elect.sync the
-            // descriptors stay in uniform registers (a 64 x 64 x 16 instruction
-            // every 33 cycles; behind `lane == 0`, every 54).
+            // warp keeps step and one elected thread issues: a 64 x 64 x 16
+            // instruction every 33 cycles behind elect.sync, every 54 behind
+            // `lane == 0`.
             constexpr uint32_t id_qk = idesc_bf16<kHG, kChunk, false>();
             constexpr uint32_t id_pv = idesc_bf16<128, kHG, true>(), id_wide = idesc_bf16<128, 2 * kHG, true>();
             const uint64_t q_desc = sw128_desc(smem_addr(sQ), 16, 1024);
@@ -1286,12 +1288,22 @@ cudaError_t launch_one_join(const Launch &lc, const PagedArgs &A, dim3 grid, int
 
 template <bool kBf16>
 cudaError_t launch_join(const Launch &lc, const PagedArgs &A, int entries, int groups, int64_t slots_max) {
-    // one token: 8 threads a column for few parts (600 rows: 1.2 us less than with
-    // 16), 16 beyond (8,192 rows: 1.1 us less than with 8)
+    // One token: 8 threads a column where its table has room for few rows (600
+    // rows 9.2 us, with 16 threads 10.7), 16 beyond (8,192 rows 14.9 us, with 8
+    // threads 15.5).  The length itself is on the device only: in a table of
+    // 262,144 rows, 256 rows take 10.0 instead of 9.1 us and 600 rows 10.7.
     if (entries == 1 && slots_max <= 2048)
         return launch_one_join<join_deep_kernel<8, 32, kBf16>>(lc, A, dim3(1, groups * 64, 4), 256);
     if (entries == 1) return launch_one_join<join_deep_kernel<16, 32, kBf16>>(lc, A, dim3(1, groups * 64, 4), 512);
+    // Up to 12 tokens, parts by the dozen: a CTA a tile of four heads (8,192 rows
+    // each: 2 tokens 18.7 us, with the other kernel 34.5; 8 tokens 29.3 and 34.6; 12
+    // tokens 37.5 and 38.8; 16 tokens 44.8 and 42.6; 24 tokens 61.1 and 54.3.  With
+    // 128 heads of 2,048 rows the two meet earlier: 4 tokens 18.9 and 23.3, 8
+    // tokens 27.1 and 24.1).
     if (entries <= 12) return launch_one_join<join_deep_kernel<4, 128, kBf16>>(lc, A, dim3(entries, groups * 64), 512);
+    // beyond, a CTA 16 heads of a tile, or 32 where CTAs are many (24 tokens of
+    // 1,500 to 6,000 rows 30.3 us, with 32 heads 32.8; 64 tokens 53.4 and 52.9; 128
+    // tokens 91.7, with 16 heads 93.4; 128-head drafts of 64 tokens 76.3 and 77.0)
     const int share = entries * groups >= 96 ? kHG / kWideHeads : 2 * kHG / kWideHeads;
     return launch_one_join<join_wide_kernel<kBf16>>(lc, A, dim3(entries, groups * 4, share), 256);
 }
