@@ -386,8 +386,9 @@ def _device_stream(fn: str, index: int, stream=None) -> int:
         raise ValueError(f"{fn}: tensors live on cuda:{index}, not on the current device")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
-    if stream.device_index != index:
-        raise ValueError(f"{fn}: the stream belongs to cuda:{stream.device_index}, not cuda:{index}")
+    own = getattr(stream, "device_index", index)     # (any object with a cuda_stream will do)
+    if own != index:
+        raise ValueError(f"{fn}: the stream belongs to cuda:{own}, not cuda:{index}")
     return stream.cuda_stream
 
 

@@ -160,3 +160,8 @@ def test_binding_refuses_a_stream_of_another_device(monkeypatch):
         csa._device_stream("f", 0, Stream(1))
     with pytest.raises(ValueError, match="current device"):
         csa._device_stream("f", 1, Stream(1))
+
+
+def test_binding_takes_any_object_with_a_stream(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert csa._device_stream("f", 0, type("Wrapped", (), dict(cuda_stream=99))()) == 99
