@@ -85,10 +85,10 @@ typedef enum {
  * swa_first_pos as soon as they start, while a preceding kernel that allows
  * programmatic dependent launch may still run: these arrays must not be
  * written by such a kernel (of the library's own, csa_page_plan alone writes
- * them, and it does not allow that launch; a copy, or a kernel without that launch attribute, completes before the
- * next one starts).  Everything else a call reads (queries, weights, keys,
- * rows, the window ring) is read only after the preceding kernel has
- * finished. */
+ * them, and it does not allow that launch; a copy, or a kernel without that
+ * launch attribute, completes before the next one starts).  Everything else a
+ * call reads (queries, weights, keys, rows, the window ring) is read only after
+ * the preceding kernel has finished. */
 typedef struct {
     int32_t num_seqs;               /* (host) B >= 1 */
     int32_t num_tokens;             /* (host) T >= 0 */
