@@ -47,16 +47,13 @@
 
 #include <type_traits>
 
-#include "csa_device.cuh"
-#include "csa_internal.h"
+#include "csa_paged_attention.cuh"
 
 namespace csa {
 namespace {
 
-constexpr int kThreads = 384;
 constexpr int kSmThreads = 128;                 // warps 4..7; the epilogue's 8..11
 constexpr int kBarSm = 1;
-constexpr int kHG = 64;                         // heads per CTA
 constexpr int kChunk = 48;
 constexpr int kSlices = kChunk / 16;            // of 16 rows: one K step of O^T each
 constexpr int kQBytes = kHG * kHD * 2;          // 64 KiB
@@ -79,42 +76,16 @@ template <int kTerms>
 __device__ __forceinline__ constexpr uint32_t o_col(int dd) {
     return kOCol + kHG * (dd + (dd < kWide<kTerms> ? dd : kWide<kTerms>));
 }
-constexpr int kMaxRec = 64;                     // segments a CTA lists at a time
-constexpr int kMaxCtas = 152;                   // CTAs of the grid at most (sizes the workspace)
 constexpr int kSegCost = 4;                     // a segment's epilogue, in chunks (3: 128 contexts of 512 rows 30.3
                                                 // us instead of 29.3; 2: 128-head drafts 82.5 instead of 76.5)
-constexpr int kCutAbove = 5;                    // chunks a token may exceed the mean before tokens are cut
+// Chunks a token may exceed the mean before tokens are cut.  (240 rows; 2 and 3
+// chunks measure the same within 0.5%.  At 8 chunks 64 tokens of 512 rows gain, 27.6
+// -> 26.4 us, and one of 256 rows loses, 9.4 -> 15.4.  At 16, 150 tokens of 250 to 500
+// rows gain, 30.8 -> 26.6 us, and 64 of 512 rows, 27.6 -> 23.4, but 64 of 512 to 1,024
+// rows lose, 27.9 -> 34.3, 128 of 32 to 1,024 rows, 31.4 -> 46.3, and one of 600, 9.0 ->
+// 22.8.)
+constexpr int kCutAbove = 5;
 constexpr int kFlushF32 = 53, kFlushBf16 = 682; // chunks between roundings of the accumulator, at most
-
-struct PagedArgs {
-    csa_paged_layout_t L;
-    int32_t H, window, ratio, bf16_out;
-    float scale_log2;
-    int32_t total_rows;       // rows of the pool: the coordinate that reads as zeros
-    FastDiv page_div, ratio_div, swa_div;   // by page_rows, ratio, swa_cap
-    FastDiv split_div[3];
-    int64_t num_pages, page_stride;
-    const __nv_bfloat16 *cache;
-    const float *sinks;
-    void *out;
-    float4 *part_o;           // [slot][head group][tile][16 quads of heads][128 columns]: 4 heads
-    float2 *part_ml;          // [slot][head group][64 heads]: m (log2 units), l
-    int2 *meta;               // by token (T <= CTAs) or by CTA: first slot, parts (0: none)
-    int32_t *status;
-};
-
-// One segment: chunks [c0, c1) of token t.
-struct Rec {
-    int32_t t, b;             // b < 0: padding
-    int32_t n, near;          // compressed rows, window rows
-    int32_t c0, c1;
-    int32_t slot;             // partial slot
-    int32_t flags;
-    int64_t first;            // first window position
-    int64_t first_res;        // oldest position the ring holds
-};
-constexpr int kRecPart = 1;   // part of a cut token: leaves (O, m, l)
-constexpr int kRecZero = 2;   // a token without rows: zeros
 
 struct Smem {
     uint64_t q_full, q_free;
@@ -129,10 +100,7 @@ struct Smem {
     float alpha[kHG];
     alignas(16) float fin[2][kHG];     // of a stretch: factors of the output,
     alignas(16) float flush[2][kHG];   // and of the partial so far
-    int32_t nrec, more;
-    int32_t t0, s0;
-    int2 wsum[kThreads / 32];    // cost, most chunks of a token
-    Rec rec[kMaxRec];
+    WorkSmem work;
 };
 
 __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
@@ -191,63 +159,6 @@ __device__ __forceinline__ uint64_t atom_desc(uint32_t saddr, uint32_t lbo, uint
 // address is below 256 KiB, so the field never carries)
 __device__ __forceinline__ constexpr uint64_t off(uint32_t bytes) { return bytes >> 4; }
 
-// What token t attends: b < 0 for padding, n = near = 0 for a bad token.
-// `per` tokens a sequence is the guess by which the sequence's length is
-// loaded in the same round trip as its number.
-__device__ __forceinline__ Rec token_rec(const PagedArgs &A, int t, int per, int &bad) {
-    Rec r{};
-    r.t = t;
-    const int g = min(t / per, A.L.num_seqs - 1);
-    r.b = __ldcg(A.L.tok_seq + t);
-    const int64_t pos = __ldcg(A.L.tok_pos + t);
-    int64_t n = __ldcg(A.L.row_len + g);
-    if (A.window > 0) r.first_res = __ldcg(A.L.swa_first_pos + g);
-    bad = 0;
-    if (r.b == -1) return r;
-    if (r.b < 0 || r.b >= A.L.num_seqs || pos < 0) {
-        bad = CSA_DEV_BAD_LAYOUT;
-        r.b = 0;
-        return r;
-    }
-    if (r.b != g) {
-        n = __ldcg(A.L.row_len + r.b);
-        if (A.window > 0) r.first_res = __ldcg(A.L.swa_first_pos + r.b);
-    }
-    const int64_t cap = static_cast<int64_t>(A.L.max_pages) * A.L.page_rows;
-    if (n < 0) {
-        bad |= CSA_DEV_BAD_LENGTH;
-        n = 0;
-    }
-    if (n > cap) {
-        bad |= CSA_DEV_CAPACITY;
-        n = cap;
-    }
-    const int64_t seen = A.ratio_div.div64(pos);
-    r.n = static_cast<int32_t>(n < seen ? n : seen);
-    if (A.window > 0) {
-        r.first = window_first(pos, A.window);
-        r.near = static_cast<int32_t>(pos - r.first + 1);
-    }
-    return r;
-}
-
-__device__ __forceinline__ int rec_window_slot(const Rec &r) { return (r.n + 7) & ~7; }
-__device__ __forceinline__ int rec_slots(const Rec &r) {
-    return r.near > 0 ? rec_window_slot(r) + r.near : r.n;
-}
-__device__ __forceinline__ int rec_chunks(const Rec &r) {
-    return r.b < 0 ? 0 : (rec_slots(r) + kChunk - 1) / kChunk;
-}
-__device__ __forceinline__ int chunk_cost(int chunks) { return chunks > 0 ? chunks + kSegCost : 1; }
-
-// Chunks after which a segment of nch chunks rounds its accumulator into the
-// partial: equal stretches of at most kMost.
-template <int kMost>
-__device__ __forceinline__ int flush_every(int nch) {
-    const int n = (nch + kMost - 1) / kMost;
-    return n > 1 ? (nch + n - 1) / n : nch;
-}
-
 // kTerms: bf16 terms of P (2 for an f32 output, 1 for bf16).
 template <int kTerms>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -264,8 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Smem &S = *reinterpret_cast<Smem *>(sOut + kStagedBytes<kTerms>);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = gridDim.x, hg = blockIdx.y, h0 = hg * kHG;
-    const int T = A.L.num_tokens, H = A.H;
+    const int hg = blockIdx.y, h0 = hg * kHG;
+    const int H = A.H;
 
     if (tid == 0) {
         mbar_init(&S.q_full, 1);
@@ -296,202 +207,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
 
-    // ---------------------------------------------------- division of the work
-    // (the layout is read before the wait for the preceding kernel, as
-    // everywhere in this library)  Chunks and costs of all tokens, a
-    // contiguous run of tokens per thread; with one token a thread its record
-    // stays in registers.
-    const int tps = max(1, T / A.L.num_seqs);
-    const int per = (T + kThreads - 1) / kThreads;
-    const int ta = min(T, tid * per), te = min(T, ta + per);
-    Rec own{};
-    int own_c = 0, own_bad = 0;
-    int cost = 0, maxc = 0;
-    for (int t = ta; t < te; ++t) {
-        own = token_rec(A, t, tps, own_bad);
-        own_c = rec_chunks(own);
-        cost += chunk_cost(own_c);
-        maxc = max(maxc, own_c);
-    }
-    int incl = cost;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    maxc = __reduce_max_sync(0xffffffffu, maxc);
-    if (lane == 31) S.wsum[warp] = make_int2(incl, maxc);
-    if (tid == 0) {
-        S.t0 = T;
-        S.nrec = 0;
-        S.more = 0;
-    }
+    Work<kChunk, kSegCost, kCutAbove> W(A, S.work);
+    W.count();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = S.tmem_holder;
-    int base = 0, U = 0;                 // units in front of this warp, of all tokens
-    maxc = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w == warp) base = U;
-        U += S.wsum[w].x;
-        maxc = max(maxc, S.wsum[w].y);
-    }
-    // Tokens are cut only where that shortens the longest CTA by more than
-    // the partials and their join cost: otherwise CTA c takes token c (T <= G),
-    // or the tokens that begin in its range.  (240 rows; 2 and 3 chunks measure
-    // the same within 0.5%.  At 8 chunks 64 tokens of 512 rows gain, 27.6 -> 26.4
-    // us, and one of 256 rows loses, 9.4 -> 15.4.  At 16, 150 tokens of 250 to 500
-    // rows gain, 30.8 -> 26.6 us, and 64 of 512 rows, 27.6 -> 23.4, but 64 of 512
-    // to 1,024 rows lose, 27.9 -> 34.3, 128 of 32 to 1,024 rows, 31.4 -> 46.3, and
-    // one of 600, 9.0 -> 22.8.)
-    const bool direct = T <= G && maxc <= static_cast<int>(A.split_div[0].div(U)) + kCutAbove;
-    const bool snap = direct || (T > G && maxc <= kCutAbove);
-    // few CTAs at work: 2 or 4 of them share a range, each with all of its
-    // logits and weights and its share of the 512 columns: the last products
-    // and the partial (32 bytes a cycle and SM) are that much shorter (8,192
-    // rows, three chunks for two CTAs 14.8 us, two for one 15.3)
-    int dlog = 0;
-    if (direct) dlog = T * 4 <= G ? 2 : T * 2 <= G ? 1 : 0;
-    else if (!snap && T <= G) dlog = U <= G / 4 ? 2 : U <= G + G / 3 ? 1 : 0;
-    const int dparts = 1 << dlog;
-    const int split = static_cast<int>(blockIdx.x) >> dlog;
-    const int ndt = 4 >> dlog;                                    // 128-column tiles of this CTA
-    const int dt0 = (static_cast<int>(blockIdx.x) & (dparts - 1)) * ndt;
-    // equal ranges of `share` units, the last ones shorter or empty: as few parts
-    // as the longest range allows
-    const int share = static_cast<int>(A.split_div[dlog].div(U + (G >> dlog) - 1));
-    int ua = 0, ub = split < T ? 1 : 0;
-    if (!direct) {
-        ua = min(split * share, U);
-        ub = min(ua + share, U);
-    }
-    const bool by_token = T <= G;
-    const bool lead = hg == 0 && dt0 == 0;       // reports errors, writes the join's list
-    // The first token of the range: the one that holds unit ua, or (whole
-    // tokens only) the first that begins at or behind it.
-    if (direct) {
-        if (tid == 0) S.t0 = split;
-    } else {
-        int s = base + incl - cost;
-        for (int t = ta; t < te; ++t) {
-            int bad;
-            const int c = per == 1 ? own_c : rec_chunks(token_rec(A, t, tps, bad));
-            const int e = s + chunk_cost(c);
-            if (snap ? s >= ua : (s <= ua && ua < e)) {
-                if (snap) {
-                    atomicMin(&S.t0, t);
-                } else {
-                    S.t0 = t;
-                    S.s0 = s;
-                }
-                break;
-            }
-            s = e;
-        }
-    }
-    __syncthreads();
-    if (per > 1 && snap && !direct) {
-        int s = base + incl - cost;
-        for (int t = ta; t < te; ++t) {
-            if (t == S.t0) S.s0 = s;
-            int bad;
-            s += chunk_cost(rec_chunks(token_rec(A, t, tps, bad)));
-        }
-        __syncthreads();
-    }
-    int t0 = S.t0, s0 = S.s0;
-
-    // Lists the segment of one token (whose units begin at s) as entry `at`.
-    // Returns the token's entry for the join; `owner`: its first chunk is here.
-    auto list = [&](Rec &r, int c, int s, int at, bool &owner) {
-        int2 m = make_int2(-1, 0);
-        owner = true;
-        r.c0 = 0;
-        r.c1 = c;
-        r.slot = 2 * split + 1;
-        if (!snap) {
-            owner = s >= ua;
-            r.c0 = min(max(ua - s, 0), c);
-            r.c1 = min(ub - s, c);
-            if (!owner) r.slot = 2 * split;
-            // the split that holds the token's last chunk
-            if (owner && c > 0) {
-                const int last = (s + c - 1) / share;
-                if (last > split) m = make_int2(r.slot, last - split + 1);
-            }
-            if (r.c1 - r.c0 < c) r.flags |= kRecPart;
-        }
-        if (r.b >= 0 && c == 0 && owner) r.flags |= kRecZero;
-        S.rec[at] = r;
-        atomicAdd(&S.nrec, 1);
-        // its first table entry on its way while the roles start
-        if (r.c0 * kChunk < r.n)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(A.L.table + static_cast<int64_t>(r.b) * A.L.max_pages +
-                                                          A.page_div.div(r.c0 * kChunk)));
-        if (at == kMaxRec - 1 && !direct) {
-            S.more = 1;
-            S.s0 = s + chunk_cost(c);
-        }
-        return m;
-    };
-    auto report = [&](const Rec &r, int bad, int2 m) {
-        raise_status(A.status, bad);
-        if (by_token) {
-            A.meta[r.t] = m;
-        } else if (m.y > 0) {
-            A.meta[split] = m;
-            A.meta[G + split] = make_int2(r.t, 0);
-        }
-    };
-    // thread i lists token t0 + i
-    auto list_next = [&]() {
-        Rec r{};
-        int bad = 0, c = 0, w = 0;
-        const bool in = tid < kMaxRec && t0 + tid < T && ub > ua;
-        if (in) {
-            r = token_rec(A, t0 + tid, tps, bad);
-            c = rec_chunks(r);
-            w = chunk_cost(c);
-        }
-        int run = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += v;
-        }
-        if (lane == 31) S.wsum[warp].x = run;
-        __syncthreads();
-        int s = s0 + run - w;
-        for (int k = 0; k < kMaxRec / 32; ++k)
-            if (k < warp) s += S.wsum[k].x;
-        if (in && s < ub) {
-            bool owner;
-            const int2 m = list(r, c, s, tid, owner);
-            if (lead && owner) report(r, bad, m);
-        }
-    };
-    if (per == 1) {
-        // the first list, from the registers
-        const int at = tid - t0;
-        const int s = base + incl - cost;
-        bool owner = false;
-        int2 m = make_int2(-1, 0);
-        if (at >= 0 && at < kMaxRec && tid < T && ub > ua && (direct ? at == 0 : s < ub))
-            m = list(own, own_c, s, at, owner);
-        pdl_wait();
-        pdl_launch_dependents();
-        if (!by_token) {
-            if (lead && tid == 0) A.meta[split] = make_int2(-1, 0);
-            __syncthreads();
-        }
-        if (lead && owner) report(own, own_bad, m);
-    } else {
-        pdl_wait();
-        pdl_launch_dependents();
-        if (lead && tid == 0) A.meta[split] = make_int2(-1, 0);
-        list_next();
-    }
+    W.divide();
+    W.first_list();
+    const int ndt = W.ndt, dt0 = W.dt0;                          // 128-column tiles of this CTA
+    const Rec *const rec = S.work.rec;
 
     // pipeline positions, kept across lists of segments
     uint32_t n_fetch = 0;                // chunks fetched
@@ -502,10 +226,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     for (;;) {
         __syncthreads();
-        t0 += kMaxRec;
-        s0 = S.s0;
-        const int nrec = S.nrec;
-        const bool more = S.more != 0;
+        W.advance();
+        const int nrec = S.work.nrec;
+        const bool more = S.work.more != 0;
         if (nrec == 0) break;
 
         if (warp >= 8) {
@@ -548,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int i = 0, k = 0, nch = 0, every = 1, z = 0;     // chunk j: k of segment i, z of a stretch
             auto settle = [&]() {
                 while (i < nrec) {
-                    nch = S.rec[i].c1 - S.rec[i].c0;
+                    nch = rec[i].c1 - rec[i].c0;
                     if (nch > 0) break;
                     ++i;
                 }
@@ -565,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (elect_one()) {
                             mbar_arrive_expect_tx(&S.q_full, kQBytes);
-                            tma_load_4d(sQ, &tm_q, 0, h0, 0, S.rec[i].t, &S.q_full, policy_evict_normal());
+                            tma_load_4d(sQ, &tm_q, 0, h0, 0, rec[i].t, &S.q_full, policy_evict_normal());
                         }
                         __syncwarp();
                         mbar_wait(&S.q_full, n_ql & 1u, A.status);
@@ -634,11 +357,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++n_sm;
                     if (bk + 1 == bn || bz + 1 == be) {
                         // ---- O^T into the partial, or the output
-                        const int t = S.rec[bi].t, flags = S.rec[bi].flags;
+                        const int t = rec[bi].t, flags = rec[bi].flags;
                         const int64_t obase = (static_cast<int64_t>(t) * H + h0) * kHD;
-                        const int64_t pslot = static_cast<int64_t>(S.rec[bi].slot) * gridDim.y + hg;
+                        const int64_t pslot = static_cast<int64_t>(rec[bi].slot) * gridDim.y + hg;
                         const int e = n_ep & 1u;
-                        (void)CSA_CHECK(S.rec[bi].slot < 2 * G && t < T, A.status);
+                        (void)CSA_CHECK(rec[bi].slot < 2 * W.G && t < W.T, A.status);
                         const bool add = bk >= be;               // the partial holds earlier stretches
                         const bool part = (flags & kRecPart) || bk + 1 < bn;
                         mbar_wait(&S.stretch[e], (n_ep >> 1) & 1u, A.status);
@@ -762,9 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int i, c;
             };
             auto settle = [&](Cursor &k) {             // to the next segment that has chunks
-                while (k.i < nrec && k.c >= S.rec[k.i].c1) {
+                while (k.i < nrec && k.c >= rec[k.i].c1) {
                     ++k.i;
-                    if (k.i < nrec) k.c = S.rec[k.i].c0;
+                    if (k.i < nrec) k.c = rec[k.i].c0;
                 }
             };
             auto advance = [&](Cursor &k) {
@@ -778,11 +501,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto look_up = [&](const Cursor &k) {
                 Entry e{-1, -1, false};
                 if (k.i >= nrec) return e;
-                const int n = S.rec[k.i].n, j = k.c * kChunk + 16 * li + rl;
+                const int n = rec[k.i].n, j = k.c * kChunk + 16 * li + rl;
                 if (j < n) {
                     const int pg = static_cast<int>(A.page_div.div(j));
                     e.in_page = j - pg * A.L.page_rows;
-                    e.page = A.L.table[static_cast<int64_t>(S.rec[k.i].b) * A.L.max_pages + pg];
+                    e.page = A.L.table[static_cast<int64_t>(rec[k.i].b) * A.L.max_pages + pg];
                     e.box = j + 8 <= n && e.in_page + 8 <= A.L.page_rows;
                 }
                 return e;
@@ -813,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // rows are read once, or once by each of two groups of heads
             const uint64_t pol = gridDim.y > 1 ? policy_evict_normal() : policy_evict_first();
-            Cursor cur{0, S.rec[0].c0};
+            Cursor cur{0, rec[0].c0};
             settle(cur);
             Cursor far = cur;
             const Entry e0 = look_up(far);
@@ -823,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Entry ahead = look_up(far);
             Place now = place(e0), next = place(e1);
             while (cur.i < nrec) {
-                const Rec &r = S.rec[cur.i];
+                const Rec &r = rec[cur.i];
                 const int j0 = cur.c * kChunk + 16 * li, wslot = rec_window_slot(r);
                 const __nv_bfloat16 *src = nullptr;
                 if (now.row >= 0) {
@@ -886,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (pending >= 0) land(false);
             bad = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bad)));
-            if (lane == 0 && lead) raise_status(A.status, bad);
+            if (lane == 0 && W.lead) raise_status(A.status, bad);
         } else if (warp >= 4) {
             // -------------------------------------------- softmax
             const int q = warp & 3;                  // TMEM lane quarter
@@ -895,10 +618,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool hv = h0 + hl < H;
             const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
             for (int i = 0; i < nrec; ++i) {
-                const int nch = S.rec[i].c1 - S.rec[i].c0;
+                const int nch = rec[i].c1 - rec[i].c0;
                 if (nch <= 0) {
-                    if (S.rec[i].flags & kRecZero) {
-                        const int64_t obase = (static_cast<int64_t>(S.rec[i].t) * H + h0) * kHD;
+                    if (rec[i].flags & kRecZero) {
+                        const int64_t obase = (static_cast<int64_t>(rec[i].t) * H + h0) * kHD;
                         for (int x = tid - 128; x < min(kHG, H - h0) * 128 * ndt; x += kSmThreads) {
                             const int64_t at = obase + (x / (128 * ndt)) * kHD + dt0 * 128 + x % (128 * ndt);
                             if (kTerms == 1) static_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16(0.f);
@@ -907,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     continue;
                 }
-                const bool cut = S.rec[i].flags & kRecPart;
+                const bool cut = rec[i].flags & kRecPart;
                 float m_ref = -INFINITY, l = 0.f, m_flush = -INFINITY;
                 const int every = flush_every<kFlush>(nch);
                 for (int k = 0, z = 0; k < nch; ++k, ++n_sm, z = z + 1 == every ? 0 : z + 1) {
@@ -1044,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         S.fin[e][hl] = f;
                         if (last && cut && dt0 == 0)
-                            A.part_ml[(static_cast<int64_t>(S.rec[i].slot) * gridDim.y + hg) * kHG + hl] =
+                            A.part_ml[(static_cast<int64_t>(rec[i].slot) * gridDim.y + hg) * kHG + hl] =
                                 make_float2(m_ref, l);
                     }
                     m_flush = m_ref;
@@ -1055,10 +778,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!more) break;
         __syncthreads();                 // the list is done with
         if (tid == 0) {
-            S.nrec = 0;
-            S.more = 0;
+            S.work.nrec = 0;
+            S.work.more = 0;
         }
-        list_next();
+        W.next_list();
     }
     tc_fence_before();
     __syncthreads();
@@ -1066,262 +789,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
-}
-
-// Joins the parts of a cut token:
-//   out = sum_s 2^(m_s - M) O_s / (sum_s 2^(m_s - M) l_s [+ 2^(sink - M)]).
-// Two shapes: a few tokens cut into up to 152 parts (one long context), and
-// many tokens in a few parts each.
-struct JoinEntry {
-    int t, ns, slot0, split0;
-    __device__ int64_t slot(int k) const { return k == 0 ? slot0 : 2 * (split0 + k); }
-};
-
-__device__ __forceinline__ JoinEntry join_entry(const PagedArgs &A) {
-    const int2 meta = A.meta[blockIdx.x];
-    JoinEntry e;
-    e.ns = meta.y > kMaxCtas ? 0 : meta.y;
-    e.slot0 = meta.x;
-    e.split0 = meta.x >> 1;
-    // by token: entry x is token x; by CTA: the token stands behind the list
-    e.t = blockIdx.x;
-    if (A.L.num_tokens > static_cast<int>(gridDim.x)) e.t = A.meta[gridDim.x + blockIdx.x].x;
-    return e;
-}
-
-// The sink's term 2^(sink - M) of a sum scaled to M >= sink (log2 units): 1 where
-// it is the maximum, an infinite one too; NaN stays NaN.
-__device__ __forceinline__ float sink_term(float sink, float M) { return sink == M ? 1.f : exp2f(sink - M); }
-
-template <bool kBf16>
-__device__ __forceinline__ void join_store(const PagedArgs &A, int64_t at, float x) {
-    if (kBf16) static_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16(x);
-    else static_cast<float *>(A.out)[at] = x;
-}
-
-// Many parts: a CTA takes four heads of kCols columns; kDeepSub threads share a
-// column's parts, eight loads of four heads each in flight (issued before the
-// weights are known), and meet in shared memory in order.  One token: 32
-// columns, so that every SM reads; a few: a whole 128-column tile.
-constexpr int kDeepPer = 8;
-
-template <int kDeepSub, int kCols, bool kBf16>
-__global__ void __launch_bounds__(kCols * kDeepSub) join_deep_kernel(const PagedArgs A) {
-    __shared__ float wgt[4][kMaxCtas];
-    __shared__ float inv_z[4];
-    __shared__ float4 red[(kDeepSub - 1) * kCols];
-    pdl_wait();
-    pdl_launch_dependents();
-    const JoinEntry J = join_entry(A);
-    const int ns = J.ns;
-    if (ns <= 0) return;
-    static_assert(kCols * kDeepSub >= 128, "four warps make the weights");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = tid / kCols;
-    const int quad = blockIdx.y & 15, tile = blockIdx.y >> 4 & 3, hg = blockIdx.y >> 6;
-    const int col = static_cast<int>(blockIdx.z) * kCols + tid % kCols;      // of the tile
-    const int groups = static_cast<int>(gridDim.y) >> 6, h0 = hg * kHG + 4 * quad;
-    if (h0 >= A.H) return;
-    const float4 *const po = A.part_o + tile * (16 * 128) + quad * 128 + col;
-    float4 v[kDeepPer];
-    auto load = [&](int k0) {
-#pragma unroll
-        for (int k = 0; k < kDeepPer; ++k)
-            if (k0 + k * kDeepSub < ns) v[k] = __ldcg(po + (J.slot(k0 + k * kDeepSub) * groups + hg) * (4 * 16 * 128));
-    };
-    load(sub);
-    if (warp < 4) {                              // the weights of head `warp`
-        constexpr int kMl = (kMaxCtas + 31) / 32;
-        float2 ml[kMl];
-        float M = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < kMl; ++k) {
-            ml[k] = make_float2(-INFINITY, 0.f);
-            if (lane + 32 * k < ns)
-                ml[k] = __ldcg(A.part_ml + (J.slot(lane + 32 * k) * groups + hg) * kHG + 4 * quad + warp);
-        }
-#pragma unroll
-        for (int k = 0; k < kMl; ++k) M = fmaxf(M, ml[k].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float sink = A.sinks && h0 + warp < A.H ? A.sinks[h0 + warp] * kLog2e : -INFINITY;
-        const float Mall = fmaxf(M, sink);
-        float z = 0.f;
-#pragma unroll
-        for (int k = 0; k < kMl; ++k) {
-            const float w = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - Mall);
-            if (lane + 32 * k < ns) wgt[warp][lane + 32 * k] = w;
-            z += w * ml[k].y;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        if (lane == 0) {
-            const bool some = M != -INFINITY;
-            if (some) z += sink_term(sink, Mall);
-            inv_z[warp] = some ? 1.f / z : 0.f;
-        }
-    }
-    __syncthreads();
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = sub; k0 < ns; k0 += kDeepPer * kDeepSub) {
-        if (k0 != sub) load(k0);
-#pragma unroll
-        for (int k = 0; k < kDeepPer; ++k) {
-            const int p = k0 + k * kDeepSub;
-            if (p >= ns) break;
-            // (heads behind the last hold anything and are not stored)
-            acc.x = fmaf(wgt[0][p], v[k].x, acc.x);
-            acc.y = fmaf(wgt[1][p], v[k].y, acc.y);
-            acc.z = fmaf(wgt[2][p], v[k].z, acc.z);
-            acc.w = fmaf(wgt[3][p], v[k].w, acc.w);
-        }
-    }
-    if (sub > 0) red[(sub - 1) * kCols + tid % kCols] = acc;
-    __syncthreads();
-    if (sub > 0) return;
-    for (int j = 0; j + 1 < kDeepSub; ++j) {
-        const float4 u = red[j * kCols + tid];
-        acc.x += u.x;
-        acc.y += u.y;
-        acc.z += u.z;
-        acc.w += u.w;
-    }
-    const float o[4] = {acc.x, acc.y, acc.z, acc.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (h0 + i < A.H)
-            join_store<kBf16>(A, (static_cast<int64_t>(J.t) * A.H + h0 + i) * kHD + tile * 128 + col, o[i] * inv_z[i]);
-}
-
-// Few parts: a CTA takes 16 heads of a tile (32 where tokens are many: fewer
-// waves of CTAs), a thread two quads of heads of its column at a time, the first
-// parts on their way before the weights are made.
-constexpr int kWidePer = 3;                      // parts in flight
-constexpr int kWideHeads = 32;                   // at most
-
-template <bool kBf16>
-__global__ void __launch_bounds__(256) join_wide_kernel(const PagedArgs A) {
-    __shared__ float4 wgt[kMaxCtas][kWideHeads / 4];   // scaled by 1 / z
-    pdl_wait();
-    pdl_launch_dependents();
-    const JoinEntry J = join_entry(A);
-    const int ns = J.ns;
-    if (ns <= 0) return;
-    const int tid = threadIdx.x, col = tid & 127, half = tid >> 7;
-    const int tile = blockIdx.y & 3, hg = blockIdx.y >> 2, groups = static_cast<int>(gridDim.y) >> 2;
-    const int most = kHG / static_cast<int>(gridDim.z);
-    const int hb = most * static_cast<int>(blockIdx.z), h0 = hg * kHG + hb;   // first head
-    if (h0 >= A.H) return;
-    const int heads = min(most, A.H - h0);
-    const float4 *const po = A.part_o + tile * (16 * 128) + hb / 4 * 128 + col;
-    float4 v[kWidePer][2];
-    auto load = [&](int k0, int qd) {                    // quads qd, qd + 1
-#pragma unroll
-        for (int k = 0; k < kWidePer; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (k0 + k < ns) v[k][e] = __ldcg(po + (J.slot(k0 + k) * groups + hg) * (4 * 16 * 128) + (qd + e) * 128);
-    };
-    load(0, 2 * half);
-    if (tid < most) {
-        const float2 *const ml = A.part_ml + hg * kHG + hb + tid;
-        const float sink = A.sinks && tid < heads ? A.sinks[h0 + tid] * kLog2e : -INFINITY;
-        constexpr int kNear = 6;                 // parts kept in registers
-        float2 x[kNear];
-#pragma unroll
-        for (int k = 0; k < kNear; ++k)
-            x[k] = k < ns ? __ldcg(ml + J.slot(k) * groups * kHG) : make_float2(-INFINITY, 0.f);
-        float M = x[0].x;
-#pragma unroll
-        for (int k = 1; k < kNear; ++k) M = fmaxf(M, x[k].x);
-        for (int k = kNear; k < ns; ++k) M = fmaxf(M, __ldcg(ml + J.slot(k) * groups * kHG).x);
-        const float Mall = fmaxf(M, sink);
-        float z = M != -INFINITY ? sink_term(sink, Mall) : 0.f;
-        auto put = [&](int k, float2 y) {
-            const float w = y.x == -INFINITY ? 0.f : exp2f(y.x - Mall);
-            reinterpret_cast<float *>(wgt[k])[tid] = w;
-            z += w * y.y;
-        };
-#pragma unroll
-        for (int k = 0; k < kNear; ++k)
-            if (k < ns) put(k, x[k]);
-        for (int k = kNear; k < ns; ++k) put(k, __ldcg(ml + J.slot(k) * groups * kHG));
-        const float f = M != -INFINITY ? 1.f / z : 0.f;
-        for (int k = 0; k < ns; ++k) reinterpret_cast<float *>(wgt[k])[tid] *= f;
-    }
-    __syncthreads();
-    const int64_t to = (static_cast<int64_t>(J.t) * A.H + h0) * kHD + tile * 128 + col;
-#pragma unroll 1
-    for (int qd = 2 * half; 4 * qd < heads; qd += 4) {
-        float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-        for (int k0 = 0; k0 < ns; k0 += kWidePer) {
-            if (k0 > 0 || qd >= 4) load(k0, qd);
-#pragma unroll
-            for (int k = 0; k < kWidePer; ++k) {
-                if (k0 + k >= ns) break;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float4 w = wgt[k0 + k][qd + e];
-                    acc[e].x = fmaf(w.x, v[k][e].x, acc[e].x);
-                    acc[e].y = fmaf(w.y, v[k][e].y, acc[e].y);
-                    acc[e].z = fmaf(w.z, v[k][e].z, acc[e].z);
-                    acc[e].w = fmaf(w.w, v[k][e].w, acc[e].w);
-                }
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float o[4] = {acc[e].x, acc[e].y, acc[e].z, acc[e].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int h = 4 * (qd + e) + i;
-                if (h < heads) join_store<kBf16>(A, to + static_cast<int64_t>(h) * kHD, o[i]);
-            }
-        }
-    }
-}
-
-template <auto kKernel>
-cudaError_t launch_one_join(const Launch &lc, const PagedArgs &A, dim3 grid, int threads) {
-    const cudaError_t e = prepare_kernel<kKernel>(0);
-    return e != cudaSuccess ? e : launch_pdl(kKernel, grid, dim3(threads), 0, lc.stream, A);
-}
-
-template <bool kBf16>
-cudaError_t launch_join(const Launch &lc, const PagedArgs &A, int entries, int groups, int64_t slots_max) {
-    // One token: 8 threads a column where its table has room for few rows (600
-    // rows 9.2 us, with 16 threads 10.7), 16 beyond (8,192 rows 14.9 us, with 8
-    // threads 15.5).  The length itself is on the device only: in a table of
-    // 262,144 rows, 256 rows take 10.0 instead of 9.1 us and 600 rows 10.7.
-    if (entries == 1 && slots_max <= 2048)
-        return launch_one_join<join_deep_kernel<8, 32, kBf16>>(lc, A, dim3(1, groups * 64, 4), 256);
-    if (entries == 1) return launch_one_join<join_deep_kernel<16, 32, kBf16>>(lc, A, dim3(1, groups * 64, 4), 512);
-    // Up to 12 tokens, parts by the dozen: a CTA a tile of four heads (8,192 rows
-    // each: 2 tokens 18.7 us, with the other kernel 34.5; 8 tokens 29.3 and 34.6; 12
-    // tokens 37.5 and 38.8; 16 tokens 44.8 and 42.6; 24 tokens 61.1 and 54.3.  With
-    // 128 heads of 2,048 rows the two meet earlier: 4 tokens 18.9 and 23.3, 8
-    // tokens 27.1 and 24.1).
-    if (entries <= 12) return launch_one_join<join_deep_kernel<4, 128, kBf16>>(lc, A, dim3(entries, groups * 64), 512);
-    // beyond, a CTA 16 heads of a tile, or 32 where CTAs are many (24 tokens of
-    // 1,500 to 6,000 rows 30.3 us, with 32 heads 32.8; 64 tokens 53.4 and 52.9; 128
-    // tokens 91.7, with 16 heads 93.4; 128-head drafts of 64 tokens 76.3 and 77.0)
-    const int share = entries * groups >= 96 ? kHG / kWideHeads : 2 * kHG / kWideHeads;
-    return launch_one_join<join_wide_kernel<kBf16>>(lc, A, dim3(entries, groups * 4, share), 256);
-}
-
-int groups_of(const csa_params_t &p) { return (p.n_heads + kHG - 1) / kHG; }
-
-struct Ws {
-    size_t meta, ml, o, total;
-};
-Ws ws_plan(const csa_params_t &p) {
-    const int groups = groups_of(p);
-    const size_t slots = 2 * static_cast<size_t>(kMaxCtas / groups) * groups;
-    Ws w{};
-    w.meta = 0;
-    w.ml = (2 * kMaxCtas * sizeof(int2) + 255) / 256 * 256;
-    w.o = w.ml + slots * kHG * sizeof(float2);
-    w.total = w.o + slots * kHG * kHD * sizeof(float);
-    return w;
 }
 
 template <int kTerms>
@@ -1338,7 +805,7 @@ cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L
                                    int64_t page_stride, const void *q, const float *sinks,
                                    csa_type_t out_type, void *out, int32_t *status, void *ws) {
     const int H = p.n_heads, groups = groups_of(p);
-    const int64_t total_rows = (num_pages - 1) * page_stride + L.page_rows;
+    const int64_t total_rows = paged_rows(L, num_pages, page_stride);
     CUtensorMap tq, tr;
     {
         // [64 columns][heads][8 column groups][tokens]
@@ -1356,30 +823,9 @@ cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L
         if (encode_tensor_map_bf16(&tr, cache, 3, dims, strides, box) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    const Ws w = ws_plan(p);
-    uint8_t *wb = static_cast<uint8_t *>(ws);
-    PagedArgs A{};
-    A.L = L;
-    A.H = H;
-    A.window = p.window;
-    A.ratio = p.ratio;
-    A.bf16_out = out_type == CSA_BF16;
-    A.scale_log2 = p.scale * kLog2e;
-    A.total_rows = static_cast<int32_t>(total_rows);
-    A.page_div = FastDiv(L.page_rows);
-    A.ratio_div = FastDiv(p.ratio);
-    A.swa_div = FastDiv(L.swa_cap > 0 ? L.swa_cap : 1);
-    A.num_pages = num_pages;
-    A.page_stride = page_stride;
+    PagedArgs A = paged_args(lc, L, p, num_pages, page_stride, sinks, out_type, out, status, ws);
     A.cache = static_cast<const __nv_bfloat16 *>(cache);
-    A.sinks = sinks;
-    A.out = out;
-    A.meta = reinterpret_cast<int2 *>(wb + w.meta);
-    A.part_ml = reinterpret_cast<float2 *>(wb + w.ml);
-    A.part_o = reinterpret_cast<float4 *>(wb + w.o);
-    A.status = status;
-    const int ctas = (lc.sm_count < kMaxCtas ? lc.sm_count : kMaxCtas) / groups;
-    for (int i = 0; i < 3; ++i) A.split_div[i] = FastDiv(ctas >> i);
+    const int ctas = static_cast<int>(A.split_div[0].d);
     cudaError_t e;
     if (A.bf16_out) {
         e = prepare_kernel<paged_attention_kernel<1>>(smem_bytes<1>());
