@@ -565,6 +565,100 @@ csa_status_t csa_paged_attention(const csa_paged_layout_t *layout, const csa_par
                                  const void *q, const float *sinks, csa_type_t out_type, void *out,
                                  int32_t *dev_status, void *ws, size_t ws_bytes, void *stream);
 
+/* 8-bit paged caches.  The same pages, slots and tables with rows of e4m3
+ * (OCP 8-bit floating point, 4 exponent and 3 mantissa bits, no infinity):
+ * a cache is a pool of code rows, one byte a value, and beside it an array of
+ * scales, one f32 a row; a value is code * scale.  A compressed row stands for
+ * a block of `ratio` tokens and serves every query head, so a scale a row is a
+ * scale for each block of tokens and head.  Row r of page p has its codes at
+ * (p * page_stride + r) * width and its scale at p * scale_stride + r
+ * (page_stride, scale_stride >= page_rows: several layers may share either
+ * pool).  csa_page_plan serves these caches as it does the others. */
+
+/* csa_paged_append_fp8: quantises row i of `rows` (bf16 or f32) into slot
+ * slots[i], for up to four (rows, cache) pairs in one launch.  The scale is
+ * 2^k with k the least integer such that every finite value of the row is at
+ * most 448 * 2^k in magnitude, held to -60 <= k <= 60 (a row of zeros: -60),
+ * and the codes are value / 2^k rounded to nearest, ties to even: both are
+ * exact functions of the row, off by at most 2^-4 of the value (of 2^k * 2^-6
+ * below that, e4m3's subnormal range).  What is not finite, or above 448 *
+ * 2^60, becomes e4m3's NaN.  width is a multiple of 16 up to 1024.  A negative
+ * slot skips its row; one at or above num_pages * page_rows sets
+ * CSA_DEV_BAD_INDEX and skips it.  Everything else in the cache stays as it
+ * was.  Slots of one call must differ (those of a plan do): where two rows
+ * have the same slot, its codes and scale come from either, mixed.  The rows,
+ * slots and the status word share no memory with a cache or its scales, else
+ * CSA_ERR_INVALID_ARGUMENT.  num_pages * page_rows, num_rows, page_stride and
+ * scale_stride < 2^31, else CSA_ERR_UNSUPPORTED. */
+typedef struct {
+    const void *rows;        /* [num_rows, width], row i at i * row_pitch bytes */
+    const int64_t *slots;    /* [num_rows] */
+    int64_t num_rows;        /* (host) >= 0 */
+    int64_t row_pitch;       /* (host) bytes, >= a row's, a multiple of 16 */
+    csa_type_t type;         /* (host) of rows */
+    int32_t width;           /* (host) values a row */
+    int32_t page_rows;       /* (host) rows per page of the cache */
+    int64_t num_pages;       /* (host) pages of the cache */
+    int64_t page_stride;     /* (host) rows from a page's codes to the next's */
+    int64_t scale_stride;    /* (host) scales from a page to the next */
+    void *cache;             /* e4m3 codes */
+    float *scales;
+} csa_append_fp8_job_t;
+
+csa_status_t csa_paged_append_fp8(const csa_append_fp8_job_t *jobs /* (host) */,
+                                  int32_t num_jobs, int32_t *dev_status, void *stream);
+
+/* csa_paged_read_fp8: row i of `out` becomes code * scale of slot slots[i], for
+ * a bf16 output rounded to nearest (with scales that csa_paged_append_fp8 wrote
+ * that product is a bf16 value already).  The same slot may be read several
+ * times.  A negative slot leaves its row of out as it was; one at or above
+ * num_pages * page_rows sets CSA_DEV_BAD_INDEX and does, too.  out shares no
+ * memory with the cache, the scales or the slots, else
+ * CSA_ERR_INVALID_ARGUMENT; sizes as above. */
+typedef struct {
+    const void *cache;       /* e4m3 codes */
+    const float *scales;
+    const int64_t *slots;    /* [num_rows] */
+    int64_t num_rows;        /* (host) >= 0 */
+    int32_t width;           /* (host) values a row, a multiple of 16 up to 1024 */
+    int32_t page_rows;       /* (host) */
+    int64_t num_pages;       /* (host) */
+    int64_t page_stride;     /* (host) */
+    int64_t scale_stride;    /* (host) */
+    csa_type_t type;         /* (host) of out */
+    int64_t out_pitch;       /* (host) bytes, >= a row's, a multiple of 16 */
+    void *out;               /* [num_rows, width], row i at i * out_pitch bytes */
+} csa_read_fp8_t;
+
+csa_status_t csa_paged_read_fp8(const csa_read_fp8_t *read /* (host) */, int32_t *dev_status,
+                                void *stream);
+
+/* csa_paged_attention_fp8: csa_paged_attention over an 8-bit cache and an
+ * 8-bit window ring, read in place:
+ *   l_j = scale q_h . (s_j c_j),   out_h = sum_j softmax_j(l [, sink]) s_j c_j.
+ * The layout, what a token attends, padding, tokens without rows, sinks, device
+ * status bits, limits and the workspace (csa_paged_workspace_size) are
+ * csa_paged_attention's, with layout->swa_kv the ring's codes [B, swa_cap, hd] and
+ * swa_scales [B, swa_cap] beside it (both may be NULL without a window).
+ *   cache, scales: width hd; only rows named by the table are read into the
+ *     result, the rest may hold anything.  Scales may be any f32 numbers of
+ *     magnitude 2^-60 to 2^60 (or 0); a NaN in a row that is seen gives NaN.
+ *   q bf16; a head whose query holds an infinity or NaN gives NaN.  A query
+ *     value enters exactly where it is at least 2^-10 of its head's largest, else
+ *     off by at most 2^-18 of that.
+ * For a bf16 output the weights enter with a relative error of at most 2^-9,
+ * for an f32 output 2^-18, each off by at most 2^-24 of the largest besides (in
+ * units of scale times weight).
+ * out, the workspace and the status word share memory with nothing else the
+ * call takes (the cache and its scales are not checked). */
+csa_status_t csa_paged_attention_fp8(const csa_paged_layout_t *layout, const csa_params_t *params,
+                                     const void *cache, const float *scales,
+                                     const float *swa_scales, int64_t num_pages,
+                                     int64_t page_stride, int64_t scale_stride, const void *q,
+                                     const float *sinks, csa_type_t out_type, void *out,
+                                     int32_t *dev_status, void *ws, size_t ws_bytes,
+                                     void *stream);
+
 #ifdef __cplusplus
 }
 #endif

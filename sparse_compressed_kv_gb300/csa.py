@@ -35,7 +35,8 @@ EXPORTS = ("csa_status_string", "csa_abi_version", "csa_workspace_size", "csa_in
            "csa_indexer_scores_fp4", "csa_decode_fp4", "csa_shard_workspace_size",
            "csa_shard_candidates", "csa_shard_merge", "csa_shard_attention", "csa_window_attention",
            "csa_shard_combine", "csa_page_plan", "csa_paged_append", "csa_paged_workspace_size",
-           "csa_paged_attention")
+           "csa_paged_attention", "csa_paged_append_fp8", "csa_paged_read_fp8",
+           "csa_paged_attention_fp8")
 MAX_APPEND_JOBS = 4  # csa_paged_append's limit (include/csa.h)
 MAX_SHARDS = 8  # csa_shard_merge's limit (include/csa.h)
 FP4_ROW = 80  # bytes per MXFP4 key row (include/csa.h)
@@ -93,6 +94,26 @@ class csa_paged_layout_t(ctypes.Structure):
     ]
 
 
+class csa_append_fp8_job_t(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("num_rows", ctypes.c_int64),
+        ("row_pitch", ctypes.c_int64), ("type", ctypes.c_int), ("width", ctypes.c_int32),
+        ("page_rows", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
+        ("cache", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+    ]
+
+
+class csa_read_fp8_t(ctypes.Structure):
+    _fields_ = [
+        ("cache", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("num_rows", ctypes.c_int64), ("width", ctypes.c_int32), ("page_rows", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+        ("scale_stride", ctypes.c_int64), ("type", ctypes.c_int), ("out_pitch", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -136,6 +157,9 @@ def load() -> ctypes.CDLL:
     Lp = ctypes.POINTER(csa_paged_layout_t)
     lib.csa_paged_workspace_size.argtypes = [Lp, Pm, ctypes.POINTER(sz)]
     lib.csa_paged_attention.argtypes = [Lp, Pm, P, i64, i64, P, P, ctypes.c_int, P, P, P, sz, P]
+    lib.csa_paged_append_fp8.argtypes = [ctypes.POINTER(csa_append_fp8_job_t), i32, P, P]
+    lib.csa_paged_read_fp8.argtypes = [ctypes.POINTER(csa_read_fp8_t), P, P]
+    lib.csa_paged_attention_fp8.argtypes = [Lp, Pm, P, P, P, i64, i64, i64, P, P, ctypes.c_int, P, P, P, sz, P]
     for fn in EXPORTS[2:]:
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
@@ -507,6 +531,8 @@ class PagedLayout:
     table [B, max_pages], the window ring [B, swa_cap, 512] (None without a
     window).  Keeps its tensors alive; made once for buffers that stay."""
 
+    ring_type = torch.bfloat16
+
     def __init__(self, tok_seq, tok_pos, row_len, table, page_rows: int, swa_kv=None,
                  swa_first_pos=None):
         T, B = int(tok_seq.shape[0]), int(row_len.shape[0])
@@ -519,7 +545,7 @@ class PagedLayout:
                                  f"got {tuple(swa_kv.shape)}")
             if swa_first_pos is None:
                 raise ValueError("swa_kv needs swa_first_pos")
-            ring = dict(swa_kv=_arg("swa_kv", swa_kv, torch.bfloat16), swa_cap=int(swa_kv.shape[1]),
+            ring = dict(swa_kv=_arg("swa_kv", swa_kv, self.ring_type), swa_cap=int(swa_kv.shape[1]),
                         swa_first_pos=_arg("swa_first_pos", swa_first_pos, torch.int64, (B,)))
         self.tensors = (tok_seq, tok_pos, row_len, table, swa_kv, swa_first_pos)
         self.device, self.num_tokens = row_len.device.index, T
@@ -553,6 +579,8 @@ def csa_paged_attention(layout: PagedLayout, prm: csa_params_t, cache, q, out, d
     s = _device_stream("csa_paged_attention", dev, stream)
     if cache.dtype != torch.bfloat16 or q.dtype != torch.bfloat16:
         raise ValueError("cache and q must be bfloat16")
+    if layout.ring_type is not torch.bfloat16:
+        raise ValueError("layout is one of 8-bit rows")
     if out.dtype != torch.float32 and out.dtype != torch.bfloat16:
         raise ValueError("out must be float32 or bfloat16")
     shape = (layout.num_tokens, prm.n_heads, prm.hd)
@@ -567,3 +595,138 @@ def csa_paged_attention(layout: PagedLayout, prm: csa_params_t, cache, q, out, d
         cache.shape[1] if cache.is_contiguous() else _page_stride(cache, layout.c.page_rows), _ptr(q, dev),
         None if sinks is None else _ptr(sinks, dev), 1 if out.dtype == torch.bfloat16 else 0,
         _ptr(out, dev), _ptr(dev_status, dev), _ptr(ws, dev), ws.numel(), s))
+
+
+# ---------------------------------------------------------------- 8-bit paged caches
+
+_FP8_TYPES = {torch.float32: 0, torch.bfloat16: 1}      # csa_type_t
+
+
+def _fp8_pool(cache, scales, page_rows: int) -> tuple:
+    """Page strides (rows) of a cache float8_e4m3fn [num_pages, at least
+    page_rows, width] and of its scales float32 [num_pages, at least page_rows]:
+    each a whole pool, or one layer's part of it."""
+    if cache.dtype != torch.float8_e4m3fn or cache.dim() != 3:
+        raise ValueError("cache must be float8_e4m3fn [num_pages, rows of a page, width], "
+                         f"got {cache.dtype} {tuple(cache.shape)}")
+    if scales.dtype != torch.float32 or scales.dim() != 2 or scales.shape[0] != cache.shape[0]:
+        raise ValueError(f"scales must be float32 [{int(cache.shape[0])}, rows of a page], "
+                         f"got {scales.dtype} {tuple(scales.shape)}")
+    return _page_stride(cache, page_rows), _page_stride(scales, page_rows)
+
+
+class AppendJobFp8:
+    """Rows [n, width] (bfloat16 or float32, dense within a row, any pitch) to
+    slots [n] of a cache float8_e4m3fn [num_pages, at least page_rows, width]
+    and its scales float32 [num_pages, at least page_rows]: a whole pool, or
+    one layer's part of it (pool[:, first:first + page_rows])."""
+
+    def __init__(self, rows, slots, cache, scales, page_rows: int):
+        if rows.dim() != 2 or rows.dtype not in _FP8_TYPES:
+            raise ValueError(f"rows must be bfloat16 or float32 [n, width], got {rows.dtype} {tuple(rows.shape)}")
+        n, width = (int(x) for x in rows.shape)
+        apart, scales_apart = _fp8_pool(cache, scales, page_rows)
+        if cache.shape[2] != width:
+            raise ValueError(f"cache rows hold {int(cache.shape[2])} values, rows {width}")
+        if n and not rows[0].is_contiguous():
+            raise ValueError("a row must be contiguous")
+        size = rows.element_size()
+        self.tensors, self.device = (rows, slots, cache, scales), cache.device.index
+        self.c = csa_append_fp8_job_t(
+            rows=_arg("rows", rows, rows.dtype, contiguous=False),
+            slots=_arg("slots", slots, torch.int64, (n,)), num_rows=n,
+            row_pitch=rows.stride(0) * size if n > 1 else width * size, type=_FP8_TYPES[rows.dtype],
+            width=width, page_rows=page_rows, num_pages=int(cache.shape[0]), page_stride=apart,
+            scale_stride=scales_apart, cache=_arg("cache", cache, cache.dtype, contiguous=False),
+            scales=_arg("scales", scales, torch.float32, contiguous=False))
+
+
+class AppendJobsFp8:
+    """Up to four AppendJobFp8 for one launch."""
+
+    def __init__(self, jobs):
+        self.jobs = list(jobs)
+        if not 1 <= len(self.jobs) <= MAX_APPEND_JOBS:
+            raise ValueError(f"1 to {MAX_APPEND_JOBS} jobs, got {len(self.jobs)}")
+        self.device = self.jobs[0].device
+        if any(j.device != self.device for j in self.jobs):
+            raise ValueError(f"jobs on devices {[j.device for j in self.jobs]}: one call runs on one")
+        self.c = (csa_append_fp8_job_t * len(self.jobs))(*[j.c for j in self.jobs])
+
+
+def csa_paged_append_fp8(jobs: AppendJobsFp8, dev_status, stream=None):
+    s = _device_stream("csa_paged_append_fp8", jobs.device, stream)
+    _check("csa_paged_append_fp8", load().csa_paged_append_fp8(jobs.c, len(jobs.jobs),
+                                                               _ptr(dev_status, jobs.device), s))
+
+
+def csa_paged_read_fp8(cache, scales, slots, out, dev_status, page_rows: int, stream=None):
+    """Rows `slots` [n] of an 8-bit cache (as for AppendJobFp8) into out [n,
+    width], bfloat16 or float32, dense within a row."""
+    if out.dim() != 2 or out.dtype not in _FP8_TYPES:
+        raise ValueError(f"out must be bfloat16 or float32 [n, width], got {out.dtype} {tuple(out.shape)}")
+    n, width = (int(x) for x in out.shape)
+    apart, scales_apart = _fp8_pool(cache, scales, page_rows)
+    if cache.shape[2] != width:
+        raise ValueError(f"cache rows hold {int(cache.shape[2])} values, out {width}")
+    if slots.dtype != torch.int64 or slots.shape != (n,):
+        raise ValueError(f"slots must be int64 [{n}], got {slots.dtype} {tuple(slots.shape)}")
+    if n and width > 1 and out.stride(1) != 1:
+        raise ValueError("a row must be contiguous")
+    size, dev = out.element_size(), out.get_device()
+    pitch = out.stride(0) * size if n > 1 else width * size
+    if pitch < width * size:
+        raise ValueError("rows of out must not overlap")
+    s = _device_stream("csa_paged_read_fp8", dev, stream)
+    r = csa_read_fp8_t(
+        cache=_ptr(cache, dev, contiguous=False), scales=_ptr(scales, dev, contiguous=False),
+        slots=_ptr(slots, dev), num_rows=n, width=width, page_rows=page_rows,
+        num_pages=cache.shape[0], page_stride=apart, scale_stride=scales_apart,
+        type=_FP8_TYPES[out.dtype], out_pitch=pitch, out=_ptr(out, dev, contiguous=False))
+    _check("csa_paged_read_fp8", load().csa_paged_read_fp8(ctypes.byref(r), _ptr(dev_status, dev), s))
+
+
+class PagedLayoutFp8(PagedLayout):
+    """csa_paged_attention_fp8's layout: PagedLayout with the window ring in
+    8 bits, swa_kv float8_e4m3fn [B, swa_cap, 512] and swa_scales float32 [B,
+    swa_cap] (None without a window)."""
+
+    ring_type = torch.float8_e4m3fn
+
+    def __init__(self, tok_seq, tok_pos, row_len, table, page_rows: int, swa_kv=None,
+                 swa_scales=None, swa_first_pos=None):
+        super().__init__(tok_seq, tok_pos, row_len, table, page_rows, swa_kv, swa_first_pos)
+        self.swa_scales, self.swa_scales_at = swa_scales, None
+        if swa_kv is not None:
+            if swa_scales is None:
+                raise ValueError("swa_kv needs swa_scales")
+            self.swa_scales_at = _arg("swa_scales", swa_scales, torch.float32, swa_kv.shape[:2])
+
+
+def csa_paged_attention_fp8(layout: PagedLayoutFp8, prm: csa_params_t, cache, scales, q, out,
+                            dev_status, ws, sinks=None, stream=None):
+    """cache float8_e4m3fn [num_pages, at least page_rows, 512] and scales
+    float32 [num_pages, at least page_rows] (whole pools, or one layer's part
+    of them), q bf16 [T, H, 512], out f32 or bf16 [T, H, 512], ws
+    paged_workspace(layout, prm)."""
+    dev = layout.device
+    s = _device_stream("csa_paged_attention_fp8", dev, stream)
+    if not isinstance(layout, PagedLayoutFp8):
+        raise ValueError("layout must be a PagedLayoutFp8")
+    if q.dtype != torch.bfloat16:
+        raise ValueError("q must be bfloat16")
+    if out.dtype not in _FP8_TYPES:
+        raise ValueError("out must be float32 or bfloat16")
+    shape = (layout.num_tokens, prm.n_heads, prm.hd)
+    if q.shape != shape or out.shape != shape:
+        raise ValueError(f"q and out must have shape {shape}")
+    apart, scales_apart = _fp8_pool(cache, scales, layout.c.page_rows)
+    if cache.shape[2] != prm.hd:
+        raise ValueError(f"cache must have shape (num_pages, rows of a page, {prm.hd})")
+    if sinks is not None and (sinks.dtype != torch.float32 or sinks.shape != (prm.n_heads,)):
+        raise ValueError(f"sinks must be float32 [{prm.n_heads}]")
+    _check("csa_paged_attention_fp8", load().csa_paged_attention_fp8(
+        layout.ref, ctypes.byref(prm), _ptr(cache, dev, contiguous=False),
+        _ptr(scales, dev, contiguous=False), layout.swa_scales_at, cache.shape[0], apart, scales_apart,
+        _ptr(q, dev), None if sinks is None else _ptr(sinks, dev), _FP8_TYPES[out.dtype], _ptr(out, dev),
+        _ptr(dev_status, dev), _ptr(ws, dev), ws.numel(), s))

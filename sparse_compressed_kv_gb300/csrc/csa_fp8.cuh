@@ -1,0 +1,45 @@
+// csa_fp8.cuh -- e4m3 codes and their scales on the device.
+#pragma once
+
+#include "csa_device.cuh"
+
+namespace csa {
+
+constexpr int kFp8MaxExp = 60;      // scales are 2^-60 .. 2^60
+
+// 2^k, -126 <= k <= 127
+__device__ __forceinline__ float exponent_f32(int k) { return __uint_as_float(static_cast<uint32_t>(k + 127) << 23); }
+
+// two values to e4m3 (to nearest, ties to even, saturating; NaN stays NaN), the
+// first in the low byte
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    return e4m3x2(a, b) | e4m3x2(c, d) << 16;
+}
+
+// two codes to f16, exactly
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t codes) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+    return r;
+}
+__device__ __forceinline__ float2 f16x2_values(uint32_t h) {
+    float2 v;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(v.x), "=f"(v.y)
+        : "r"(h));
+    return v;
+}
+__device__ __forceinline__ void e4m3x4_values(uint32_t codes, float *v) {
+    const float2 a = f16x2_values(e4m3x2_f16x2(codes)), b = f16x2_values(e4m3x2_f16x2(codes >> 16));
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = b.x;
+    v[3] = b.y;
+}
+
+}  // namespace csa

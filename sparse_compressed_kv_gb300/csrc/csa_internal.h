@@ -196,6 +196,14 @@ cudaError_t launch_paged_attention(const Launch &lc, const csa_paged_layout_t &L
                                    int64_t page_stride, const void *q, const float *sinks,
                                    csa_type_t out_type, void *out, int32_t *status, void *ws);
 
+// The same over e4m3 rows with a scale each (csa_paged_attention_fp8.cu).
+cudaError_t launch_paged_attention_fp8(const Launch &lc, const csa_paged_layout_t &L,
+                                       const csa_params_t &p, const void *cache, const float *scales,
+                                       const float *swa_scales, int64_t num_pages,
+                                       int64_t page_stride, int64_t scale_stride, const void *q,
+                                       const float *sinks, csa_type_t out_type, void *out,
+                                       int32_t *status, void *ws);
+
 // Division of 32-bit numbers by a number known on the host: a high product, an
 // average and a shift instead of a division (T. Granlund, P. Montgomery,
 // "Division by invariant integers using multiplication", 1994).
