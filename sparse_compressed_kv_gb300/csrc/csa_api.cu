@@ -108,8 +108,8 @@ CUresult encode_tensor_map_2d_bf16(CUtensorMap *map, const void *base, uint64_t 
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-CUresult encode_tensor_map_bf16(CUtensorMap *map, const void *base, uint32_t rank,
-                                const uint64_t *dims, const uint64_t *strides, const uint32_t *box) {
+static CUresult encode_sw128(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint32_t rank,
+                             const uint64_t *dims, const uint64_t *strides, const uint32_t *box) {
     resolve_encode();
     if (!g_encode) return CUDA_ERROR_NOT_SUPPORTED;
     cuuint64_t d[5], s[4];
@@ -120,9 +120,19 @@ CUresult encode_tensor_map_bf16(CUtensorMap *map, const void *base, uint32_t ran
         e[i] = 1;
         if (i + 1 < rank) s[i] = strides[i];
     }
-    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), d, s, b, e,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return g_encode(map, type, rank, const_cast<void *>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+CUresult encode_tensor_map_bf16(CUtensorMap *map, const void *base, uint32_t rank,
+                                const uint64_t *dims, const uint64_t *strides, const uint32_t *box) {
+    return encode_sw128(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides, box);
+}
+
+CUresult encode_tensor_map_u8(CUtensorMap *map, const void *base, uint32_t rank,
+                              const uint64_t *dims, const uint64_t *strides, const uint32_t *box) {
+    return encode_sw128(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rank, dims, strides, box);
 }
 
 CUresult encode_tensor_map_2d_u8(CUtensorMap *map, const void *base, uint64_t inner_bytes,

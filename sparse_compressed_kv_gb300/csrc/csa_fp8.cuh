@@ -42,4 +42,27 @@ __device__ __forceinline__ void e4m3x4_values(uint32_t codes, float *v) {
     v[3] = b.y;
 }
 
+// ---------------------------------------------------------------- tensor cores
+
+// Instruction descriptor: kind::f8f6f4, A e4m3, B e4m3 or e5m2, f32 accumulator,
+// M x N, A transposed (MN-major) or not.
+template <int M, int N, bool kTransA, bool kE5m2B>
+__device__ __forceinline__ constexpr uint32_t idesc_fp8() {
+    return (1u << 4)                                // D: f32
+           | ((kE5m2B ? 1u : 0u) << 10)             // (A: 0, e4m3)
+           | ((kTransA ? 1u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// 8-bit operands from shared memory, K = 32
+__device__ __forceinline__ void umma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 }  // namespace csa

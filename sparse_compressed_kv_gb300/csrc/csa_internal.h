@@ -284,6 +284,8 @@ CUresult encode_tensor_map_2d_bf16(CUtensorMap *map, const void *base, uint64_t 
 // 1 ..) in bytes; 128-byte swizzle, zeros out of bounds.
 CUresult encode_tensor_map_bf16(CUtensorMap *map, const void *base, uint32_t rank,
                                 const uint64_t *dims, const uint64_t *strides, const uint32_t *box);
+CUresult encode_tensor_map_u8(CUtensorMap *map, const void *base, uint32_t rank,
+                              const uint64_t *dims, const uint64_t *strides, const uint32_t *box);
 // Dense byte rows of inner_bytes each, no swizzle.
 CUresult encode_tensor_map_2d_u8(CUtensorMap *map, const void *base, uint64_t inner_bytes,
                                  uint64_t outer, uint32_t box_inner, uint32_t box_outer);

@@ -12,6 +12,9 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kHG = 64;                         // heads per CTA
+constexpr int kSmThreads = 128;                 // warps 4..7 (softmax); 8..11 (products, epilogue)
+constexpr int kBarSm = 1;
+constexpr int kOutBytes = 1024;                 // of an epilogue warp: 32 columns x 16 heads in bf16
 constexpr int kMaxRec = 64;                     // segments a CTA lists at a time
 constexpr int kMaxCtas = 152;                   // CTAs of the grid at most (sizes the workspace)
 
@@ -334,6 +337,149 @@ struct Work {
         s0 = S.s0;
     }
 };
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, P;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
+                                            int32_t z, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
+// Unswizzled K-major operand: atoms of 8 rows x 16 bytes, 128 contiguous bytes
+// each, `lbo` apart along K and `sbo` along the rows.
+__device__ __forceinline__ uint64_t atom_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return sw128_desc(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7u) << 61);
+}
+
+// a byte offset as a step of a descriptor's start-address field (every shared
+// address is below 256 KiB, so the field never carries)
+__device__ __forceinline__ constexpr uint64_t off(uint32_t bytes) { return bytes >> 4; }
+
+// O^T of a stretch into the partial, or the output, by the four epilogue warps:
+// tile by tile, each handed back to the products once it is in registers.
+//   o_tmem  the first tile's first column, in this warp's lanes; each tile has 64
+//           columns (heads), the first kWide ones 64 more that are added to them
+//   add     the partial holds earlier stretches, to be scaled by `flush`
+//   part    leave (O, m, l); otherwise the output, scaled by `fin`
+template <bool kBf16, int kWide>
+__device__ __forceinline__ void drain_stretch(const PagedArgs &A, uint32_t o_tmem, const float *fin,
+                                              const float *flush, uint64_t *ofree, uint8_t *sOut, int dt0,
+                                              int ndt, int hmax, int64_t obase, int64_t pslot, bool add,
+                                              bool part) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int dl = (warp & 3) * 32 + lane;       // column of a tile
+#pragma unroll 1
+    for (int dd = 0; dd < ndt; ++dd) {
+        // one column per lane; a partial keeps four heads together,
+        // so that a warp stores 512 contiguous bytes
+        float4 *const pd = A.part_o + (pslot * 4 + dt0 + dd) * (16 * 128) + dl;
+#pragma unroll 1
+        for (int hb = 0; hb < kHG; hb += 32) {
+            if (hb >= hmax) break;
+            uint32_t o[32];
+            const uint32_t oc = o_tmem + kHG * (dd + (dd < kWide ? dd : kWide)) + hb;
+            tmem_ld16_raw(oc, *reinterpret_cast<uint32_t(*)[16]>(o));
+            tmem_ld16_raw(oc + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
+            float4 *const pq = pd + hb / 4 * 128;
+            if (dd < kWide) {
+#pragma unroll
+                for (int y = 0; y < 32; y += 16) {
+                    uint32_t lo[16];
+                    tmem_ld16_raw(oc + kHG + y, lo);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        o[x + y] = __float_as_uint(__uint_as_float(o[x + y]) + __uint_as_float(lo[x]));
+                }
+            }
+            if (add) {
+                float4 old[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) old[x] = pq[x * 128];
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const float4 f = *reinterpret_cast<const float4 *>(flush + hb + 4 * x);
+                    o[4 * x] = __float_as_uint(fmaf(old[x].x, f.x, __uint_as_float(o[4 * x])));
+                    o[4 * x + 1] = __float_as_uint(fmaf(old[x].y, f.y, __uint_as_float(o[4 * x + 1])));
+                    o[4 * x + 2] = __float_as_uint(fmaf(old[x].z, f.z, __uint_as_float(o[4 * x + 2])));
+                    o[4 * x + 3] = __float_as_uint(fmaf(old[x].w, f.w, __uint_as_float(o[4 * x + 3])));
+                }
+            }
+            tmem_wait_ld();
+            if (hb + 32 >= hmax) {           // the tile is in registers
+                tc_fence_before();
+                mbar_arrive(&ofree[dd]);
+            }
+            if (part) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    pq[x * 128] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                              __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+                continue;
+            }
+            // (all factors before the first store, which the compiler
+            // would not let a later factor's load pass: 5,600 instead
+            // of 14,100 cycles for 64 heads)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float4 f = *reinterpret_cast<const float4 *>(fin + hb + 4 * x);
+                o[4 * x] = __float_as_uint(__uint_as_float(o[4 * x]) * f.x);
+                o[4 * x + 1] = __float_as_uint(__uint_as_float(o[4 * x + 1]) * f.y);
+                o[4 * x + 2] = __float_as_uint(__uint_as_float(o[4 * x + 2]) * f.z);
+                o[4 * x + 3] = __float_as_uint(__uint_as_float(o[4 * x + 3]) * f.w);
+            }
+            const int64_t at = obase + hb * kHD + (dt0 + dd) * 128;
+            if constexpr (kBf16) {
+                // through shared memory, so that a lane stores 16 bytes of a head (256
+                // tokens of 1K rows 74.2 -> 72.4 us against a column a lane)
+                __nv_bfloat16 *const stage =
+                    reinterpret_cast<__nv_bfloat16 *>(sOut + (warp & 3) * kOutBytes);
+                __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(A.out) + at +
+                                           (lane >> 2) * kHD + (warp & 3) * 32 + (lane & 3) * 8;
+#pragma unroll
+                for (int y = 0; y < 32; y += 16) {
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        stage[x * 32 + lane] = __float2bfloat16(__uint_as_float(o[x + y]));
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < 16; x += 8) {
+                        const uint4 v = reinterpret_cast<const uint4 *>(stage)[x * 4 + lane];
+                        if (hb + x + y + (lane >> 2) < hmax) *reinterpret_cast<uint4 *>(dst + (x + y) * kHD) = v;
+                    }
+                }
+                __syncwarp();                // (some lanes stored, some did not)
+            } else {
+                // a column a lane (16 bytes a lane: 83.8 -> 84.6 us for 128-head drafts)
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    if (hb + x < hmax) static_cast<float *>(A.out)[at + x * kHD + dl] = __uint_as_float(o[x]);
+            }
+        }
+    }
+}
 
 // Joins the parts of a cut token:
 //   out = sum_s 2^(m_s - M) O_s / (sum_s 2^(m_s - M) l_s [+ 2^(sink - M)]).
