@@ -65,4 +65,16 @@ __device__ __forceinline__ void umma_fp8(uint32_t d_tmem, uint64_t a_desc, uint6
         : "memory");
 }
 
+// The same with A from tensor memory: row m in lane m, the 32 bytes of a K step in
+// 8 columns.
+__device__ __forceinline__ void umma_fp8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 }  // namespace csa

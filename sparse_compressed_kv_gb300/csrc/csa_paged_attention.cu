@@ -52,6 +52,8 @@
 namespace csa {
 namespace {
 
+constexpr int kThreads = 384;
+constexpr int kSmThreads = 128;                 // warps 4..7
 constexpr int kChunk = 48;
 constexpr int kSlices = kChunk / 16;            // of 16 rows: one K step of O^T each
 constexpr int kQBytes = kHG * kHD * 2;          // 64 KiB
@@ -59,8 +61,9 @@ constexpr int kGroupBytes = 8 * kHD * 2;        // 8 rows: 8 KiB
 constexpr int kStageBytes = kChunk / 8 * kGroupBytes;   // 48 KiB
 constexpr int kStages = 3;
 constexpr int kPBytes = kHG * kChunk * 2;       // one bf16 term of P: 6 KiB
+constexpr int kStagedHeads = 16;                // of a bf16 output, on their way through shared memory
 template <int kTerms>
-constexpr int kStagedBytes = kTerms == 1 ? 4 * kOutBytes : 0;
+constexpr int kStagedBytes = kTerms == 1 ? 4 * staged_bytes(kStagedHeads) : 0;
 constexpr int kSCol = 0;                        // two S buffers of 64 columns
 constexpr int kOCol = 128;                      // O^T: 4 tiles x 64 heads
 constexpr uint32_t kTmemCols = 512;
@@ -73,6 +76,7 @@ template <int kTerms>
 __device__ __forceinline__ constexpr uint32_t o_col(int dd) {
     return kOCol + kHG * (dd + (dd < kWide<kTerms> ? dd : kWide<kTerms>));
 }
+constexpr int kMaxRec = 64;                     // segments a CTA lists at a time
 constexpr int kSegCost = 4;                     // a segment's epilogue, in chunks (3: 128 contexts of 512 rows 30.3
                                                 // us instead of 29.3; 2: 128-head drafts 82.5 instead of 76.5)
 // Chunks a token may exceed the mean before tokens are cut.  (240 rows; 2 and 3
@@ -97,7 +101,7 @@ struct Smem {
     float alpha[kHG];
     alignas(16) float fin[2][kHG];     // of a stretch: factors of the output,
     alignas(16) float flush[2][kHG];   // and of the partial so far
-    WorkSmem work;
+    WorkSmem<kMaxRec> work;
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *m, int32_t x, int32_t y,
@@ -154,9 +158,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&S.pfree, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.stretch[i], kSmThreads);
-            mbar_init(&S.stretch_free[i], kSmThreads);
+            mbar_init(&S.stretch_free[i], kEpThreads);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&S.ofree[i], kSmThreads);
+        for (int i = 0; i < 4; ++i) mbar_init(&S.ofree[i], kEpThreads);
         mbar_fence_init();
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_rows);
@@ -167,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
 
-    Work<kChunk, kSegCost, kCutAbove> W(A, S.work);
+    Work<kThreads, kMaxRec, kChunk, kSegCost, kCutAbove> W(A, S.work);
     W.count();
     __syncthreads();
     tc_fence_after();
@@ -328,8 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ++n_ep;
                         __syncwarp();
                         tc_fence_after();
-                        drain_stretch<kTerms == 1, kWide<kTerms>>(
-                            A, tmem + lane_off + kOCol, S.fin[e], S.flush[e], S.ofree, sOut, dt0, ndt, hmax, obase, pslot,
+                        drain_stretch<kTerms == 1, kWide<kTerms>, kStagedHeads>(
+                            A, tmem + lane_off + kOCol, S.fin[e], S.flush[e], S.ofree, sOut + (warp & 3) * staged_bytes(kStagedHeads), dt0,
+                            ndt, 0, kHG, hmax, obase, pslot,
                             add, part);
                         mbar_arrive(&S.stretch_free[e]);
                         __syncwarp();

@@ -10,12 +10,11 @@
 namespace csa {
 namespace {
 
-constexpr int kThreads = 384;
 constexpr int kHG = 64;                         // heads per CTA
-constexpr int kSmThreads = 128;                 // warps 4..7 (softmax); 8..11 (products, epilogue)
+constexpr int kEpThreads = 128;                 // four warps: the epilogue, which also issue the products
 constexpr int kBarSm = 1;
-constexpr int kOutBytes = 1024;                 // of an epilogue warp: 32 columns x 16 heads in bf16
-constexpr int kMaxRec = 64;                     // segments a CTA lists at a time
+// of an epilogue warp, on their way to a bf16 output: 32 columns of some heads
+constexpr int staged_bytes(int heads) { return heads * 32 * 2; }
 constexpr int kMaxCtas = 152;                   // CTAs of the grid at most (sizes the workspace)
 
 struct PagedArgs {
@@ -103,22 +102,23 @@ __device__ __forceinline__ int flush_every(int nch) {
 
 // The division of the work, the part in shared memory: counts, and the list of
 // the CTA's next segments.
+template <int kMaxRec>
 struct WorkSmem {
     int32_t nrec, more;
     int32_t t0, s0;
-    int2 wsum[kThreads / 32];    // cost, most chunks of a token
+    int2 wsum[16];               // of a warp: cost, most chunks of a token
     Rec rec[kMaxRec];
 };
 
-// Every CTA counts the chunks of kChunk row slots of all tokens for itself and
-// takes an equal contiguous range of them; a segment costs kSegCost chunks more.
+// Every CTA (of kThreads threads) counts the chunks of kChunk row slots of all tokens for itself and
+// takes an equal contiguous range of them, kMaxRec segments at a time; a segment costs kSegCost chunks more.
 // Used by all threads: count(), a barrier, divide(), first_list(), then next_list()
 // between barriers while S.more is set.  (The layout is read before the wait for
 // the preceding kernel, as everywhere in this library.)
-template <int kChunk, int kSegCost, int kCutAbove>
+template <int kThreads, int kMaxRec, int kChunk, int kSegCost, int kCutAbove>
 struct Work {
     const PagedArgs &A;
-    WorkSmem &S;
+    WorkSmem<kMaxRec> &S;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = gridDim.x, T = A.L.num_tokens;
     const bool by_token = T <= G;
@@ -132,7 +132,7 @@ struct Work {
     int split = 0, share = 0, ua = 0, ub = 0, t0 = 0, s0 = 0;
     int ndt = 4, dt0 = 0;                // 128-column tiles of this CTA, the first
 
-    __device__ __forceinline__ Work(const PagedArgs &args, WorkSmem &smem) : A(args), S(smem) {}
+    __device__ __forceinline__ Work(const PagedArgs &args, WorkSmem<kMaxRec> &smem) : A(args), S(smem) {}
 
     static __device__ __forceinline__ int chunks(const Rec &r) {
         return r.b < 0 ? 0 : (rec_slots(r) + kChunk - 1) / kChunk;
@@ -375,16 +375,18 @@ __device__ __forceinline__ uint64_t atom_desc(uint32_t saddr, uint32_t lbo, uint
 // address is below 256 KiB, so the field never carries)
 __device__ __forceinline__ constexpr uint64_t off(uint32_t bytes) { return bytes >> 4; }
 
-// O^T of a stretch into the partial, or the output, by the four epilogue warps:
-// tile by tile, each handed back to the products once it is in registers.
+// O^T of a stretch into the partial, or the output, by the epilogue's warps: tile by
+// tile, each handed back to the products once it is in registers.  A warp has the
+// columns of its quarter and the heads hb0 .. hb1 - 1 (multiples of 32) below hmax.
 //   o_tmem  the first tile's first column, in this warp's lanes; each tile has 64
 //           columns (heads), the first kWide ones 64 more that are added to them
 //   add     the partial holds earlier stretches, to be scaled by `flush`
+//   sOut    staged_bytes(kStagedHeads) of this warp's own, for a bf16 output
 //   part    leave (O, m, l); otherwise the output, scaled by `fin`
-template <bool kBf16, int kWide>
+template <bool kBf16, int kWide, int kStagedHeads>
 __device__ __forceinline__ void drain_stretch(const PagedArgs &A, uint32_t o_tmem, const float *fin,
                                               const float *flush, uint64_t *ofree, uint8_t *sOut, int dt0,
-                                              int ndt, int hmax, int64_t obase, int64_t pslot, bool add,
+                                              int ndt, int hb0, int hb1, int hmax, int64_t obase, int64_t pslot, bool add,
                                               bool part) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int dl = (warp & 3) * 32 + lane;       // column of a tile
@@ -394,8 +396,11 @@ __device__ __forceinline__ void drain_stretch(const PagedArgs &A, uint32_t o_tme
         // so that a warp stores 512 contiguous bytes
         float4 *const pd = A.part_o + (pslot * 4 + dt0 + dd) * (16 * 128) + dl;
 #pragma unroll 1
-        for (int hb = 0; hb < kHG; hb += 32) {
-            if (hb >= hmax) break;
+        for (int hb = hb0; hb < hb1; hb += 32) {
+            if (hb >= hmax) {                    // (hb0: nothing to do)
+                if (hb == hb0) mbar_arrive(&ofree[dd]);
+                break;
+            }
             uint32_t o[32];
             const uint32_t oc = o_tmem + kHG * (dd + (dd < kWide ? dd : kWide)) + hb;
             tmem_ld16_raw(oc, *reinterpret_cast<uint32_t(*)[16]>(o));
@@ -427,7 +432,7 @@ __device__ __forceinline__ void drain_stretch(const PagedArgs &A, uint32_t o_tme
                 }
             }
             tmem_wait_ld();
-            if (hb + 32 >= hmax) {           // the tile is in registers
+            if (hb + 32 >= min(hb1, hmax)) { // the tile is in registers
                 tc_fence_before();
                 mbar_arrive(&ofree[dd]);
             }
@@ -454,18 +459,18 @@ __device__ __forceinline__ void drain_stretch(const PagedArgs &A, uint32_t o_tme
                 // through shared memory, so that a lane stores 16 bytes of a head (256
                 // tokens of 1K rows 74.2 -> 72.4 us against a column a lane)
                 __nv_bfloat16 *const stage =
-                    reinterpret_cast<__nv_bfloat16 *>(sOut + (warp & 3) * kOutBytes);
+                    reinterpret_cast<__nv_bfloat16 *>(sOut);
                 __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(A.out) + at +
                                            (lane >> 2) * kHD + (warp & 3) * 32 + (lane & 3) * 8;
 #pragma unroll
-                for (int y = 0; y < 32; y += 16) {
+                for (int y = 0; y < 32; y += kStagedHeads) {
                     __syncwarp();
 #pragma unroll
-                    for (int x = 0; x < 16; ++x)
+                    for (int x = 0; x < kStagedHeads; ++x)
                         stage[x * 32 + lane] = __float2bfloat16(__uint_as_float(o[x + y]));
                     __syncwarp();
 #pragma unroll
-                    for (int x = 0; x < 16; x += 8) {
+                    for (int x = 0; x < kStagedHeads; x += 8) {
                         const uint4 v = reinterpret_cast<const uint4 *>(stage)[x * 4 + lane];
                         if (hb + x + y + (lane >> 2) < hmax) *reinterpret_cast<uint4 *>(dst + (x + y) * kHD) = v;
                     }

@@ -5,15 +5,16 @@
 // The division of the work, the segments, the partials and the joins are those
 // of the bf16 rows' kernel (csa_paged_attention.cuh); a chunk is 64 row slots, and
 // the codes are the tensor cores' operands as they lie in memory:
-//   warps 0..3    fetch a chunk's rows, 16 each: 8 rows of one page are one TMA box
-//                 (128 columns x 8 rows x 4 column groups: 4 KiB), others go row
-//                 by row with 16-byte cp.async; and each row's scale
-//   warps 4..7    the query, 16 heads each, split in two e4m3 terms where a segment
-//                 begins; softmax with a lazily raised maximum
-//   warps 8..11   warp 8: S = Q . rows^T (M = 64 heads x 2 terms, N = 64 rows, K =
-//                 512), one chunk ahead of warp 9: O^T += rows^T . P^T (M = 128
-//                 columns a tile, N = 64 heads, K = 64 rows); all four: a segment's
-//                 epilogue
+//   warps 0..7    the query, 8 heads each, split in two e4m3 terms where a segment
+//                 begins; softmax with a lazily raised maximum, warps 0..3 of the
+//                 chunk's rows 0..31, warps 4..7 of the others;
+//                 and a segment's epilogue, under the next segment's first logits
+//   warp 8        S = Q . rows^T (M = 64 heads x 2 terms from tensor memory, N = 64
+//                 rows, K = 512)
+//   warp 9        O^T += rows^T . P^T (M = 128 columns a tile, N = 64 heads, K = 64 rows)
+//   warps 10, 11  fetch a chunk's rows, 32 each: 8 rows of one page are one TMA box
+//                 (128 columns x 8 rows x 4 column groups: 4 KiB), others go row by
+//                 row with 16-byte cp.async; and each row's scale
 // A group's 4 KiB hold 4 column groups of 8 rows x 128 bytes (the swizzle atom):
 // the K-major operand of S and the MN-major operand of O^T.
 //
@@ -40,30 +41,43 @@
 namespace csa {
 namespace {
 
+constexpr int kThreads = 384;
+constexpr int kBarQ = 2;                        // 2 .. 5: the two warps of a quarter of the softmax
+constexpr int kSmThreads = 256;                 // warps 0..7, half of them for each 32 rows of a chunk
+constexpr int kSmGroup = kSmThreads / 2;
 constexpr int kChunk = 64;
-constexpr int kSlices = kChunk / 16;            // of 16 rows, one per fetch warp
-constexpr int kSteps = kChunk / 32;             // of 32 rows: one K step of O^T each
-constexpr int kQBytes = 2 * kHG * kHD;          // 64 KiB
+constexpr int kSteps = kChunk / 32;             // of 32 rows: a fetch warp, half of the softmax, a K step of O^T each
 constexpr int kGroupBytes = 8 * kHD;            // 8 rows: 4 KiB
 constexpr int kStageBytes = kChunk / 8 * kGroupBytes;   // 32 KiB
-constexpr int kStages = 4;
+// What shared memory has room for beside two buffers of P (12 KiB each, 24 KiB with
+// an f32 output).
+template <int kTerms>
+constexpr int kStages = kTerms == 3 ? 6 : 5;
+constexpr int kPBufs = 2;
+constexpr int kMaxStages = 6;
+constexpr int kStagedHeads = 16;                // of a bf16 output, on their way through shared memory (P's)
 constexpr int kTermBytes = kHG * 16;            // 16 rows of a term of P
 template <int kTerms>
 constexpr int kPieceBytes = kTerms * kTermBytes;
-template <int kTerms>
-constexpr int kStagedBytes = kTerms == 3 ? 4 * kOutBytes : 0;
 constexpr int kSCol = 0;                        // two S buffers of 64 columns
 constexpr int kOCol = 128;                      // O^T: 4 tiles x 64 heads
+constexpr int kQCol = 384;                      // the query: 128 rows x 512 codes
 constexpr uint32_t kTmemCols = 512;
-// The first two tiles take two terms from one reading of the rows (N = 128: 64.6
-// cycles instead of twice 48.3) into 64 columns each; tensor memory has room for
-// no more.
-constexpr int kWide = 2;
-__device__ __forceinline__ constexpr uint32_t o_col(int dd) { return kOCol + kHG * (dd + (dd < kWide ? dd : kWide)); }
+constexpr int kMaxRec = 32;                     // segments a CTA lists at a time
 constexpr int kSegCost = 3;                     // a segment's epilogue, in chunks
 constexpr int kCutAbove = 4;                    // chunks a token may exceed the mean before tokens are cut
 constexpr int kFlushF32 = 27, kFlushBf16 = 341; // chunks between roundings of the accumulator, at most
 constexpr float kTop = 7.f;                     // log2 of the weight that the maximum is brought to
+
+// mbar_wait whose loop is a call: the first try is nearly all that stays in line (what
+// the roles run together is more than the instruction caches next to the schedulers
+// hold; 32 contexts 95.6 -> 92.6 us).
+__device__ __noinline__ void wait_slowly(uint64_t *bar, uint32_t parity, int32_t *status) {
+    mbar_wait(bar, parity, status);
+}
+__device__ __forceinline__ void wait_for(uint64_t *bar, uint32_t parity, int32_t *status) {
+    if (__builtin_expect(!mbar_try_wait(bar, parity), 0)) wait_slowly(bar, parity, status);
+}
 
 struct PagedFp8Args : PagedArgs {
     const uint8_t *codes;
@@ -74,21 +88,53 @@ struct PagedFp8Args : PagedArgs {
 
 struct Smem {
     uint64_t q_full;
-    uint64_t full[kStages], empty[kStages][kSteps];    // a stage is released 32 rows at a time
+    uint64_t full[kMaxStages], empty[kMaxStages][kSteps];    // a stage is released 32 rows at a time
     uint64_t sfull[2], sfree[2];
-    uint64_t pfull[kSteps], pfree;
-    uint64_t stretch[2], stretch_free[2];   // the factors of a stretch are written, used
+    uint64_t pfull[2][kSteps], pfree[2];
     uint64_t ofree[4];           // a tile of O^T is drained
     uint32_t tmem_holder;
-    uint32_t maskw[kStages][kSlices];
-    uint32_t flag[2][4];
-    float alpha[kHG];
-    alignas(16) float scale[kStages][kChunk];   // of a row (absent rows: 0),
-    alignas(16) float scale_log[kStages][kChunk];   // and its logarithm
-    alignas(16) float fin[2][kHG];     // of a stretch: factors of the output,
-    alignas(16) float flush[2][kHG];   // and of the partial so far
-    WorkSmem work;
+    uint32_t maskw[kMaxStages][kSteps];
+    uint32_t risen[4];           // heads to be rescaled, 16 a word
+    float alpha[kHG];            // ... and by what
+    float rise[2][kHG];          // the two halves' maxima, where one rose too far
+    float part_l[kHG];           // the second half's sum of weights
+    float q_scale[kHG];          // a head's factor from sums of codes to logits (log2 units)
+    alignas(16) float scale[kMaxStages][kChunk];   // of a row (absent rows: 0),
+    alignas(16) float scale_log[kMaxStages][kChunk];   // and its logarithm
+    alignas(16) float fin[kHG];        // of a stretch: factors of the output,
+    alignas(16) float flush[kHG];      // and of the partial so far
+    WorkSmem<kMaxRec> work;
 };
+
+// Whether a thread of the softmax says so, behind a barrier of all of them.
+__device__ __forceinline__ bool any_of(bool mine) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(static_cast<uint32_t>(mine)), "n"(kBarSm), "n"(kSmThreads)
+        : "memory");
+    return any != 0;
+}
+
+// Two f32 operations an instruction.
+union Pair {
+    float2 v;
+    uint64_t u;
+};
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    Pair x{a}, y{b}, r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(x.u), "l"(y.u));
+    return r.v;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    Pair x{a}, y{b}, r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(x.u), "l"(y.u));
+    return r.v;
+}
 
 // 2 x 16 lanes of tensor memory: threads 0..15 read lanes 0..15 of the address at
 // columns c .. c + 15, threads 16..31 the same lanes at columns c + 16 .. c + 31.
@@ -111,10 +157,10 @@ __device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// the nearest e5m2 values of two f16, the first in the low byte
-__device__ __forceinline__ uint32_t f16x2_e5m2x2(uint32_t h) {
+// the nearest e4m3 values of two f16, the first in the low byte
+__device__ __forceinline__ uint32_t f16x2_e4m3x2(uint32_t h) {
     uint16_t r;
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
     return r;
 }
 
@@ -126,8 +172,10 @@ __device__ __forceinline__ uint32_t upper_bytes(uint32_t &a, uint32_t &b) {
     b = f16x2_sub(b, b & 0xFF00FF00u);
     return t;
 }
+// The last term: rounded, by half of the byte's last place (an addition; the
+// conversion instructions run at a quarter of its rate).
 __device__ __forceinline__ uint32_t last_bytes(uint32_t a, uint32_t b) {
-    return f16x2_e5m2x2(a) | f16x2_e5m2x2(b) << 16;
+    return __byte_perm(a + 0x00800080u, b + 0x00800080u, 0x7531);
 }
 
 // Four weights as kTerms words of four e5m2 values each.
@@ -152,37 +200,76 @@ __device__ __forceinline__ void split_weights(const float (&p)[4], uint32_t (&t)
     }
 }
 
-// One head of the query as the operand's rows r (hi) and r + 16 (lo) of 128; a
-// lane has 16 columns.  Returns the factor that takes sums of codes back to the
-// query's units (NaN where the query is not finite).
-__device__ __forceinline__ float split_query(const uint4 (&raw)[2], uint8_t *sQ, int r, int lane) {
-    const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
-    uint32_t top = 0;
+// 16 columns of a head of the query as codes hi and lo, by integer operations on
+// the bits of two numbers at a time: the 64 heads' 32,768 numbers are bound by the
+// instructions issued, some 8 a number with conversions and 6 so.  Returns the factor
+// that takes sums of codes back to the query's units (NaN where the query is not finite).
+__device__ __forceinline__ float split_query(const uint4 &v0, const uint4 &v1, uint4 &hi, uint4 &lo) {
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    uint32_t mag[8], top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+    for (int i = 0; i < 8; ++i) {
+        mag[i] = w[i] & 0x7FFF7FFFu;
+        top = __vmaxu2(top, mag[i]);
+    }
     top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
-    // 1.m 2^(e - 127) to 2^7
-    const int k = min(134 - static_cast<int>(top >> 7), 126);
-    const float f = exponent_f32(k);
-    uint32_t hi[4], lo[4];
+    // The largest exponent becomes 7 (f16's 22): bf16's exponent field moves down by
+    // `drop`, which leaves f16's bits without the last three; what would fall below
+    // f16's range becomes 0.
+    const uint32_t drop = max(top >> 7, 22u) - 22u;
+    const uint32_t d2 = drop << 7 | drop << 23;
+    uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float x[4];
+        uint32_t hc[2], lc[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            x[2 * j] = __uint_as_float(w[2 * i + j] << 16) * f;
-            x[2 * j + 1] = __uint_as_float(w[2 * i + j] & 0xFFFF0000u) * f;
+            const uint32_t m = __vmaxu2(mag[2 * i + j], d2) - d2;
+            // hi: three mantissa bits, nothing below 2^-6 (e4m3's normal numbers, whose
+            // exponent field is f16's less 8); its code in each half's upper byte
+            const uint32_t t = __vmaxu2(m, 0x04800480u) & 0x0FF00FF0u;
+            hc[j] = t * 16u - 0x40004000u;
+            lc[j] = f16x2_e4m3x2(f16x2_sub(m << 3, t << 3) ^ (w[2 * i + j] & 0x80008000u));
         }
-        hi[i] = e4m3x4(x[0], x[1], x[2], x[3]);
-        float h[4];
-        e4m3x4_values(hi[i], h);
-        lo[i] = e4m3x4(x[0] - h[0], x[1] - h[1], x[2] - h[2], x[3] - h[3]);
+        h[i] = __byte_perm(hc[0], hc[1], 0x7531) | (__byte_perm(w[2 * i], w[2 * i + 1], 0x7531) & 0x80808080u);
+        l[i] = lc[0] | lc[1] << 16;
     }
-    uint8_t *const at = sQ + (lane >> 3) * (2 * kHG * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
-                        (((lane & 7) ^ (r & 7)) << 4);
-    *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4 *>(at + 2 * 1024) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    return top >= 0x7F80u ? NAN : exponent_f32(-k);
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+    // 2^(drop + 22 - 134), by halves: the exponent may be out of range for one factor
+    const int k = static_cast<int>(drop) - 112;
+    return top >= 0x7F80u ? NAN : exponent_f32(k / 2) * exponent_f32(k - k / 2);
+}
+
+// A contiguous copy into shared memory, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_addr(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+// One 32-bit column of tensor memory, a lane a thread.
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+    return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float x) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(x)) : "memory");
+}
+
+// 32 lanes x 32 consecutive 32-bit columns from registers
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
 }
 
 // kTerms: e5m2 terms of P (6 for an f32 output, 3 for bf16).
@@ -192,13 +279,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kBf16 = kTerms == 3;
     constexpr int kFlush = kBf16 ? kFlushBf16 : kFlushF32;
     constexpr int kPiece = kPieceBytes<kTerms>;          // 16 rows of P
+    constexpr int kSt = kStages<kTerms>, kPB = kPBufs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem<1024>(smem_raw);
-    uint8_t *sQ = smem;                                  // [4 col groups][128 rows][128 B]
-    uint8_t *sRows = sQ + kQBytes;                       // [stage][8 groups][4 col groups][8 rows][128 B]
-    uint8_t *sP = sRows + kStages * kStageBytes;         // [16 rows of the chunk][term][64 heads][16 B]
-    uint8_t *sOut = sP + kChunk / 16 * kPiece;           // [epilogue warp][16 heads][32 columns], bf16 output
-    Smem &S = *reinterpret_cast<Smem *>(sOut + kStagedBytes<kTerms>);
+    uint8_t *sRows = smem;                               // [stage][8 groups][4 col groups][8 rows][128 B]
+    uint8_t *sP = sRows + kSt * kStageBytes;             // [buffer][16 rows of the chunk][term][64 heads][16 B]
+    Smem &S = *reinterpret_cast<Smem *>(sP + kPB * (kChunk / 16) * kPiece);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hg = blockIdx.y, h0 = hg * kHG;
@@ -206,18 +292,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         mbar_init(&S.q_full, kSmThreads);
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(&S.full[i], kSlices);
+        for (int i = 0; i < kSt; ++i) {
+            mbar_init(&S.full[i], kSteps);
             for (int k = 0; k < kSteps; ++k) mbar_init(&S.empty[i][k], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.sfull[i], 1);
             mbar_init(&S.sfree[i], kSmThreads);
-            mbar_init(&S.pfull[i], kSmThreads);
-            mbar_init(&S.stretch[i], kSmThreads);
-            mbar_init(&S.stretch_free[i], kSmThreads);
+            for (int k = 0; k < kSteps; ++k) mbar_init(&S.pfull[i][k], kSmGroup);
+            mbar_init(&S.pfree[i], 1);
         }
-        mbar_init(&S.pfree, 1);
         for (int i = 0; i < 4; ++i) mbar_init(&S.ofree[i], kSmThreads);
         mbar_fence_init();
         tma_prefetch_desc(&tm_rows);
@@ -227,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     tc_fence_before();
-    Work<kChunk, kSegCost, kCutAbove> W(A, S.work);
+    Work<kThreads, kMaxRec, kChunk, kSegCost, kCutAbove> W(A, S.work);
     W.count();
     __syncthreads();
     tc_fence_after();
@@ -239,10 +323,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // pipeline positions, kept across lists of segments
     uint32_t n_fetch = 0;                // chunks fetched
-    uint32_t nq = 0, np = 0;             // chunks whose S / O^T product was issued
-    uint32_t n_ql = 0;                   // queries used
-    uint32_t n_sm = 0;                   // chunks through the softmax; whose O^T product was issued
-    uint32_t n_ep = 0;                   // stretches through the softmax, the epilogue
+    uint32_t nq = 0, np = 0;             // chunks whose S / O^T products were issued
+    // (a segment's query passes through two stages, ahead of its chunks, so that
+    // chunk n of segment m is number n + 2 m + 2 of what the stages hold)
+    uint32_t n_ql = 0;                   // segments begun
+    uint32_t n_sm = 0;                   // chunks through the softmax
+    uint32_t n_st = 0;                   // stretches begun by the products
 
     for (;;) {
         __syncthreads();
@@ -251,152 +337,100 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool more = S.work.more != 0;
         if (nrec == 0) break;
 
-        if (warp >= 8) {
-            // -------------------------------------------- products, epilogue
-            // Step j: warp 8 issues S of chunk j, warp 9 O^T of chunk j - 1, and
-            // all four drain O^T where that chunk ends a stretch.
-            constexpr uint32_t id_qk = idesc_fp8<2 * kHG, kChunk, false, false>();
-            constexpr uint32_t id_pv = idesc_fp8<128, kHG, true, true>(), id_wide = idesc_fp8<128, 2 * kHG, true, true>();
-            const uint64_t q_desc = sw128_desc(smem_addr(sQ), 16, 1024);
+        if (warp == 8) {
+            // -------------------------------------------- S = Q . rows^T
+            // A whole warp keeps step and one elected thread issues, here and below.
+            constexpr uint32_t id = idesc_fp8<2 * kHG, kChunk, false, false>();
             const uint64_t r_desc = sw128_desc(smem_addr(sRows), 16, kGroupBytes);
-            const uint64_t a_desc = sw128_desc(smem_addr(sRows) + dt0 * 1024, 1024, kGroupBytes);
-            const uint64_t p_desc = atom_desc(smem_addr(sP), kPiece, 128);
-            const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-            const int hmax = min(kHG, H - h0);
-            auto product = [&](int dd, int ks, uint64_t ad, uint32_t acc) {
-                const uint64_t av = ad + off(dd * 1024 + ks * 4 * kGroupBytes);
-                const uint32_t d = tmem + o_col(dd);
-                const uint64_t pd = p_desc + off(2 * ks * kPiece);
-                if (dd < kWide) {
-#pragma unroll
-                    for (int t = 0; t + 1 < kTerms; t += 2)
-                        umma_fp8(d, av, pd + off(t * kTermBytes), id_wide, t > 0 ? 1u : acc);
-                    if (kTerms & 1) umma_fp8(d, av, pd + off((kTerms - 1) * kTermBytes), id_pv, 1u);
-                } else {
-#pragma unroll
-                    for (int t = 0; t < kTerms; ++t)
-                        umma_fp8(d, av, pd + off(t * kTermBytes), id_pv, t > 0 ? 1u : acc);
-                }
-            };
-            auto pv = [&](auto ntile, uint64_t ad, int st, int ks) {
-#pragma unroll
-                for (int dd = 0; dd < ntile; ++dd) product(dd, ks, ad, 1u);
-                umma_commit(&S.empty[st][ks]);
-                if (ks + 1 == kSteps) umma_commit(&S.pfree);
-            };
-            int i = 0, k = 0, nch = 0, every = 1, z = 0;     // chunk j: k of segment i, z of a stretch
-            auto settle = [&]() {
-                while (i < nrec) {
-                    nch = rec[i].c1 - rec[i].c0;
-                    if (nch > 0) break;
-                    ++i;
-                }
-                k = z = 0;
-                if (i < nrec) every = flush_every<kFlush>(nch);
-            };
-            settle();
-            int bi = -1, bk = 0, bz = 0, bn = 0, be = 1;     // the chunk before it
-            for (;;) {
-                if (warp == 8 && i < nrec) {
-                    if (k == 0) {
-                        mbar_wait(&S.q_full, n_ql & 1u, A.status);
-                        ++n_ql;
-                    }
-                    const int st = nq % kStages, sb = nq & 1u;
-                    mbar_wait(&S.full[st], (nq / kStages) & 1u, A.status);
-                    mbar_wait(&S.sfree[sb], ((nq >> 1) & 1u) ^ 1u, A.status);
-                    ++nq;
+            for (int i = 0; i < nrec; ++i) {
+                const int nch = rec[i].c1 - rec[i].c0;
+                if (nch <= 0) continue;
+                wait_for(&S.q_full, n_ql & 1u, A.status);
+                ++n_ql;
+                for (int k = 0; k < nch; ++k, ++nq) {
+                    const uint32_t slot = nq + 2 * n_ql;
+                    const int st = slot % kSt, sb = nq & 1u;
+                    wait_for(&S.full[st], (slot / kSt) & 1u, A.status);
+                    wait_for(&S.sfree[sb], ((nq >> 1) & 1u) ^ 1u, A.status);
                     __syncwarp();
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint64_t rd = r_desc + off(st * kStageBytes);
+                        uint64_t rd = r_desc + off(st * kStageBytes);
+                        uint32_t qa = tmem + kQCol;
                         const uint32_t d = tmem + kSCol + sb * 64;
+#pragma unroll 1
+                        for (int cg = 0; cg < kHD / 128; ++cg, qa += 32, rd += off(1024)) {
 #pragma unroll
-                        for (int kk = 0; kk < kHD / 32; ++kk) {
-                            const uint32_t cg = kk >> 2, ko = (kk & 3) * 32;
-                            umma_fp8(d, q_desc + off(cg * (2 * kHG * 128) + ko), rd + off(cg * 1024 + ko), id_qk,
-                                     kk > 0 ? 1u : 0u);
+                            for (int x = 0; x < 4; ++x)
+                                umma_fp8_ts(d, qa + 8 * x, rd + off(x * 32), id, x > 0 ? 1u : cg);
                         }
                         umma_commit(&S.sfull[sb]);
                     }
                     __syncwarp();
                 }
-                if (warp == 9 && bi >= 0) {
-                    const int st = np % kStages;
-                    const uint32_t pp = np & 1u;
-                    mbar_wait(&S.pfull[0], pp, A.status);
-                    ++np;
-                    const uint64_t ad = a_desc + off(st * kStageBytes);
-                    if (bz == 0) {
-                        mbar_wait(&S.pfull[1], pp, A.status);
-                        // a stretch's first chunk, tile by tile as the stretch
-                        // before it leaves tensor memory
-                        for (int dd = 0; dd < ndt; ++dd) {
-                            if (n_ep > 0) mbar_wait(&S.ofree[dd], (n_ep - 1) & 1u, A.status);
+            }
+        } else if (warp == 9) {
+            // -------------------------------------------- O^T += rows^T . P^T
+            constexpr uint32_t id = idesc_fp8<128, kHG, true, true>();
+            const uint64_t a_desc = sw128_desc(smem_addr(sRows) + dt0 * 1024, 1024, kGroupBytes);
+            const uint64_t p_desc = atom_desc(smem_addr(sP), kPiece, 128);
+            auto product = [&](int dd, uint64_t ad, uint64_t pd, uint32_t acc) {
+#pragma unroll
+                for (int t = 0; t < kTerms; ++t)
+                    umma_fp8(tmem + kOCol + kHG * dd, ad + off(dd * 1024), pd + off(t * kTermBytes), id, t > 0 ? 1u : acc);
+            };
+            for (int i = 0; i < nrec; ++i) {
+                const int nch = rec[i].c1 - rec[i].c0;
+                if (nch <= 0) continue;
+                ++n_ql;
+                const int every = flush_every<kFlush>(nch);
+                for (int k = 0, z = 0; k < nch; ++k, ++np, z = z + 1 == every ? 0 : z + 1) {
+                    const int st = (np + 2 * n_ql) % kSt, pb = np % kPB;
+#pragma unroll 1
+                    for (int ks = 0; ks < kSteps; ++ks) {
+                        const uint64_t ad = a_desc + off(st * kStageBytes + ks * 4 * kGroupBytes);
+                        const uint64_t pd = p_desc + off((pb * (kChunk / 16) + 2 * ks) * kPiece);
+                        wait_for(&S.pfull[pb][ks], (np / kPB) & 1u, A.status);
+                        if (z == 0 && ks == 0) {
+                            // a stretch's first product: tile by tile, as the stretch before it
+                            // leaves them
+#pragma unroll 1
+                            for (int dd = 0; dd < ndt; ++dd) {
+                                if (n_st > 0) wait_for(&S.ofree[dd], (n_st - 1) & 1u, A.status);
+                                __syncwarp();
+                                tc_fence_after();
+                                if (elect_one()) product(dd, ad, pd, 0u);
+                                __syncwarp();
+                            }
+                            ++n_st;
+                        } else {
                             __syncwarp();
                             tc_fence_after();
                             if (elect_one()) {
+                                uint64_t a = ad;
+                                uint32_t d = tmem + kOCol;
+#pragma unroll 1
+                                for (int dd = 0; dd < ndt; ++dd, a += off(1024), d += kHG) {
 #pragma unroll
-                                for (int ks = 0; ks < kSteps; ++ks) product(dd, ks, ad, ks > 0 ? 1u : 0u);
-                                if (dd + 1 == ndt) {
-                                    for (int ks = 0; ks < kSteps; ++ks) umma_commit(&S.empty[st][ks]);
-                                    umma_commit(&S.pfree);
+                                    for (int t = 0; t < kTerms; ++t) umma_fp8(d, a, pd + off(t * kTermBytes), id, 1u);
                                 }
                             }
                             __syncwarp();
                         }
-                    } else {
-#pragma unroll
-                        for (int ks = 0; ks < kSteps; ++ks) {
-                            if (ks > 0) mbar_wait(&S.pfull[ks], pp, A.status);
-                            __syncwarp();
-                            tc_fence_after();
-                            if (elect_one()) {
-                                if (ndt == 4) pv(std::integral_constant<int, 4>{}, ad, st, ks);
-                                else if (ndt == 2) pv(std::integral_constant<int, 2>{}, ad, st, ks);
-                                else pv(std::integral_constant<int, 1>{}, ad, st, ks);
-                            }
-                            __syncwarp();
+                        if (elect_one()) {
+                            umma_commit(&S.empty[st][ks]);
+                            if (ks + 1 == kSteps) umma_commit(&S.pfree[pb]);
                         }
-                    }
-                }
-                if (bi >= 0) {
-                    ++n_sm;
-                    if (bk + 1 == bn || bz + 1 == be) {
-                        // ---- O^T into the partial, or the output
-                        const int t = rec[bi].t, flags = rec[bi].flags;
-                        const int64_t obase = (static_cast<int64_t>(t) * H + h0) * kHD;
-                        const int64_t pslot = static_cast<int64_t>(rec[bi].slot) * gridDim.y + hg;
-                        const int e = n_ep & 1u;
-                        (void)CSA_CHECK(rec[bi].slot < 2 * W.G && t < W.T, A.status);
-                        const bool add = bk >= be;               // the partial holds earlier stretches
-                        const bool part = (flags & kRecPart) || bk + 1 < bn;
-                        mbar_wait(&S.stretch[e], (n_ep >> 1) & 1u, A.status);
-                        mbar_wait(&S.pfree, (n_sm - 1) & 1u, A.status);   // its last product
-                        ++n_ep;
-                        __syncwarp();
-                        tc_fence_after();
-                        drain_stretch<kBf16, kWide>(A, tmem + lane_off + kOCol, S.fin[e], S.flush[e], S.ofree, sOut, dt0,
-                                                    ndt, hmax, obase, pslot, add, part);
-                        mbar_arrive(&S.stretch_free[e]);
                         __syncwarp();
                     }
-                }
-                if (i >= nrec) break;
-                bi = i, bk = k, bz = z, bn = nch, be = every;
-                z = z + 1 == every ? 0 : z + 1;
-                if (++k == nch) {
-                    ++i;
-                    settle();
                 }
             }
-        } else if (warp < kSlices) {
+        } else if (warp >= 10) {
             // -------------------------------------------- row fetch
-            // The warp walks the list's chunks, 16 rows of each.  Lane l (and
-            // l + 16) looks after row l; three chunks before it is copied its page
-            // number is on its way from the table, two before it its scale.
-            const int li = warp;
-            const int rl = lane & 15;
+            // The warp walks the list's chunks, a row of each a lane: three chunks
+            // before it is copied its page number is on its way from the table, two
+            // before it its scale.
+            const int li = warp - 10;
             int bad = 0;
             struct Cursor {
                 int i, c;
@@ -412,23 +446,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 settle(k);
             };
             struct Entry {
-                int32_t page, at;                      // row of the page; or (page -2) of the rings; < 0: no row
+                int32_t page, at;                      // row of the page; or (page kRing) of the rings; < 0: no row
                 bool box;                              // 8 rows of one page from here on
             };
+            constexpr int32_t kRing = -2;
             auto look_up = [&](const Cursor &k) {
                 Entry e{-1, -1, false};
                 if (k.i >= nrec) return e;
                 const Rec &r = rec[k.i];
-                const int j = k.c * kChunk + 16 * li + rl, w = j - rec_window_slot(r);
+                const int j = k.c * kChunk + 32 * li + lane, w = j - rec_window_slot(r);
                 if (j < r.n) {
                     const int pg = static_cast<int>(A.page_div.div(j));
                     e.at = j - pg * A.L.page_rows;
-                    e.page = A.L.table[static_cast<int64_t>(r.b) * A.L.max_pages + pg];
+                    e.page = max(A.L.table[static_cast<int64_t>(r.b) * A.L.max_pages + pg], -1);
                     e.box = j + 8 <= r.n && e.at + 8 <= A.L.page_rows;
-                    if (e.page == -2) e.page = -1;
                 } else if (w >= 0 && w < r.near) {
                     const int64_t x = r.first + w;
-                    e.page = -2;
+                    e.page = kRing;
                     if (x < r.first_res) bad |= CSA_DEV_MISSING_SWA;
                     else e.at = r.b * A.L.swa_cap + static_cast<int32_t>(A.swa_div.mod64(x));
                 }
@@ -438,12 +472,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint8_t *src;                    // the row's codes, or null
                 float scale;
                 int32_t row;                           // row of the pool, or -1
-                uint32_t box;                          // bit g: group g of 8 rows is one box
+                uint32_t box;                          // bit 8 g: group g of 8 rows is one box
             };
             auto place = [&](const Entry &e) {
                 Place p{nullptr, 0.f, -1, 0};
                 if (e.at >= 0) {
-                    if (e.page == -2) {
+                    if (e.page == kRing) {
                         p.src = static_cast<const uint8_t *>(A.L.swa_kv) + static_cast<int64_t>(e.at) * kHD;
                         p.scale = __ldcg(A.swa_scales + e.at);
                     } else if (e.page < 0 || e.page >= A.num_pages) {
@@ -458,8 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                const uint32_t bx = __ballot_sync(0xffffffffu, e.box);
-                p.box = (bx & 1u) | (bx >> 7 & 2u);
+                p.box = __ballot_sync(0xffffffffu, e.box) & 0x01010101u;
                 return p;
             };
             int pending = -1;                          // stage whose cp.async rows are in flight
@@ -476,84 +509,122 @@ __global__ void __launch_bounds__(kThreads, 1)
             Cursor cur{0, rec[0].c0};
             settle(cur);
             Cursor far = cur;
-            const Entry e0 = look_up(far);
-            advance(far);
-            const Entry e1 = look_up(far);
-            advance(far);
-            Entry ahead = look_up(far);
-            Place now = place(e0), next = place(e1);
+            Place now{}, next{};
+            Entry ahead{-1, -1, false};
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+                now = next;
+                next = place(ahead);
+                ahead = look_up(far);
+                advance(far);
+            }
+            int of = -1;                               // the segment whose query has had its stages
             while (cur.i < nrec) {
-                const uint32_t okm = __ballot_sync(0xffffffffu, now.src != nullptr) & 0xFFFFu;
-                const int32_t y1 = __shfl_sync(0xffffffffu, now.row, 8);
-                const int st = n_fetch % kStages;
-                const uint32_t ph = ((n_fetch / kStages) & 1u) ^ 1u;
-                uint64_t *const empty = &S.empty[st][li / 2];
-                if (pending >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(empty, ph))) land(false);
-                mbar_wait(empty, ph, A.status);
-                __syncwarp();
-                uint8_t *rows = sRows + st * kStageBytes + 2 * li * kGroupBytes;
-                if (lane < 16) {
-                    S.scale[st][16 * li + rl] = now.scale;
-                    S.scale_log[st][16 * li + rl] =
-                        now.src ? __log2f(fminf(fmaxf(fabsf(now.scale), 0x1p-60f), 0x1p60f)) : 0.f;
-                }
-                if (lane == 0) {
-                    S.maskw[st][li] = okm;
-                    if (now.box) {
-                        // (a bad page: a box behind the pool reads as zeros)
-                        mbar_expect_tx(&S.full[st], (now.box == 3u ? 2 : 1) * kGroupBytes);
-                        if (now.box & 1u)
-                            tma_load_3d(rows, &tm_rows, 0, now.row >= 0 ? now.row : A.total_rows, 0, &S.full[st], pol);
-                        if (now.box & 2u)
-                            tma_load_3d(rows + kGroupBytes, &tm_rows, 0, y1 >= 0 ? y1 : A.total_rows, 0, &S.full[st], pol);
+                // (the queue moves up first: the loads that it starts take as long as the
+                // stage's wait)
+                now = next;
+                next = place(ahead);
+                ahead = look_up(far);
+                advance(far);
+                if (cur.i != of) {
+                    // two stages for the query, 32 heads each
+                    of = cur.i;
+                    if (pending >= 0) land(false);
+#pragma unroll 1
+                    for (int x = 0; x < 2; ++x, ++n_fetch) {
+                        // (the whole stage, which the other warp's rows may still be in)
+                        for (int k = 0; k < kSteps; ++k)
+                            wait_for(&S.empty[n_fetch % kSt][k], ((n_fetch / kSt) & 1u) ^ 1u, A.status);
+                        __syncwarp();
+                        if (lane == 0) {
+                            uint64_t *const full = &S.full[n_fetch % kSt];
+                            const int h = h0 + 32 * x, heads = min(32, H - h);
+                            if (li == 0 && heads > 0) {
+                                mbar_expect_tx(full, heads * kHD * 2);
+                                bulk_load(sRows + n_fetch % kSt * kStageBytes,
+                                          A.q + (static_cast<int64_t>(rec[of].t) * H + h) * kHD, heads * kHD * 2, full);
+                            }
+                            mbar_arrive(full);
+                        }
                     }
                 }
-                const bool by_row = now.box != 3u;
+                const uint32_t okm = __ballot_sync(0xffffffffu, now.src != nullptr);
+                const int32_t y = __shfl_sync(0xffffffffu, now.row, (8 * lane) & 31);     // of group `lane`
+                const int st = n_fetch % kSt;
+                const uint32_t ph = ((n_fetch / kSt) & 1u) ^ 1u;
+                uint64_t *const empty = &S.empty[st][li], *const full = &S.full[st];
+                if (pending >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(empty, ph))) land(false);
+                wait_for(empty, ph, A.status);
+                __syncwarp();
+                uint8_t *rows = sRows + st * kStageBytes + 4 * li * kGroupBytes;
+                S.scale[st][32 * li + lane] = now.scale;
+                S.scale_log[st][32 * li + lane] =
+                    now.src ? __log2f(fminf(fmaxf(fabsf(now.scale), 0x1p-60f), 0x1p60f)) : 0.f;
+                if (lane == 0) {
+                    S.maskw[st][li] = okm;
+                    if (now.box) mbar_expect_tx(full, __popc(now.box) * kGroupBytes);
+                }
+                __syncwarp();
+                // (a bad page: a box behind the pool reads as zeros)
+                if (lane < 4 && (now.box >> (8 * lane) & 1u))
+                    tma_load_3d(rows + lane * kGroupBytes, &tm_rows, 0, y >= 0 ? y : A.total_rows, 0, full, pol);
+                const bool by_row = now.box != 0x01010101u;
                 if (by_row) {
 #pragma unroll 1
-                    for (int g = 0; g < 2; ++g) {
-                        if (now.box >> g & 1u) continue;
-#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        if (now.box >> (8 * x) & 1u) continue;
+#pragma unroll 4
                         for (int rr = 0; rr < 8; ++rr) {
                             const uint8_t *p = reinterpret_cast<const uint8_t *>(__shfl_sync(
-                                0xffffffffu, reinterpret_cast<unsigned long long>(now.src), 8 * g + rr));
-                            cp_async16(rows + g * kGroupBytes + (lane >> 3) * 1024 + rr * 128 + (((lane & 7) ^ rr) << 4),
+                                0xffffffffu, reinterpret_cast<unsigned long long>(now.src), 8 * x + rr));
+                            cp_async16(rows + x * kGroupBytes + (lane >> 3) * 1024 + rr * 128 + (((lane & 7) ^ rr) << 4),
                                        p ? p + lane * 16 : A.codes, p != nullptr);
                         }
                     }
                     cp_async_commit();
                 }
-                // the queue moves up
-                now = next;
-                next = place(ahead);
-                advance(far);
-                ahead = look_up(far);
                 advance(cur);
                 if (pending >= 0) land(by_row);
-                if (by_row) {
-                    pending = st;
-                } else {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&S.full[st]);
-                }
+                __syncwarp();
+                if (by_row) pending = st;
+                else if (lane == 0) mbar_arrive(full);
                 ++n_fetch;
             }
             if (pending >= 0) land(false);
             bad = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bad)));
             if (lane == 0 && W.lead) raise_status(A.status, bad);
-        } else if (warp >= 4 && warp < 8) {
+        } else {
             // -------------------------------------------- the query, softmax
             const int q = warp & 3;                  // TMEM lane quarter
-            const int hl = q * 16 + (lane & 15);     // head of this lane (two lanes per head)
-            const bool upper = lane >= 16;           // rows 16..31 and 48..63 of the chunk, others 0..15 and 32..47
+            const int g = warp >> 2;                 // rows 0..31 of a chunk, or 32..63
+            const int hl = q * 16 + (lane & 15);     // head of this lane (four lanes per head, two of each half)
+            const bool upper = lane >= 16;           // the second 16 of those rows
+            const int r0 = 32 * g + (upper ? 16 : 0);
             const bool hv = h0 + hl < H;
             const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+            // O^T of the stretch whose last chunk was the one before n_sm, into the partial
+            // or the output; each half of the warps takes 32 heads
+            auto drain = [&](int of, bool add, bool part) {
+                const Rec &r = rec[of];
+                (void)CSA_CHECK(r.slot < 2 * W.G && r.t < W.T, A.status);
+                wait_for(&S.pfree[(n_sm - 1) % kPB], ((n_sm - 1) / kPB) & 1u, A.status);
+                __syncwarp();
+                named_bar_sync(kBarSm, kSmThreads);      // (the factors are written)
+                tc_fence_after();
+                drain_stretch<kBf16, 0, kStagedHeads>(
+                    A, tmem + lane_off + kOCol, S.fin, S.flush, S.ofree, sP + warp * staged_bytes(kStagedHeads), dt0, ndt,
+                    32 * g, 32 * g + 32, min(kHG, H - h0), (static_cast<int64_t>(r.t) * H + h0) * kHD,
+                    static_cast<int64_t>(r.slot) * gridDim.y + hg, add, part);
+                __syncwarp();
+            };
+            int left = -1;                           // the segment whose O^T is still to be drained
+            bool left_add = false;
             for (int i = 0; i < nrec; ++i) {
                 const int nch = rec[i].c1 - rec[i].c0;
                 if (nch <= 0) {
                     if (rec[i].flags & kRecZero) {
                         const int64_t obase = (static_cast<int64_t>(rec[i].t) * H + h0) * kHD;
-                        for (int x = tid - 128; x < min(kHG, H - h0) * 128 * ndt; x += kSmThreads) {
+                        for (int x = tid; x < min(kHG, H - h0) * 128 * ndt; x += kSmThreads) {
                             const int64_t at = obase + (x / (128 * ndt)) * kHD + dt0 * 128 + x % (128 * ndt);
                             if (kBf16) static_cast<__nv_bfloat16 *>(A.out)[at] = __float2bfloat16(0.f);
                             else static_cast<float *>(A.out)[at] = 0.f;
@@ -561,167 +632,230 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     continue;
                 }
-                // (the segment before this one is done with Q: its last logits have
-                // come)  Four heads' loads at a time.
-                float c = 0.f;
-                const uint4 *const src = reinterpret_cast<const uint4 *>(
-                    A.q + (static_cast<int64_t>(rec[i].t) * H + h0 + q * 16) * kHD) + 2 * lane;
-#pragma unroll 1
-                for (int g = 0; g < 16; g += 4) {
-                    uint4 raw[4][2];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            raw[x][y] = h0 + q * 16 + g + x < H ? __ldcg(src + (g + x) * (kHD / 8) + y) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float f = split_query(raw[x], sQ, 32 * q + g + x, lane);
-                        if ((lane & 15) == g + x) c = f * A.scale_log2;
+                // (the segment before this one is done with Q when its last logits have
+                // come)
+                if (n_sm > 0) wait_for(&S.sfull[(n_sm - 1) & 1u], ((n_sm - 1) >> 1) & 1u, A.status);
+                __syncwarp();
+                tc_fence_after();
+                // Eight heads a warp, each split in its place (a lane has 16 columns; a
+                // head's 512 codes hi, then lo, in pieces of 16 whose order depends on the
+                // head); then half a row of codes a lane into tensor memory.
+                {
+                    const uint32_t slot = n_sm + 2 * n_ql;
+                    const int st0 = slot % kSt, st1 = (slot + 1) % kSt;
+                    wait_for(&S.full[st0], (slot / kSt) & 1u, A.status);
+                    wait_for(&S.full[st1], ((slot + 1) / kSt) & 1u, A.status);
+                    __syncwarp();
+                    uint8_t *const qs = sRows + (q < 2 ? st0 : st1) * kStageBytes + (q & 1) * (16 * 1024);
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 2
+                    for (int x = 8 * g; x < 8 * g + 8; ++x) {
+                        uint8_t *const at = qs + x * 1024;
+                        const bool real = h0 + q * 16 + x < H;
+                        const uint4 v0 = real ? reinterpret_cast<const uint4 *>(at)[2 * lane] : zero;
+                        const uint4 v1 = real ? reinterpret_cast<const uint4 *>(at)[2 * lane + 1] : zero;
+                        uint4 hi, lo;
+                        const float f = split_query(v0, v1, hi, lo);
+                        __syncwarp();
+                        reinterpret_cast<uint4 *>(at)[lane ^ (x & 7)] = hi;
+                        reinterpret_cast<uint4 *>(at + 512)[lane ^ (x & 7)] = lo;
+                        if (lane == 0) S.q_scale[q * 16 + x] = f * A.scale_log2;
                     }
+                    __syncwarp();
+                    named_bar_sync(kBarQ + q, 64);
+                    const uint4 *const get = reinterpret_cast<const uint4 *>(qs + (lane & 15) * 1024 + (lane >> 4) * 512) + 16 * g;
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t o[32];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const uint4 u = get[(8 * half + x) ^ (lane & 7)];
+                            o[4 * x] = u.x;
+                            o[4 * x + 1] = u.y;
+                            o[4 * x + 2] = u.z;
+                            o[4 * x + 3] = u.w;
+                        }
+                        tmem_st32(tmem + lane_off + kQCol + 64 * g + 32 * half, o);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    fence_proxy_async_smem();
+                    mbar_arrive(&S.q_full);
+                    wait_for(&S.q_full, n_ql & 1u, A.status);       // (all are done: the stages go back)
+                    if (tid == 0)
+                        for (int k = 0; k < kSteps; ++k) {
+                            mbar_arrive(&S.empty[st0][k]);
+                            mbar_arrive(&S.empty[st1][k]);
+                        }
+                    __syncwarp();
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(&S.q_full);
+                ++n_ql;
+                // the segment before this one, under this one's first logits
+                if (left >= 0) drain(left, left_add, rec[left].flags & kRecPart);
+                const float c = S.q_scale[hl];
 
                 const bool cut = rec[i].flags & kRecPart;
                 float m_ref = -INFINITY, l = 0.f, m_flush = -INFINITY;
                 const int every = flush_every<kFlush>(nch);
+                const float2 c2 = make_float2(c, c);
                 for (int k = 0, z = 0; k < nch; ++k, ++n_sm, z = z + 1 == every ? 0 : z + 1) {
-                    const int st = n_sm % kStages, sb = n_sm & 1u;
+                    const uint32_t slot = n_sm + 2 * n_ql;
+                    const int st = slot % kSt, sb = n_sm & 1u;
+                    // the rows' masks and scales, before their logits come
+                    wait_for(&S.full[st], (slot / kSt) & 1u, A.status);
+                    const uint32_t mw = S.maskw[st][g] >> (r0 & 16) & 0xFFFFu;
+                    float2 s[8], x[8], y[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        *reinterpret_cast<float4 *>(s + 2 * j) = *reinterpret_cast<const float4 *>(S.scale[st] + r0 + 4 * j);
+                        *reinterpret_cast<float4 *>(y + 2 * j) = *reinterpret_cast<const float4 *>(S.scale_log[st] + r0 + 4 * j);
+                    }
                     // (a wait's lanes may leave it at different polls; what is
                     // .aligned below, tensor memory and barriers, wants the warp whole)
-                    mbar_wait(&S.sfull[sb], (n_sm >> 1) & 1u, A.status);
+                    wait_for(&S.sfull[sb], (n_sm >> 1) & 1u, A.status);
                     __syncwarp();
                     tc_fence_after();
-                    float x[32];
                     {
-                        uint32_t hi[2][16], lo[2][16];
-                        const uint32_t at = tmem + lane_off + kSCol + sb * 64;
-                        tmem_ld16x2_next_raw(at, hi[0]);
-                        tmem_ld16x2_next_raw(at + (16u << 16), lo[0]);
-                        tmem_ld16x2_next_raw(at + 32, hi[1]);
-                        tmem_ld16x2_next_raw(at + (16u << 16) + 32, lo[1]);
+                        uint32_t hi[16], lo[16];
+                        const uint32_t at = tmem + lane_off + kSCol + sb * 64 + 32 * g;
+                        tmem_ld16x2_next_raw(at, hi);
+                        tmem_ld16x2_next_raw(at + (16u << 16), lo);
                         tmem_wait_ld();
                         tc_fence_before();
                         mbar_arrive(&S.sfree[sb]);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            x[j] = __uint_as_float(hi[j >> 4][j & 15]) + __uint_as_float(lo[j >> 4][j & 15]);
+                        for (int j = 0; j < 8; ++j)
+                            x[j] = mul2(add2(make_float2(__uint_as_float(hi[2 * j]), __uint_as_float(hi[2 * j + 1])),
+                                             make_float2(__uint_as_float(lo[2 * j]), __uint_as_float(lo[2 * j + 1]))),
+                                        mul2(s[j], c2));
                     }
-                    mbar_wait(&S.full[st], (n_sm / kStages) & 1u, A.status);   // orders masks and scales
-                    const uint32_t m0 = S.maskw[st][upper ? 1 : 0], m1 = S.maskw[st][upper ? 3 : 2];
-                    const bool all = __all_sync(0xffffffffu, (m0 & m1) == 0xFFFFu);
-                    // logits; the maximum is that of the logits plus their scales' logarithms
-                    const float *const sc = S.scale[st] + (upper ? 16 : 0), *const sl = S.scale_log[st] + (upper ? 16 : 0);
-                    float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if (__any_sync(0xffffffffu, mw != 0xFFFFu)) {
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const int at = (j & 15) + (j >> 4) * 32;
-                        const float4 s4 = *reinterpret_cast<const float4 *>(sc + at);
-                        const float4 l4 = *reinterpret_cast<const float4 *>(sl + at);
-                        const float s[4] = {s4.x, s4.y, s4.z, s4.w}, lg[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[j + e] *= s[e] * c;
-                        if (!all) {
-                            const uint32_t m = j < 16 ? m0 : m1;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (!(m >> ((j & 15) + e) & 1u)) x[j + e] = -INFINITY;
+                        for (int j = 0; j < 8; ++j) {
+                            if (!(mw >> (2 * j) & 1u)) x[j].x = -INFINITY;
+                            if (!(mw >> (2 * j + 1) & 1u)) x[j].y = -INFINITY;
                         }
+                    }
+                    // the maximum is that of the logits plus their scales' logarithms
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) mq[e] = fmaxf(mq[e], x[j + e] + lg[e]);
-                    }
-                    float mc = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+                    for (int j = 0; j < 8; ++j) y[j] = add2(x[j], y[j]);
+                    float mc = fmaxf(y[0].x, y[0].y);
+#pragma unroll
+                    for (int j = 1; j < 8; ++j) mc = fmaxf(mc, fmaxf(y[j].x, y[j].y));
                     mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, 16));
-                    // a head whose maximum rises by more than kRescaleAbove rescales
-                    // what has been accumulated
-                    const bool need = hv && m_ref != -INFINITY && mc > m_ref + kRescaleAbove;
-                    const uint32_t wneed = __ballot_sync(0xffffffffu, need);
-                    if (lane == 0) S.flag[sb][q] = wneed;
-                    float alpha = 1.f;
-                    if (need) {
-                        alpha = exp2f(m_ref - mc);
-                        m_ref = mc;
-                        l *= alpha;
-                    } else if (m_ref == -INFINITY) {
-                        m_ref = mc;
-                    }
-                    __syncwarp();
-                    named_bar_sync(kBarSm, kSmThreads);
-                    const bool any = (S.flag[sb][0] | S.flag[sb][1] | S.flag[sb][2] | S.flag[sb][3]) != 0;
-                    if (any && z != 0) {
-                        if (!upper) S.alpha[hl] = alpha;
-                        mbar_wait(&S.pfree, (n_sm - 1) & 1u, A.status);   // the product before this one
+                    // a head whose maximum rises by more than kRescaleAbove (the first one
+                    // does) rescales what has been accumulated
+                    if (any_of(hv && mc > m_ref + kRescaleAbove)) {
+                        if (!upper) S.rise[g][hl] = mc;
                         __syncwarp();
                         named_bar_sync(kBarSm, kSmThreads);
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int y = 0; y < static_cast<int>(o_col(ndt) - kOCol); y += 16) {
-                            uint32_t o[16];
-                            const uint32_t ta2 = tmem + lane_off + kOCol + y;
-                            tmem_ld16_raw(ta2, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * S.alpha[y % kHG + e]);
-                            tmem_st16(ta2, o);
+                        mc = fmaxf(S.rise[0][hl], S.rise[1][hl]);
+                        float alpha = 1.f;
+                        if (hv && mc > m_ref + kRescaleAbove) {
+                            if (m_ref != -INFINITY) alpha = exp2f(m_ref - mc);
+                            m_ref = mc;
+                            l *= alpha;
                         }
-                        tmem_wait_st();
-                        tc_fence_before();
-                        named_bar_sync(kBarSm, kSmThreads);
+                        if (z != 0) {
+                            const uint32_t mine = __ballot_sync(0xffffffffu, alpha != 1.f) & 0xFFFFu;
+                            if (g == 0 && !upper) S.alpha[hl] = alpha;
+                            if (g == 0 && lane == 0) S.risen[q] = mine;
+                            // the product before this one (and the one before that: a wait
+                            // tells a phase from the next, but not from the one after)
+                            wait_for(&S.pfree[n_sm % kPB], ((n_sm / kPB) & 1u) ^ 1u, A.status);
+                            wait_for(&S.pfree[(n_sm - 1) % kPB], ((n_sm - 1) / kPB) & 1u, A.status);
+                            __syncwarp();
+                            named_bar_sync(kBarSm, kSmThreads);
+                            tc_fence_after();
+                            // head by head (seldom more than a few), a tile or two a half of
+                            // the warps
+                            uint64_t heads = S.risen[0] | static_cast<uint64_t>(S.risen[1]) << 16 |
+                                             static_cast<uint64_t>(S.risen[2]) << 32 | static_cast<uint64_t>(S.risen[3]) << 48;
+                            while (heads) {
+                                const int h = __ffsll(heads) - 1;
+                                heads &= heads - 1;
+                                const uint32_t o = tmem + lane_off + kOCol + h;
+                                const float f = S.alpha[h];
+                                if (ndt == 4) {
+                                    const float x0 = tmem_ld1(o + 2 * kHG * g), x1 = tmem_ld1(o + 2 * kHG * g + kHG);
+                                    tmem_wait_ld();
+                                    tmem_st1(o + 2 * kHG * g, x0 * f);
+                                    tmem_st1(o + 2 * kHG * g + kHG, x1 * f);
+                                } else if (g < ndt) {
+                                    const float x0 = tmem_ld1(o + kHG * g);
+                                    tmem_wait_ld();
+                                    tmem_st1(o + kHG * g, x0 * f);
+                                }
+                            }
+                            tmem_wait_st();
+                            tc_fence_before();
+                            named_bar_sync(kBarSm, kSmThreads);
+                        }
                     }
                     const float mr = m_ref == -INFINITY ? 0.f : m_ref - kTop;
-                    float sq[2] = {0.f, 0.f};
+                    const float2 m2 = make_float2(-mr, -mr);
+                    float2 sum = make_float2(0.f, 0.f);
+                    uint32_t w[4][kTerms];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t w[4][kTerms];
+                    for (int u = 0; u < 4; ++u) {
+                        float p[4];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const float4 s4 = *reinterpret_cast<const float4 *>(sc + half * 32 + 4 * u);
-                            const float s[4] = {s4.x, s4.y, s4.z, s4.w};
-                            float p[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                p[e] = fast_exp2(x[half * 16 + 4 * u + e] - mr);
-                                sq[e & 1] += p[e];
-                                p[e] *= s[e];
-                            }
-                            split_weights<kTerms>(p, w[u]);
+                        for (int e = 0; e < 2; ++e) {
+                            float2 v = add2(x[2 * u + e], m2);
+                            v = make_float2(fast_exp2(v.x), fast_exp2(v.y));
+                            sum = add2(sum, v);
+                            v = mul2(v, s[2 * u + e]);
+                            p[2 * e] = v.x;
+                            p[2 * e + 1] = v.y;
                         }
-                        if (half == 0 && n_sm > 0) mbar_wait(&S.pfree, (n_sm - 1) & 1u, A.status);
-                        uint8_t *const at = sP + (2 * half + (upper ? 1 : 0)) * kPiece + hl * 16;
-#pragma unroll
-                        for (int t = 0; t < kTerms; ++t)
-                            *reinterpret_cast<uint4 *>(at + t * kTermBytes) = make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]);
-                        fence_proxy_async_smem();
-                        mbar_arrive(&S.pfull[half]);
+                        split_weights<kTerms>(p, w[u]);
                     }
-                    const float sum = sq[0] + sq[1];
-                    l += sum + __shfl_xor_sync(0xffffffffu, sum, 16);
+                    l += sum.x + sum.y;
+                    const int pb = n_sm % kPB;
+                    wait_for(&S.pfree[pb], ((n_sm / kPB) & 1u) ^ 1u, A.status);
+                    uint8_t *const at = sP + (pb * (kChunk / 16) + 2 * g + (upper ? 1 : 0)) * kPiece + hl * 16;
+#pragma unroll
+                    for (int t = 0; t < kTerms; ++t)
+                        *reinterpret_cast<uint4 *>(at + t * kTermBytes) = make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]);
+                    fence_proxy_async_smem();
+                    mbar_arrive(&S.pfull[pb][g]);
 
                     const bool last = k + 1 == nch;
                     if (!last && z + 1 != every) continue;
+                    if (last) {                          // the weights' sum
+                        __syncwarp();
+                        l += __shfl_xor_sync(0xffffffffu, l, 16);
+                        if (g == 1 && !upper) S.part_l[hl] = l;
+                        named_bar_sync(kBarSm, kSmThreads);
+                        if (g == 0) l += S.part_l[hl];
+                    }
                     // the stretch's factors for the epilogue
-                    const int e = n_ep & 1u;
-                    mbar_wait(&S.stretch_free[e], ((n_ep >> 1) & 1u) ^ 1u, A.status);
-                    ++n_ep;
-                    if (!upper) {
-                        S.flush[e][hl] = m_flush == -INFINITY ? 1.f : exp2f(m_flush - m_ref);
+                    if (g == 0 && !upper) {
+                        S.flush[hl] = m_flush == -INFINITY ? 1.f : exp2f(m_flush - m_ref);
                         float f = 1.f;
                         if (last && !cut) {
                             float zs = l;
                             if (A.sinks && hv) zs += exp2f(A.sinks[h0 + hl] * kLog2e - mr);
                             f = m_ref == -INFINITY && l == 0.f ? 0.f : 1.f / zs;     // (a sink of NaN: NaN)
                         }
-                        S.fin[e][hl] = f;
+                        S.fin[hl] = f;
                         if (last && cut && dt0 == 0)
                             A.part_ml[(static_cast<int64_t>(rec[i].slot) * gridDim.y + hg) * kHG + hl] =
                                 make_float2(m_ref == -INFINITY ? m_ref : mr, l);
                     }
                     m_flush = m_ref;
-                    mbar_arrive(&S.stretch[e]);
+                    __syncwarp();
+                    if (last) {
+                        left = i;
+                        left_add = k >= every;           // the partial holds earlier stretches
+                    } else {
+                        ++n_sm;
+                        drain(i, k >= every, true);
+                        --n_sm;
+                    }
                 }
             }
+            if (left >= 0) drain(left, left_add, rec[left].flags & kRecPart);
         }
         if (!more) break;
         __syncthreads();                 // the list is done with
@@ -740,13 +874,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int kTerms>
-size_t smem_bytes() {
-    return 1024 + kQBytes + kStages * kStageBytes + kChunk / 16 * kPieceBytes<kTerms> + kStagedBytes<kTerms> + sizeof(Smem);
+constexpr size_t smem_bytes() {
+    return 1024 + kStages<kTerms> * kStageBytes + kPBufs * (kChunk / 16) * kPieceBytes<kTerms> + sizeof(Smem);
 }
-
-constexpr size_t kSmemMost = 227 * 1024;
-static_assert(1024 + kQBytes + kStages * kStageBytes + kChunk / 16 * kPieceBytes<6> + kStagedBytes<6> + sizeof(Smem) <= kSmemMost);
-static_assert(1024 + kQBytes + kStages * kStageBytes + kChunk / 16 * kPieceBytes<3> + kStagedBytes<3> + sizeof(Smem) <= kSmemMost);
+static_assert(smem_bytes<3>() <= 227 * 1024 && smem_bytes<6>() <= 227 * 1024);
 
 }  // namespace
 
