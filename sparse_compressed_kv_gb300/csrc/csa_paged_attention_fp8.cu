@@ -120,6 +120,18 @@ __device__ __forceinline__ bool any_of(bool mine) {
     return any != 0;
 }
 
+// 2 x 16 lanes of tensor memory: threads 0..15 read lanes 0..15 of the address at
+// columns c .. c + 15, threads 16..31 the same lanes at columns c + 16 .. c + 31.
+__device__ __forceinline__ void tmem_ld16x2_next_raw(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16], 16;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
 // Two f32 operations an instruction.
 union Pair {
     float2 v;
@@ -134,18 +146,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     Pair x{a}, y{b}, r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(x.u), "l"(y.u));
     return r.v;
-}
-
-// 2 x 16 lanes of tensor memory: threads 0..15 read lanes 0..15 of the address at
-// columns c .. c + 15, threads 16..31 the same lanes at columns c + 16 .. c + 31.
-__device__ __forceinline__ void tmem_ld16x2_next_raw(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16], 16;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
 }
 
 __device__ __forceinline__ uint32_t f16x2(float a, float b) {
@@ -200,45 +200,32 @@ __device__ __forceinline__ void split_weights(const float (&p)[4], uint32_t (&t)
     }
 }
 
-// 16 columns of a head of the query as codes hi and lo, by integer operations on
-// the bits of two numbers at a time: the 64 heads' 32,768 numbers are bound by the
-// instructions issued, some 8 a number with conversions and 6 so.  Returns the factor
-// that takes sums of codes back to the query's units (NaN where the query is not finite).
+// 16 columns of a head of the query as codes hi and lo.  Returns the factor that takes
+// sums of codes back to the query's units (NaN where the query is not finite).  (Two
+// numbers at a time by conversions; by integer operations on their bits, 12 instead of 10
+// instructions, the 64 heads take 5,000 cycles instead of 4,000.)
 __device__ __forceinline__ float split_query(const uint4 &v0, const uint4 &v1, uint4 &hi, uint4 &lo) {
     const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-    uint32_t mag[8], top = 0;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+    // 1.m 2^(e - 127) to 2^7 (f16 holds what e4m3's terms need: down to 2^-14, and
+    // 8 bits); by halves, since the factor may be out of range
+    const int k = 134 - static_cast<int>(top >> 7), k1 = k / 2;
+    const float f1 = exponent_f32(k1), f2 = exponent_f32(k - k1);
+    const float2 s1 = make_float2(f1, f1), s2 = make_float2(f2, f2);
+    uint32_t h[8], l[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        mag[i] = w[i] & 0x7FFF7FFFu;
-        top = __vmaxu2(top, mag[i]);
+        const float2 x = mul2(mul2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), s1), s2);
+        const uint32_t y = f16x2(x.x, x.y);
+        h[i] = f16x2_e4m3x2(y);
+        l[i] = f16x2_e4m3x2(f16x2_sub(y, e4m3x2_f16x2(h[i])));
     }
-    top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
-    // The largest exponent becomes 7 (f16's 22): bf16's exponent field moves down by
-    // `drop`, which leaves f16's bits without the last three; what would fall below
-    // f16's range becomes 0.
-    const uint32_t drop = max(top >> 7, 22u) - 22u;
-    const uint32_t d2 = drop << 7 | drop << 23;
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t hc[2], lc[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t m = __vmaxu2(mag[2 * i + j], d2) - d2;
-            // hi: three mantissa bits, nothing below 2^-6 (e4m3's normal numbers, whose
-            // exponent field is f16's less 8); its code in each half's upper byte
-            const uint32_t t = __vmaxu2(m, 0x04800480u) & 0x0FF00FF0u;
-            hc[j] = t * 16u - 0x40004000u;
-            lc[j] = f16x2_e4m3x2(f16x2_sub(m << 3, t << 3) ^ (w[2 * i + j] & 0x80008000u));
-        }
-        h[i] = __byte_perm(hc[0], hc[1], 0x7531) | (__byte_perm(w[2 * i], w[2 * i + 1], 0x7531) & 0x80808080u);
-        l[i] = lc[0] | lc[1] << 16;
-    }
-    hi = make_uint4(h[0], h[1], h[2], h[3]);
-    lo = make_uint4(l[0], l[1], l[2], l[3]);
-    // 2^(drop + 22 - 134), by halves: the exponent may be out of range for one factor
-    const int k = static_cast<int>(drop) - 112;
-    return top >= 0x7F80u ? NAN : exponent_f32(k / 2) * exponent_f32(k - k / 2);
+    hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    lo = make_uint4(l[0] | l[1] << 16, l[2] | l[3] << 16, l[4] | l[5] << 16, l[6] | l[7] << 16);
+    return top >= 0x7F80u ? NAN : exponent_f32(-k1) * exponent_f32(k1 - k);
 }
 
 // A contiguous copy into shared memory, a multiple of 16 bytes.
@@ -509,6 +496,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             Cursor cur{0, rec[0].c0};
             settle(cur);
             Cursor far = cur;
+            // the query of a segment: two stages ahead of its rows, 32 heads each
+            int of = -1;                               // the segment whose query has been fetched
+            auto query = [&](int i) {
+                of = i;
+                if (pending >= 0) land(false);
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x, ++n_fetch) {
+                    // (the whole stage, which the other warp's rows may still be in)
+                    for (int k = 0; k < kSteps; ++k)
+                        wait_for(&S.empty[n_fetch % kSt][k], ((n_fetch / kSt) & 1u) ^ 1u, A.status);
+                    __syncwarp();
+                    if (lane == 0) {
+                        uint64_t *const full = &S.full[n_fetch % kSt];
+                        const int h = h0 + 32 * x, heads = min(32, H - h);
+                        if (li == 0 && heads > 0) {
+                            mbar_expect_tx(full, heads * kHD * 2);
+                            bulk_load(sRows + n_fetch % kSt * kStageBytes,
+                                      A.q + (static_cast<int64_t>(rec[i].t) * H + h) * kHD, heads * kHD * 2, full);
+                        }
+                        mbar_arrive(full);
+                    }
+                }
+            };
+            if (cur.i < nrec) query(cur.i);
             Place now{}, next{};
             Entry ahead{-1, -1, false};
 #pragma unroll 1
@@ -518,7 +529,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ahead = look_up(far);
                 advance(far);
             }
-            int of = -1;                               // the segment whose query has had its stages
             while (cur.i < nrec) {
                 // (the queue moves up first: the loads that it starts take as long as the
                 // stage's wait)
@@ -526,28 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 next = place(ahead);
                 ahead = look_up(far);
                 advance(far);
-                if (cur.i != of) {
-                    // two stages for the query, 32 heads each
-                    of = cur.i;
-                    if (pending >= 0) land(false);
-#pragma unroll 1
-                    for (int x = 0; x < 2; ++x, ++n_fetch) {
-                        // (the whole stage, which the other warp's rows may still be in)
-                        for (int k = 0; k < kSteps; ++k)
-                            wait_for(&S.empty[n_fetch % kSt][k], ((n_fetch / kSt) & 1u) ^ 1u, A.status);
-                        __syncwarp();
-                        if (lane == 0) {
-                            uint64_t *const full = &S.full[n_fetch % kSt];
-                            const int h = h0 + 32 * x, heads = min(32, H - h);
-                            if (li == 0 && heads > 0) {
-                                mbar_expect_tx(full, heads * kHD * 2);
-                                bulk_load(sRows + n_fetch % kSt * kStageBytes,
-                                          A.q + (static_cast<int64_t>(rec[of].t) * H + h) * kHD, heads * kHD * 2, full);
-                            }
-                            mbar_arrive(full);
-                        }
-                    }
-                }
+                if (cur.i != of) query(cur.i);
                 const uint32_t okm = __ballot_sync(0xffffffffu, now.src != nullptr);
                 const int32_t y = __shfl_sync(0xffffffffu, now.row, (8 * lane) & 31);     // of group `lane`
                 const int st = n_fetch % kSt;
