@@ -64,7 +64,7 @@ constexpr int kOCol = 128;                      // O^T: 4 tiles x 64 heads
 constexpr int kQCol = 384;                      // the query: 128 rows x 512 codes
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxRec = 32;                     // segments a CTA lists at a time
-constexpr int kSegCost = 3;                     // a segment's epilogue, in chunks
+constexpr int kSegCost = 2;                     // a segment's epilogue, in chunks
 constexpr int kCutAbove = 4;                    // chunks a token may exceed the mean before tokens are cut
 constexpr int kFlushF32 = 27, kFlushBf16 = 341; // chunks between roundings of the accumulator, at most
 constexpr float kTop = 7.f;                     // log2 of the weight that the maximum is brought to
@@ -212,20 +212,20 @@ __device__ __forceinline__ float split_query(const uint4 &v0, const uint4 &v1, u
     top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
     // 1.m 2^(e - 127) to 2^7 (f16 holds what e4m3's terms need: down to 2^-14, and
     // 8 bits); by halves, since the factor may be out of range
-    const int k = 134 - static_cast<int>(top >> 7), k1 = k / 2;
-    const float f1 = exponent_f32(k1), f2 = exponent_f32(k - k1);
-    const float2 s1 = make_float2(f1, f1), s2 = make_float2(f2, f2);
+    const int k = min(134 - static_cast<int>(top >> 7), 126);
+    const float f = exponent_f32(k);
+    const float2 s1 = make_float2(f, f);
     uint32_t h[8], l[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float2 x = mul2(mul2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), s1), s2);
+        const float2 x = mul2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), s1);
         const uint32_t y = f16x2(x.x, x.y);
         h[i] = f16x2_e4m3x2(y);
         l[i] = f16x2_e4m3x2(f16x2_sub(y, e4m3x2_f16x2(h[i])));
     }
     hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
     lo = make_uint4(l[0] | l[1] << 16, l[2] | l[3] << 16, l[4] | l[5] << 16, l[6] | l[7] << 16);
-    return top >= 0x7F80u ? NAN : exponent_f32(-k1) * exponent_f32(k1 - k);
+    return top >= 0x7F80u ? NAN : exponent_f32(-k);
 }
 
 // A contiguous copy into shared memory, a multiple of 16 bytes.
@@ -234,6 +234,11 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                      smem_addr(dst)),
                  "l"(src), "r"(bytes), "r"(smem_addr(bar))
                  : "memory");
+}
+
+// The barrier's phase waits for this thread's cp.async copies too.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // One 32-bit column of tensor memory, a lane a thread.
@@ -339,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int st = slot % kSt, sb = nq & 1u;
                     wait_for(&S.full[st], (slot / kSt) & 1u, A.status);
                     wait_for(&S.sfree[sb], ((nq >> 1) & 1u) ^ 1u, A.status);
+                    fence_proxy_async_smem();            // (rows that came one by one)
                     __syncwarp();
                     tc_fence_after();
                     if (elect_one()) {
@@ -456,40 +462,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return e;
             };
             struct Place {
-                const uint8_t *src;                    // the row's codes, or null
+                int32_t row;                           // of the pool or of the rings, or -1
                 float scale;
-                int32_t row;                           // row of the pool, or -1
                 uint32_t box;                          // bit 8 g: group g of 8 rows is one box
+                uint32_t ring;                         // ... of the rings (no group holds rows of both)
             };
             auto place = [&](const Entry &e) {
-                Place p{nullptr, 0.f, -1, 0};
+                Place p{-1, 0.f, 0, 0};
                 if (e.at >= 0) {
                     if (e.page == kRing) {
-                        p.src = static_cast<const uint8_t *>(A.L.swa_kv) + static_cast<int64_t>(e.at) * kHD;
+                        p.row = e.at;
                         p.scale = __ldcg(A.swa_scales + e.at);
                     } else if (e.page < 0 || e.page >= A.num_pages) {
                         bad |= CSA_DEV_BAD_INDEX;
                     } else {
                         p.row = static_cast<int32_t>(e.page * A.page_stride) + e.at;
-                        if (!CSA_CHECK(p.row < A.total_rows, A.status)) {
-                            p.row = -1;
-                        } else {
-                            p.src = A.codes + static_cast<int64_t>(p.row) * kHD;
-                            p.scale = __ldcg(A.scales + e.page * A.scale_stride + e.at);
-                        }
+                        if (!CSA_CHECK(p.row < A.total_rows, A.status)) p.row = -1;
+                        else p.scale = __ldcg(A.scales + e.page * A.scale_stride + e.at);
                     }
                 }
                 p.box = __ballot_sync(0xffffffffu, e.box) & 0x01010101u;
+                p.ring = __ballot_sync(0xffffffffu, e.page == kRing);
                 return p;
-            };
-            int pending = -1;                          // stage whose cp.async rows are in flight
-            auto land = [&](bool newer) {              // ... have landed: hand the stage over
-                if (newer) cp_async_wait<1>();
-                else cp_async_wait<0>();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.full[pending]);
-                pending = -1;
             };
             // rows are read once, or once by each of two groups of heads
             const uint64_t pol = gridDim.y > 1 ? policy_evict_normal() : policy_evict_first();
@@ -500,7 +494,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             int of = -1;                               // the segment whose query has been fetched
             auto query = [&](int i) {
                 of = i;
-                if (pending >= 0) land(false);
 #pragma unroll 1
                 for (int x = 0; x < 2; ++x, ++n_fetch) {
                     // (the whole stage, which the other warp's rows may still be in)
@@ -537,18 +530,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ahead = look_up(far);
                 advance(far);
                 if (cur.i != of) query(cur.i);
-                const uint32_t okm = __ballot_sync(0xffffffffu, now.src != nullptr);
+                const uint32_t okm = __ballot_sync(0xffffffffu, now.row >= 0);
                 const int32_t y = __shfl_sync(0xffffffffu, now.row, (8 * lane) & 31);     // of group `lane`
                 const int st = n_fetch % kSt;
                 const uint32_t ph = ((n_fetch / kSt) & 1u) ^ 1u;
                 uint64_t *const empty = &S.empty[st][li], *const full = &S.full[st];
-                if (pending >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(empty, ph))) land(false);
                 wait_for(empty, ph, A.status);
                 __syncwarp();
                 uint8_t *rows = sRows + st * kStageBytes + 4 * li * kGroupBytes;
                 S.scale[st][32 * li + lane] = now.scale;
                 S.scale_log[st][32 * li + lane] =
-                    now.src ? __log2f(fminf(fmaxf(fabsf(now.scale), 0x1p-60f), 0x1p60f)) : 0.f;
+                    now.row >= 0 ? __log2f(fminf(fmaxf(fabsf(now.scale), 0x1p-60f), 0x1p60f)) : 0.f;
                 if (lane == 0) {
                     S.maskw[st][li] = okm;
                     if (now.box) mbar_expect_tx(full, __popc(now.box) * kGroupBytes);
@@ -557,29 +549,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (a bad page: a box behind the pool reads as zeros)
                 if (lane < 4 && (now.box >> (8 * lane) & 1u))
                     tma_load_3d(rows + lane * kGroupBytes, &tm_rows, 0, y >= 0 ? y : A.total_rows, 0, full, pol);
-                const bool by_row = now.box != 0x01010101u;
-                if (by_row) {
+                if (now.box != 0x01010101u) {
 #pragma unroll 1
                     for (int x = 0; x < 4; ++x) {
                         if (now.box >> (8 * x) & 1u) continue;
-#pragma unroll 4
+                        const uint8_t *const from =
+                            (now.ring >> (8 * x) & 1u ? static_cast<const uint8_t *>(A.L.swa_kv) : A.codes) + lane * 16;
+                        uint8_t *const to = rows + x * kGroupBytes + (lane >> 3) * 1024;
+#pragma unroll
                         for (int rr = 0; rr < 8; ++rr) {
-                            const uint8_t *p = reinterpret_cast<const uint8_t *>(__shfl_sync(
-                                0xffffffffu, reinterpret_cast<unsigned long long>(now.src), 8 * x + rr));
-                            cp_async16(rows + x * kGroupBytes + (lane >> 3) * 1024 + rr * 128 + (((lane & 7) ^ rr) << 4),
-                                       p ? p + lane * 16 : A.codes, p != nullptr);
+                            const int32_t row = __shfl_sync(0xffffffffu, now.row, 8 * x + rr);
+                            cp_async16(to + rr * 128 + (((lane & 7) ^ rr) << 4), from + static_cast<int64_t>(max(row, 0)) * kHD,
+                                       row >= 0);
                         }
                     }
-                    cp_async_commit();
+                    // (the stage is full when they have landed; nobody waits for them here)
+                    cp_async_arrive(full);
                 }
                 advance(cur);
-                if (pending >= 0) land(by_row);
                 __syncwarp();
-                if (by_row) pending = st;
-                else if (lane == 0) mbar_arrive(full);
+                if (lane == 0) mbar_arrive(full);
                 ++n_fetch;
             }
-            if (pending >= 0) land(false);
             bad = static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bad)));
             if (lane == 0 && W.lead) raise_status(A.status, bad);
         } else {
@@ -645,7 +636,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint4 v1 = real ? reinterpret_cast<const uint4 *>(at)[2 * lane + 1] : zero;
                         uint4 hi, lo;
                         const float f = split_query(v0, v1, hi, lo);
-                        __syncwarp();
                         reinterpret_cast<uint4 *>(at)[lane ^ (x & 7)] = hi;
                         reinterpret_cast<uint4 *>(at + 512)[lane ^ (x & 7)] = lo;
                         if (lane == 0) S.q_scale[q * 16 + x] = f * A.scale_log2;
