@@ -36,76 +36,131 @@ __device__ __forceinline__ int fp8_exponent(uint32_t amax) {
     return min(max(k, -kFp8MaxExp), kFp8MaxExp);
 }
 
-// One warp a row: its values stay in registers between the maximum and the
-// codes, so a row is read once; a lane has up to kUnits runs of 8 values.
-template <int kUnits>
-__device__ __forceinline__ void append_row(const AppendFp8Job &J, uint32_t row, int64_t slot, int lane) {
-    float x[kUnits][8];
-    uint32_t amax = 0;
-    const char *const src = J.rows + row * J.row_pitch;
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-        const uint32_t at = lane + 32 * u;
-        uint4 a = make_uint4(0, 0, 0, 0), b = a;
-        if (at < J.units) {
-            if (J.f32) {
-                a = __ldcs(reinterpret_cast<const uint4 *>(src + at * 32));
-                b = __ldcs(reinterpret_cast<const uint4 *>(src + at * 32 + 16));
-            } else {
-                a = __ldcs(reinterpret_cast<const uint4 *>(src + at * 16));
-            }
-        }
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[u][i] = __uint_as_float(J.f32 ? w[i] : i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t m = __float_as_uint(x[u][i]) & 0x7FFFFFFFu;
-            amax = max(amax, m < 0x7F800000u ? m : 0u);
-        }
-    }
-    const int k = fp8_exponent(__reduce_max_sync(0xffffffffu, amax));
-    const float inv = exponent_f32(-k);
-    const uint32_t s = static_cast<uint32_t>(slot), page = J.page_rows.div(s), in = s - page * J.page_rows.d;
-    uint8_t *const dst = J.cache + (page * J.page_stride + in) * (J.units * 8);
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-        const uint32_t at = lane + 32 * u;
-        if (at >= J.units) break;
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            y[i] = x[u][i] * inv;
-            if (!(fabsf(y[i]) <= 448.f)) y[i] = NAN;           // (the conversion would saturate)
-        }
-        *reinterpret_cast<uint2 *>(dst + at * 8) =
-            make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
-    }
-    if (lane == 0) J.scales[page * J.scale_stride + in] = exponent_f32(k);
-}
+constexpr uint32_t kFp8Largest = (60u + 8 + 127) << 23 | 0x600000u;   // 448 * 2^60, as f32 bits
 
-template <int kUnits>
+// Eight values of a row, bf16 or f32.
+struct Values {
+    float x[8];
+    __device__ __forceinline__ Values(const uint4 (&raw)[2], bool f32) {
+        const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = __uint_as_float(f32 ? w[e] : e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+    }
+};
+
+// One warp a row: its values stay in registers between the maximum and the
+// codes, so a row is read once; a lane has up to kUnits runs of 8 values.  kRows rows
+// at a time, and the slots of the next ones on their way, keep enough bytes in flight.
+template <int kUnits, int kRows>
 __global__ void __launch_bounds__(kFp8Threads) append_fp8_kernel(const AppendFp8Args A, int32_t *status) {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t all = A.start[A.num_jobs], step = static_cast<int64_t>(gridDim.x) * kFp8Warps;
-    int bad = 0;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kFp8Warps + (threadIdx.x >> 5); i < all; i += step) {
+    auto job_of = [&](int64_t i) {
         int j = 0;
 #pragma unroll
         for (int q = 1; q < CSA_MAX_APPEND_JOBS; ++q)
             if (q < A.num_jobs && i >= A.start[q]) j = q;
-        const AppendFp8Job &J = A.job[j];
-        const uint32_t row = static_cast<uint32_t>(i - A.start[j]);
-        const int64_t slot = J.slots[row];
-        if (slot < 0) continue;
-        if (slot >= J.slot_end) {
-            bad = CSA_DEV_BAD_INDEX;
-            continue;
+        return j;
+    };
+    auto slot_of = [&](int64_t i) {
+        if (i >= all) return int64_t(-1);
+        const int j = job_of(i);
+        return A.job[j].slots[i - A.start[j]];
+    };
+    int bad = 0;
+    int64_t i0 = static_cast<int64_t>(blockIdx.x) * kFp8Warps + (threadIdx.x >> 5);
+    int64_t coming[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) coming[r] = slot_of(i0 + r * step);
+    for (; i0 < all; i0 += kRows * step) {
+        int64_t slot[kRows];
+        uint4 raw[kRows][kUnits][2];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t i = i0 + r * step;
+            const int j = job_of(i);
+            const AppendFp8Job &J = A.job[j];
+            slot[r] = coming[r];
+            if (slot[r] >= J.slot_end) {
+                bad = CSA_DEV_BAD_INDEX;
+                slot[r] = -1;
+            }
+            const char *const src = J.rows + (i - A.start[j]) * J.row_pitch;
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const uint32_t at = lane + 32 * u;
+                raw[r][u][0] = raw[r][u][1] = make_uint4(0, 0, 0, 0);
+                if (slot[r] < 0 || at >= J.units) continue;
+                if (J.f32) {
+                    raw[r][u][0] = __ldcs(reinterpret_cast<const uint4 *>(src + at * 32));
+                    raw[r][u][1] = __ldcs(reinterpret_cast<const uint4 *>(src + at * 32 + 16));
+                } else {
+                    raw[r][u][0] = __ldcs(reinterpret_cast<const uint4 *>(src + at * 16));
+                }
+            }
         }
-        append_row<kUnits>(J, row, slot, lane);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) coming[r] = slot_of(i0 + (kRows + r) * step);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            if (slot[r] < 0) continue;
+            const AppendFp8Job &J = A.job[job_of(i0 + r * step)];
+            // the largest magnitude, of two numbers at a time for bf16
+            uint32_t amax = 0;
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const uint4 a = raw[r][u][0], b = raw[r][u][1];
+                if (J.f32) {
+                    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) amax = max(amax, w[e] & 0x7FFFFFFFu);
+                } else {
+                    const uint32_t m = __vmaxu2(__vmaxu2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu),
+                                                __vmaxu2(a.z & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu));
+                    amax = max(amax, max(m << 16, m & 0xFFFF0000u));
+                }
+            }
+            amax = __reduce_max_sync(0xffffffffu, amax);
+            // something infinite, NaN or above the largest scale: these become NaN, and the
+            // scale is that of the others
+            const bool odd = amax > kFp8Largest;
+            if (odd) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int u = 0; u < kUnits; ++u) {
+                    const Values v(raw[r][u], J.f32);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t x = __float_as_uint(v.x[e]) & 0x7FFFFFFFu;
+                        m = max(m, x < 0x7F800000u ? x : 0u);
+                    }
+                }
+                amax = __reduce_max_sync(0xffffffffu, m);
+            }
+            const int k = fp8_exponent(amax);
+            const float inv = exponent_f32(-k);
+            const uint32_t s = static_cast<uint32_t>(slot[r]), page = J.page_rows.div(s), in = s - page * J.page_rows.d;
+            uint8_t *const dst = J.cache + (page * J.page_stride + in) * (J.units * 8);
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const uint32_t at = lane + 32 * u;
+                if (at >= J.units) break;
+                Values y(raw[r][u], J.f32);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y.x[e] *= inv;
+                if (odd) {                               // (the conversion would saturate)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (!(fabsf(y.x[e]) <= 448.f)) y.x[e] = NAN;
+                }
+                *reinterpret_cast<uint2 *>(dst + at * 8) =
+                    make_uint2(e4m3x4(y.x[0], y.x[1], y.x[2], y.x[3]), e4m3x4(y.x[4], y.x[5], y.x[6], y.x[7]));
+            }
+            if (lane == 0) J.scales[page * J.scale_stride + in] = exponent_f32(k);
+        }
     }
     if (lane == 0) raise_status(status, bad);
 }
@@ -118,7 +173,8 @@ struct ReadFp8Args {
     uint32_t slot_end;
 };
 
-// One warp a row, 16 bytes of the output a lane at a time.
+// One warp a row, 16 bytes of the output a lane at a time, two ahead of the first
+// store, and the slot of the next row.
 template <bool kF32>
 __global__ void __launch_bounds__(kFp8Threads) read_fp8_kernel(const ReadFp8Args A, int32_t *status) {
     pdl_wait();
@@ -128,8 +184,11 @@ __global__ void __launch_bounds__(kFp8Threads) read_fp8_kernel(const ReadFp8Args
     const int lane = threadIdx.x & 31;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kFp8Warps;
     int bad = 0;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kFp8Warps + (threadIdx.x >> 5); i < R.num_rows; i += step) {
-        const int64_t slot = R.slots[i];
+    int64_t i = static_cast<int64_t>(blockIdx.x) * kFp8Warps + (threadIdx.x >> 5);
+    int64_t coming = i < R.num_rows ? R.slots[i] : -1;
+    for (; i < R.num_rows; i += step) {
+        const int64_t slot = coming;
+        coming = i + step < R.num_rows ? R.slots[i + step] : -1;
         if (slot < 0) continue;
         if (slot >= A.slot_end) {
             bad = CSA_DEV_BAD_INDEX;
@@ -139,20 +198,28 @@ __global__ void __launch_bounds__(kFp8Threads) read_fp8_kernel(const ReadFp8Args
         const uint8_t *const src = static_cast<const uint8_t *>(R.cache) + (page * R.page_stride + in) * R.width;
         const float scale = R.scales[page * R.scale_stride + in];
         char *const dst = static_cast<char *>(R.out) + i * R.out_pitch;
-        for (int c = lane; c < R.width / kVals; c += 32) {
-            if (kF32) {
-                float v[4];
-                e4m3x4_values(*reinterpret_cast<const uint32_t *>(src + c * 4), v);
-                *reinterpret_cast<float4 *>(dst + c * 16) =
-                    make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
-            } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(src + c * 8);
+        const int pieces = R.width / kVals;
+        for (int c = lane; c < pieces; c += 64) {
+            uint2 w[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                w[u] = make_uint2(0, 0);
+                if (c + 32 * u >= pieces) continue;
+                if (kF32) w[u].x = *reinterpret_cast<const uint32_t *>(src + (c + 32 * u) * 4);
+                else w[u] = *reinterpret_cast<const uint2 *>(src + (c + 32 * u) * 8);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (c + 32 * u >= pieces) continue;
                 float v[8];
-                e4m3x4_values(w.x, v);
-                e4m3x4_values(w.y, v + 4);
-                *reinterpret_cast<uint4 *>(dst + c * 16) =
-                    make_uint4(pack_bf16x2(v[0] * scale, v[1] * scale), pack_bf16x2(v[2] * scale, v[3] * scale),
-                               pack_bf16x2(v[4] * scale, v[5] * scale), pack_bf16x2(v[6] * scale, v[7] * scale));
+                e4m3x4_values(w[u].x, v);
+                if (!kF32) e4m3x4_values(w[u].y, v + 4);
+#pragma unroll
+                for (int e = 0; e < kVals; ++e) v[e] *= scale;
+                *reinterpret_cast<uint4 *>(dst + (c + 32 * u) * 16) =
+                    kF32 ? make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]))
+                         : make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                      pack_bf16x2(v[6], v[7]));
             }
         }
     }
@@ -240,7 +307,8 @@ extern "C" csa_status_t csa_paged_append_fp8(const csa_append_fp8_job_t *jobs, i
     const dim3 g(static_cast<unsigned>(grid)), b(kFp8Threads);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto launch = [&](auto units) {
-        constexpr auto kernel = append_fp8_kernel<decltype(units)::value>;
+        constexpr int kUnits = decltype(units)::value;
+        constexpr auto kernel = append_fp8_kernel<kUnits, kUnits == 4 ? 1 : 2>;
         const cudaError_t e = prepare_kernel<kernel>(0);
         return cuda_status(e != cudaSuccess ? e : launch_pdl(kernel, g, b, 0, s, A, dev_status));
     };
@@ -273,7 +341,7 @@ extern "C" csa_status_t csa_paged_read_fp8(const csa_read_fp8_t *read, int32_t *
     const csa_status_t st = current_device(&sms);
     if (st != CSA_OK) return st;
     int64_t grid = (R.num_rows + kFp8Warps - 1) / kFp8Warps;
-    if (grid > 8 * sms) grid = 8 * sms;
+    if (grid > 64 * sms) grid = 64 * sms;
     const ReadFp8Args A{R, FastDiv(R.page_rows), static_cast<uint32_t>(R.num_pages * R.page_rows)};
     const dim3 g(static_cast<unsigned>(grid)), b(kFp8Threads);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
