@@ -106,6 +106,7 @@ struct Smem {
     WorkSmem<kMaxRec> work;
 };
 
+
 // Whether a thread of the softmax says so, behind a barrier of all of them.
 __device__ __forceinline__ bool any_of(bool mine) {
     uint32_t any;
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++n_ql;
                 for (int k = 0; k < nch; ++k, ++nq) {
                     const uint32_t slot = nq + 2 * n_ql;
-                    const int st = slot % kSt, sb = nq & 1u;
+                    const uint32_t st = slot % kSt, sb = nq & 1u;
                     wait_for(&S.full[st], (slot / kSt) & 1u, A.status);
                     wait_for(&S.sfree[sb], ((nq >> 1) & 1u) ^ 1u, A.status);
                     fence_proxy_async_smem();            // (rows that came one by one)
@@ -378,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++n_ql;
                 const int every = flush_every<kFlush>(nch);
                 for (int k = 0, z = 0; k < nch; ++k, ++np, z = z + 1 == every ? 0 : z + 1) {
-                    const int st = (np + 2 * n_ql) % kSt, pb = np % kPB;
-#pragma unroll 1
+                    const uint32_t st = (np + 2 * n_ql) % kSt, pb = np % kPB;
+#pragma unroll
                     for (int ks = 0; ks < kSteps; ++ks) {
                         const uint64_t ad = a_desc + off(st * kStageBytes + ks * 4 * kGroupBytes);
                         const uint64_t pd = p_desc + off((pb * (kChunk / 16) + 2 * ks) * kPiece);
@@ -400,12 +401,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __syncwarp();
                             tc_fence_after();
                             if (elect_one()) {
-                                uint64_t a = ad;
-                                uint32_t d = tmem + kOCol;
-#pragma unroll 1
-                                for (int dd = 0; dd < ndt; ++dd, a += off(1024), d += kHG) {
+                                if (ndt == 4) {
 #pragma unroll
-                                    for (int t = 0; t < kTerms; ++t) umma_fp8(d, a, pd + off(t * kTermBytes), id, 1u);
+                                    for (int dd = 0; dd < 4; ++dd)
+#pragma unroll
+                                        for (int t = 0; t < kTerms; ++t)
+                                            umma_fp8(tmem + kOCol + kHG * dd, ad + off(dd * 1024), pd + off(t * kTermBytes), id, 1u);
+                                } else {
+                                    uint64_t a = ad;
+                                    uint32_t d = tmem + kOCol;
+#pragma unroll 1
+                                    for (int dd = 0; dd < ndt; ++dd, a += off(1024), d += kHG) {
+#pragma unroll
+                                        for (int t = 0; t < kTerms; ++t) umma_fp8(d, a, pd + off(t * kTermBytes), id, 1u);
+                                    }
                                 }
                             }
                             __syncwarp();
