@@ -644,8 +644,8 @@ csa_status_t csa_paged_read_fp8(const csa_read_fp8_t *read /* (host) */, int32_t
  *     result, the rest may hold anything.  Scales may be any f32 numbers of
  *     magnitude 2^-60 to 2^60 (or 0); a NaN in a row that is seen gives NaN.
  *   q bf16; a head whose query holds an infinity or NaN gives NaN.  A query
- *     value enters exactly where it is at least 2^-10 of its head's largest, else
- *     off by at most 2^-18 of that.
+ *     value enters exactly where it is at least 2^-9 of its head's largest, else
+ *     off by at most 2^-17 of that.
  * For a bf16 output the weights enter with a relative error of at most 2^-9,
  * for an f32 output 2^-18, each off by at most 2^-24 of the largest besides (in
  * units of scale times weight).

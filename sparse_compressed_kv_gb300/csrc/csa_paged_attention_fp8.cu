@@ -21,7 +21,8 @@
 // Q = hi + lo: a head's largest magnitude is brought to [2^7, 2^8) by a power of
 // two; hi is the nearest e4m3 value, lo the nearest to what is left.  A bf16
 // number has 8 bits and each term takes 4, so the two are exact down to 2^-10 of
-// the largest (lo's last place is 2^-9).  Rows 32 q + i and 32 q + 16 + i of the
+// 2^8 (lo's last place is 2^-9; below that a value is off by up to 2^-10, 2^-17 of its
+// head's largest).  Rows 32 q + i and 32 q + 16 + i of the
 // operand are the terms of head 16 q + i, so that both sums lie in the same warp's
 // quarter of tensor memory, and the softmax adds them.
 //
@@ -31,6 +32,17 @@
 // with the maximum m of l_j + log2 s_j brought to 2^7 (and up to 2^15 before it is
 // raised) a weight is cut off below 2^-24 of the largest, so that ten thousands of
 // small weights keep their sum.
+//
+// What bounds it, with 64 heads and a bf16 output: the tensor cores.  A chunk's products
+// take them 16 x 32 cycles for S (A in tensor memory) and 24 x 48 for O^T, whose operands
+// pass 128 bytes a cycle of shared memory (each measured alone): 1,670 cycles; the loop
+// takes 1,900, 34 KB of rows and scales each.  540,000 rows of 32 contexts 75.6 us (3.7
+// TB/s; the bytes alone 40.8), a million tokens at ratio 4 (262,144 rows) 44.6 us (20.0).
+// Three terms of 64 columns read a tile of O^T's A three times; one product of 128
+// or 192 columns would not, but the accumulators would need 512 or 768 columns of tensor
+// memory.  What a call begins and ends with, one long context on all SMs: 3,000 cycles
+// until the query is there, 4,200 to split and store it, 2,400 to the first O^T product;
+// 4,000 for the drain of a partial (128 KiB at 32 bytes a cycle); and the join's kernel.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -44,13 +56,14 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kBarQ = 2;                        // 2 .. 5: the two warps of a quarter of the softmax
 constexpr int kSmThreads = 256;                 // warps 0..7, half of them for each 32 rows of a chunk
-constexpr int kSmGroup = kSmThreads / 2;
+constexpr int kSmGroup = kSmThreads / 2;        // that half
 constexpr int kChunk = 64;
 constexpr int kSteps = kChunk / 32;             // of 32 rows: a fetch warp, half of the softmax, a K step of O^T each
 constexpr int kGroupBytes = 8 * kHD;            // 8 rows: 4 KiB
 constexpr int kStageBytes = kChunk / 8 * kGroupBytes;   // 32 KiB
 // What shared memory has room for beside two buffers of P (12 KiB each, 24 KiB with
-// an f32 output).
+// an f32 output): a row takes 1,300 to 1,900 cycles from its copy's start, as long as a
+// chunk's products, and a stage is held by two of them besides.
 template <int kTerms>
 constexpr int kStages = kTerms == 3 ? 6 : 5;
 constexpr int kPBufs = 2;
@@ -64,9 +77,15 @@ constexpr int kOCol = 128;                      // O^T: 4 tiles x 64 heads
 constexpr int kQCol = 384;                      // the query: 128 rows x 512 codes
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxRec = 32;                     // segments a CTA lists at a time
-constexpr int kSegCost = 2;                     // a segment's epilogue, in chunks
-constexpr int kCutAbove = 4;                    // chunks a token may exceed the mean before tokens are cut
-constexpr int kFlushF32 = 27, kFlushBf16 = 341; // chunks between roundings of the accumulator, at most
+// A segment's epilogue, in chunks: 2, 3 and 4 are 31.2, 32.5 and 33.9 us with 128 contexts
+// at ratio 128, 85.0, 85.1 and 83.8 us with 32 long ones.
+constexpr int kSegCost = 2;
+// Chunks a token may exceed the mean before tokens are cut: with 6 a token of 5 chunks by
+// itself takes 15.3 us instead of 9.8; 3 and 4 are alike.
+constexpr int kCutAbove = 4;
+// Chunks between roundings of the accumulator, at most: what the tensor cores drop grows
+// with the products that are added in a row (six or three terms, 64 rows).
+constexpr int kFlushF32 = 27, kFlushBf16 = 341;
 constexpr float kTop = 7.f;                     // log2 of the weight that the maximum is brought to
 
 // mbar_wait whose loop is a call: the first try is nearly all that stays in line (what
@@ -227,6 +246,18 @@ __device__ __forceinline__ float split_query(const uint4 &v0, const uint4 &v1, u
     hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
     lo = make_uint4(l[0] | l[1] << 16, l[2] | l[3] << 16, l[4] | l[5] << 16, l[6] | l[7] << 16);
     return top >= 0x7F80u ? NAN : exponent_f32(-k);
+}
+
+// A load under a condition that nothing waits for until the result is used (where a
+// branch's two ends are joined by a move, that does).
+__device__ __forceinline__ int32_t load_if(const int32_t *p, bool ok) {
+    int32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.b32 %0, [%1];\n\t}"
+                 : "=r"(r) : "l"(p), "r"(static_cast<uint32_t>(ok)));
+    return r;
+}
+__device__ __forceinline__ float load_if(const float *p, bool ok) {
+    return __int_as_float(load_if(reinterpret_cast<const int32_t *>(p), ok));
 }
 
 // A contiguous copy into shared memory, a multiple of 16 bytes.
@@ -401,6 +432,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __syncwarp();
                             tc_fence_after();
                             if (elect_one()) {
+                                // (all columns, unrolled: the loop's issue alone held the tensor
+                                // cores up, 32 contexts 82.3 us instead of 76.1)
                                 if (ndt == 4) {
 #pragma unroll
                                     for (int dd = 0; dd < 4; ++dd)
@@ -429,9 +462,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp >= 10) {
             // -------------------------------------------- row fetch
-            // The warp walks the list's chunks, a row of each a lane: three chunks
-            // before it is copied its page number is on its way from the table, two
-            // before it its scale.
+            // The warp walks the list's chunks, a row of each a lane: two chunks before it
+            // is copied its page number is on its way from the table, one before it its
+            // scale.  (Whole chunks by turns, two rows a lane, take as long in the loop, but a
+            // call's first rows start later: 256 rows 10.7 us instead of 9.6.)
             const int li = warp - 10;
             int bad = 0;
             struct Cursor {
@@ -448,23 +482,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 settle(k);
             };
             struct Entry {
-                int32_t page, at;                      // row of the page; or (page kRing) of the rings; < 0: no row
-                bool box;                              // 8 rows of one page from here on
+                int32_t page, at;                      // the table's entry; row of the page or of the rings, < 0: no row
+                bool ring, box;                        // 8 rows of one page from here on
             };
-            constexpr int32_t kRing = -2;
             auto look_up = [&](const Cursor &k) {
-                Entry e{-1, -1, false};
+                Entry e{-1, -1, false, false};
                 if (k.i >= nrec) return e;
                 const Rec &r = rec[k.i];
                 const int j = k.c * kChunk + 32 * li + lane, w = j - rec_window_slot(r);
-                if (j < r.n) {
-                    const int pg = static_cast<int>(A.page_div.div(j));
-                    e.at = j - pg * A.L.page_rows;
-                    e.page = max(A.L.table[static_cast<int64_t>(r.b) * A.L.max_pages + pg], -1);
-                    e.box = j + 8 <= r.n && e.at + 8 <= A.L.page_rows;
-                } else if (w >= 0 && w < r.near) {
+                const bool in = j < r.n;
+                const int pg = static_cast<int>(A.page_div.div(in ? j : 0));
+                e.page = load_if(A.L.table + static_cast<int64_t>(r.b) * A.L.max_pages + pg, in);
+                const int at = j - pg * A.L.page_rows;
+                if (in) e.at = at;
+                e.box = in && j + 8 <= r.n && at + 8 <= A.L.page_rows;
+                if (!in && w >= 0 && w < r.near) {
                     const int64_t x = r.first + w;
-                    e.page = kRing;
+                    e.ring = true;
                     if (x < r.first_res) bad |= CSA_DEV_MISSING_SWA;
                     else e.at = r.b * A.L.swa_cap + static_cast<int32_t>(A.swa_div.mod64(x));
                 }
@@ -477,21 +511,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t ring;                         // ... of the rings (no group holds rows of both)
             };
             auto place = [&](const Entry &e) {
-                Place p{-1, 0.f, 0, 0};
-                if (e.at >= 0) {
-                    if (e.page == kRing) {
-                        p.row = e.at;
-                        p.scale = __ldcg(A.swa_scales + e.at);
-                    } else if (e.page < 0 || e.page >= A.num_pages) {
-                        bad |= CSA_DEV_BAD_INDEX;
-                    } else {
-                        p.row = static_cast<int32_t>(e.page * A.page_stride) + e.at;
-                        if (!CSA_CHECK(p.row < A.total_rows, A.status)) p.row = -1;
-                        else p.scale = __ldcg(A.scales + e.page * A.scale_stride + e.at);
-                    }
-                }
+                Place p;
+                const bool paged = e.at >= 0 && !e.ring;
+                const bool out = paged && static_cast<uint32_t>(e.page) >= static_cast<uint32_t>(A.num_pages);
+                p.row = e.ring ? e.at : static_cast<int32_t>(e.page * A.page_stride) + e.at;
+                if (out) bad |= CSA_DEV_BAD_INDEX;
+                if (e.at < 0 || out) p.row = -1;
+                if (!CSA_CHECK(e.ring || p.row < A.total_rows, A.status)) p.row = -1;
+                p.scale = load_if(e.ring ? A.swa_scales + e.at : A.scales + e.page * A.scale_stride + e.at, p.row >= 0);
                 p.box = __ballot_sync(0xffffffffu, e.box) & 0x01010101u;
-                p.ring = __ballot_sync(0xffffffffu, e.page == kRing);
+                p.ring = __ballot_sync(0xffffffffu, e.ring);
                 return p;
             };
             // rows are read once, or once by each of two groups of heads
@@ -523,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (cur.i < nrec) query(cur.i);
             Place now{}, next{};
-            Entry ahead{-1, -1, false};
+            Entry ahead{-1, -1, false, false};
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
                 now = next;
@@ -544,12 +573,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int st = n_fetch % kSt;
                 const uint32_t ph = ((n_fetch / kSt) & 1u) ^ 1u;
                 uint64_t *const empty = &S.empty[st][li], *const full = &S.full[st];
+                const float slog = now.row >= 0 ? __log2f(fminf(fmaxf(fabsf(now.scale), 0x1p-60f), 0x1p60f)) : 0.f;
                 wait_for(empty, ph, A.status);
                 __syncwarp();
                 uint8_t *rows = sRows + st * kStageBytes + 4 * li * kGroupBytes;
                 S.scale[st][32 * li + lane] = now.scale;
-                S.scale_log[st][32 * li + lane] =
-                    now.row >= 0 ? __log2f(fminf(fmaxf(fabsf(now.scale), 0x1p-60f), 0x1p60f)) : 0.f;
+                S.scale_log[st][32 * li + lane] = slog;
                 if (lane == 0) {
                     S.maskw[st][li] = okm;
                     if (now.box) mbar_expect_tx(full, __popc(now.box) * kGroupBytes);

@@ -97,9 +97,10 @@ class PagedFp8(H.Paged):
 #   bf16: a weight off by at most 2^-9, the output rounded to bf16 (2^-8).
 #   f32: a weight off by at most 2^-18.  Its logit: 16 products of 32 columns into
 #     an f32 accumulator, one step (2^-23) each, and products with the scales.
-#     The query: about 1 value in 400 is below 2^-10 of its head's largest (3.5)
-#     and off by 2^-18 of that; two of 512, times a row's values (up to 3.5 times
-#     a magnitude of 2) and the scale 512^-.5: at most 2^-17.  The output: sums of
+#     The query: a value below 2^-2 where its head's largest is brought to 224
+#     (3.5: 2^-8, one value in 300) is off by 2^-10, 2^-17.8 of the largest; two of
+#     512, times a row's values (2.5 times a magnitude of 2) and the scale 512^-.5: at
+#     most 2^-17.  The output: sums of
 #     32 rows, six terms each, at most 1,728 rows before they are added, rounded, to the partial:
 #     324 steps, half of 2^-23 each on average.
 REL = {torch.bfloat16: (2 ** -18 + 2 ** -16) ** 0.5,
