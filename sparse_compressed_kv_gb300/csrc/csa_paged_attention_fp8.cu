@@ -72,9 +72,18 @@ constexpr int kStagedHeads = 16;                // of a bf16 output, on their wa
 constexpr int kTermBytes = kHG * 16;            // 16 rows of a term of P
 template <int kTerms>
 constexpr int kPieceBytes = kTerms * kTermBytes;
-constexpr int kSCol = 0;                        // two S buffers of 64 columns
-constexpr int kOCol = 128;                      // O^T: 4 tiles x 64 heads
-constexpr int kQCol = 384;                      // the query: 128 rows x 512 codes
+// Tensor memory: S in buffers of 64 columns; O^T, 4 tiles of 64 columns (heads); the
+// query, 128 rows x 512 codes.  With an f32 output's six terms the columns of a second S
+// buffer go to the first tile, which takes two terms from one reading of its rows into 64
+// columns each (128-head drafts 81.0 -> 78.6 us; a bf16 output's three: 0 to 2% slower).
+template <int kTerms>
+constexpr int kSBufs = kTerms == 3 ? 2 : 1;
+template <int kTerms>
+constexpr int kWide = kTerms == 3 ? 0 : 1;      // tiles of O^T that take two terms at a time
+constexpr int kSCol = 0;
+template <int kTerms>
+constexpr int kOCol = 64 * kSBufs<kTerms>;
+constexpr int kQCol = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxRec = 32;                     // segments a CTA lists at a time
 // A segment's epilogue, in chunks: 2, 3 and 4 are 31.2, 32.5 and 33.9 us with 128 contexts
@@ -303,7 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool kBf16 = kTerms == 3;
     constexpr int kFlush = kBf16 ? kFlushBf16 : kFlushF32;
     constexpr int kPiece = kPieceBytes<kTerms>;          // 16 rows of P
-    constexpr int kSt = kStages<kTerms>, kPB = kPBufs;
+    constexpr int kSt = kStages<kTerms>, kPB = kPBufs, kSB = kSBufs<kTerms>;
+    constexpr int kWd = kWide<kTerms>, kO = kOCol<kTerms>;
+    auto o_col = [](int dd) { return kO + kHG * (dd + (dd < kWd ? dd : kWd)); };
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = align_smem<1024>(smem_raw);
     uint8_t *sRows = smem;                               // [stage][8 groups][4 col groups][8 rows][128 B]
@@ -373,9 +384,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++n_ql;
                 for (int k = 0; k < nch; ++k, ++nq) {
                     const uint32_t slot = nq + 2 * n_ql;
-                    const uint32_t st = slot % kSt, sb = nq & 1u;
+                    const uint32_t st = slot % kSt, sb = nq % kSB;
                     wait_for(&S.full[st], (slot / kSt) & 1u, A.status);
-                    wait_for(&S.sfree[sb], ((nq >> 1) & 1u) ^ 1u, A.status);
+                    wait_for(&S.sfree[sb], ((nq / kSB) & 1u) ^ 1u, A.status);
                     fence_proxy_async_smem();            // (rows that came one by one)
                     __syncwarp();
                     tc_fence_after();
@@ -396,13 +407,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == 9) {
             // -------------------------------------------- O^T += rows^T . P^T
-            constexpr uint32_t id = idesc_fp8<128, kHG, true, true>();
+            constexpr uint32_t id = idesc_fp8<128, kHG, true, true>(), id_wide = idesc_fp8<128, 2 * kHG, true, true>();
             const uint64_t a_desc = sw128_desc(smem_addr(sRows) + dt0 * 1024, 1024, kGroupBytes);
             const uint64_t p_desc = atom_desc(smem_addr(sP), kPiece, 128);
             auto product = [&](int dd, uint64_t ad, uint64_t pd, uint32_t acc) {
+                if (dd < kWd) {
 #pragma unroll
-                for (int t = 0; t < kTerms; ++t)
-                    umma_fp8(tmem + kOCol + kHG * dd, ad + off(dd * 1024), pd + off(t * kTermBytes), id, t > 0 ? 1u : acc);
+                    for (int t = 0; t < kTerms; t += 2)
+                        umma_fp8(tmem + o_col(dd), ad + off(dd * 1024), pd + off(t * kTermBytes), t + 1 < kTerms ? id_wide : id,
+                                 t > 0 ? 1u : acc);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < kTerms; ++t)
+                        umma_fp8(tmem + o_col(dd), ad + off(dd * 1024), pd + off(t * kTermBytes), id, t > 0 ? 1u : acc);
+                }
             };
             for (int i = 0; i < nrec; ++i) {
                 const int nch = rec[i].c1 - rec[i].c0;
@@ -436,18 +454,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 // cores up, 32 contexts 82.3 us instead of 76.1)
                                 if (ndt == 4) {
 #pragma unroll
-                                    for (int dd = 0; dd < 4; ++dd)
-#pragma unroll
-                                        for (int t = 0; t < kTerms; ++t)
-                                            umma_fp8(tmem + kOCol + kHG * dd, ad + off(dd * 1024), pd + off(t * kTermBytes), id, 1u);
+                                    for (int dd = 0; dd < 4; ++dd) product(dd, ad, pd, 1u);
                                 } else {
-                                    uint64_t a = ad;
-                                    uint32_t d = tmem + kOCol;
-#pragma unroll 1
-                                    for (int dd = 0; dd < ndt; ++dd, a += off(1024), d += kHG) {
-#pragma unroll
-                                        for (int t = 0; t < kTerms; ++t) umma_fp8(d, a, pd + off(t * kTermBytes), id, 1u);
-                                    }
+                                    product(0, ad, pd, 1u);
+                                    if (ndt == 2) product(1, ad, pd, 1u);
                                 }
                             }
                             __syncwarp();
@@ -629,8 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 named_bar_sync(kBarSm, kSmThreads);      // (the factors are written)
                 tc_fence_after();
-                drain_stretch<kBf16, 0, kStagedHeads>(
-                    A, tmem + lane_off + kOCol, S.fin, S.flush, S.ofree, sP + warp * staged_bytes(kStagedHeads), dt0, ndt,
+                drain_stretch<kBf16, kWd, kStagedHeads>(
+                    A, tmem + lane_off + kO, S.fin, S.flush, S.ofree, sP + warp * staged_bytes(kStagedHeads), dt0, ndt,
                     32 * g, 32 * g + 32, min(kHG, H - h0), (static_cast<int64_t>(r.t) * H + h0) * kHD,
                     static_cast<int64_t>(r.slot) * gridDim.y + hg, add, part);
                 __syncwarp();
@@ -652,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // (the segment before this one is done with Q when its last logits have
                 // come)
-                if (n_sm > 0) wait_for(&S.sfull[(n_sm - 1) & 1u], ((n_sm - 1) >> 1) & 1u, A.status);
+                if (n_sm > 0) wait_for(&S.sfull[(n_sm - 1) % kSB], ((n_sm - 1) / kSB) & 1u, A.status);
                 __syncwarp();
                 tc_fence_after();
                 // Eight heads a warp, each split in its place (a lane has 16 columns; a
@@ -717,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 c2 = make_float2(c, c);
                 for (int k = 0, z = 0; k < nch; ++k, ++n_sm, z = z + 1 == every ? 0 : z + 1) {
                     const uint32_t slot = n_sm + 2 * n_ql;
-                    const int st = slot % kSt, sb = n_sm & 1u;
+                    const int st = slot % kSt, sb = n_sm % kSB;
                     // the rows' masks and scales, before their logits come
                     wait_for(&S.full[st], (slot / kSt) & 1u, A.status);
                     const uint32_t mw = S.maskw[st][g] >> (r0 & 16) & 0xFFFFu;
@@ -729,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // (a wait's lanes may leave it at different polls; what is
                     // .aligned below, tensor memory and barriers, wants the warp whole)
-                    wait_for(&S.sfull[sb], (n_sm >> 1) & 1u, A.status);
+                    wait_for(&S.sfull[sb], (n_sm / kSB) & 1u, A.status);
                     __syncwarp();
                     tc_fence_after();
                     {
@@ -791,17 +801,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                             while (heads) {
                                 const int h = __ffsll(heads) - 1;
                                 heads &= heads - 1;
-                                const uint32_t o = tmem + lane_off + kOCol + h;
+                                const uint32_t o = tmem + lane_off + h;
                                 const float f = S.alpha[h];
+                                const int dd = ndt == 4 ? 2 * g : g;
+                                const uint32_t a = o + o_col(dd), b = o + o_col(dd + 1);
+                                if (dd < kWd) {                    // (its second half)
+                                    const float x = tmem_ld1(a + kHG);
+                                    tmem_wait_ld();
+                                    tmem_st1(a + kHG, x * f);
+                                }
                                 if (ndt == 4) {
-                                    const float x0 = tmem_ld1(o + 2 * kHG * g), x1 = tmem_ld1(o + 2 * kHG * g + kHG);
+                                    const float x0 = tmem_ld1(a), x1 = tmem_ld1(b);
                                     tmem_wait_ld();
-                                    tmem_st1(o + 2 * kHG * g, x0 * f);
-                                    tmem_st1(o + 2 * kHG * g + kHG, x1 * f);
-                                } else if (g < ndt) {
-                                    const float x0 = tmem_ld1(o + kHG * g);
+                                    tmem_st1(a, x0 * f);
+                                    tmem_st1(b, x1 * f);
+                                } else if (dd < ndt) {
+                                    const float x0 = tmem_ld1(a);
                                     tmem_wait_ld();
-                                    tmem_st1(o + kHG * g, x0 * f);
+                                    tmem_st1(a, x0 * f);
                                 }
                             }
                             tmem_wait_st();
