@@ -259,14 +259,16 @@ __device__ __forceinline__ float split_query(const uint4 &v0, const uint4 &v1, u
 
 // A load under a condition that nothing waits for until the result is used (where a
 // branch's two ends are joined by a move, that does).
-__device__ __forceinline__ int32_t load_if(const int32_t *p, bool ok) {
+template <bool kL2>
+__device__ __forceinline__ int32_t load_if(const void *p, bool ok) {
     int32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.b32 %0, [%1];\n\t}"
-                 : "=r"(r) : "l"(p), "r"(static_cast<uint32_t>(ok)));
+    if constexpr (kL2)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.cg.b32 %0, [%1];\n\t}"
+                     : "=r"(r) : "l"(p), "r"(static_cast<uint32_t>(ok)));
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.b32 %0, [%1];\n\t}"
+                     : "=r"(r) : "l"(p), "r"(static_cast<uint32_t>(ok)));
     return r;
-}
-__device__ __forceinline__ float load_if(const float *p, bool ok) {
-    return __int_as_float(load_if(reinterpret_cast<const int32_t *>(p), ok));
 }
 
 // A contiguous copy into shared memory, a multiple of 16 bytes.
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int j = k.c * kChunk + 32 * li + lane, w = j - rec_window_slot(r);
                 const bool in = j < r.n;
                 const int pg = static_cast<int>(A.page_div.div(in ? j : 0));
-                e.page = load_if(A.L.table + static_cast<int64_t>(r.b) * A.L.max_pages + pg, in);
+                e.page = load_if<false>(A.L.table + static_cast<int64_t>(r.b) * A.L.max_pages + pg, in);
                 const int at = j - pg * A.L.page_rows;
                 if (in) e.at = at;
                 e.box = in && j + 8 <= r.n && at + 8 <= A.L.page_rows;
@@ -528,7 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (out) bad |= CSA_DEV_BAD_INDEX;
                 if (e.at < 0 || out) p.row = -1;
                 if (!CSA_CHECK(e.ring || p.row < A.total_rows, A.status)) p.row = -1;
-                p.scale = load_if(e.ring ? A.swa_scales + e.at : A.scales + e.page * A.scale_stride + e.at, p.row >= 0);
+                p.scale = __int_as_float(load_if<true>(
+                    e.ring ? A.swa_scales + e.at : A.scales + e.page * A.scale_stride + e.at, p.row >= 0));
                 p.box = __ballot_sync(0xffffffffu, e.box) & 0x01010101u;
                 p.ring = __ballot_sync(0xffffffffu, e.ring);
                 return p;
