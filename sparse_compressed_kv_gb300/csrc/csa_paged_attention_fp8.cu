@@ -33,11 +33,13 @@
 // raised) a weight is cut off below 2^-24 of the largest, so that ten thousands of
 // small weights keep their sum.
 //
-// What bounds it, with 64 heads and a bf16 output: the tensor cores.  A chunk's products
-// take them 16 x 32 cycles for S (A in tensor memory) and 24 x 48 for O^T, whose operands
-// pass 128 bytes a cycle of shared memory (each measured alone): 1,670 cycles; the loop
-// takes 1,900, 34 KB of rows and scales each.  540,000 rows of 32 contexts 75.6 us (3.7
-// TB/s; the bytes alone 40.8), a million tokens at ratio 4 (262,144 rows) 44.6 us (20.0).
+// What bounds it, with 64 heads: shared memory, which passes 128 bytes a cycle.  For a
+// bf16 output a chunk's products read 176 KB (the rows once for S and once a term for
+// O^T, the weights once a tile), 32 KB of rows and 12 KB of weights are written: 1,720
+// cycles.  (The products alone: 16 x 32 cycles for S, A in tensor memory, and 24 x 48 for
+// O^T, 1,670.)  The loop takes 1,900; for an f32 output 352 KB, 2,750, and 3,050.
+// 540,000 rows of 32 contexts 75.7 us (3.7 TB/s; the bytes alone 40.8), a million tokens
+// at ratio 4 (262,144 rows) 44.6 us (20.0).
 // Three terms of 64 columns read a tile of O^T's A three times; one product of 128
 // or 192 columns would not, but the accumulators would need 512 or 768 columns of tensor
 // memory.  What a call begins and ends with, one long context on all SMs: 3,000 cycles

@@ -622,6 +622,48 @@ def test_attention_replayed_with_other_lengths(cuda_device):
         F.check(out, p.reference(), F32)
 
 
+def test_append_and_read_replayed_on_another_stream(cuda_device):
+    # one graph of both calls, other rows, slots and results at each replay; every
+    # append overwrites codes and scales beside those that a replay before it read
+    dev, n, page_rows = cuda_device, 700, 24
+    g = torch.Generator().manual_seed(77)
+    rows = torch.empty(n, 512, dtype=BF16, device=dev)
+    slots, back = (torch.empty(n, dtype=torch.int64, device=dev) for _ in range(2))
+    cache = torch.zeros(40, page_rows, 512, device=dev).to(F8)
+    scales, out = torch.ones(40, page_rows, device=dev), torch.zeros(n, 512, device=dev)
+    status, s = status_word(dev), torch.cuda.Stream()
+    jobs = csa.AppendJobsFp8([csa.AppendJobFp8(rows, slots, cache, scales, page_rows)])
+    held = np.zeros((40 * page_rows, 512), np.uint8), np.ones(40 * page_rows)
+
+    def fill():
+        x = torch.randn(n, 512, generator=g) * torch.exp2(torch.randint(-9, 9, (n, 1), generator=g).float())
+        at, of = torch.randperm(40 * page_rows, generator=g)[:n], torch.randint(-1, 40 * page_rows, (n,), generator=g)
+        rows.copy_(x)
+        slots.copy_(at)
+        back.copy_(of)
+        held[0][at], held[1][at] = F.quantise(x.to(BF16).double().numpy())
+        torch.cuda.synchronize()
+        return of
+
+    def calls():
+        csa.csa_paged_append_fp8(jobs, status, stream=s)
+        csa.csa_paged_read_fp8(cache, scales, back, out, status, page_rows, stream=s)
+
+    fill()
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        calls()
+    want = out.cpu().double()
+    for _ in range(4):
+        of = fill()
+        graph.replay()
+        torch.cuda.synchronize()
+        want[of >= 0] = F.values(*held)[of[of >= 0]]
+        assert int(status.item()) == 0 and torch.equal(out.cpu().double(), want)
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("captured", [False, True])
