@@ -38,7 +38,7 @@
 // O^T, the weights once a tile), 32 KB of rows and 12 KB of weights are written: 1,720
 // cycles.  (The products alone: 16 x 32 cycles for S, A in tensor memory, and 24 x 48 for
 // O^T, 1,670.)  The loop takes 1,900; for an f32 output 352 KB, 2,750, and 3,050.
-// 540,000 rows of 32 contexts 75.7 us (3.7 TB/s; the bytes alone 40.8), a million tokens
+// 540,000 rows of 32 contexts 75.4 us (3.7 TB/s; the bytes alone 40.8), a million tokens
 // at ratio 4 (262,144 rows) 44.6 us (20.0).
 // Three terms of 64 columns read a tile of O^T's A three times; one product of 128
 // or 192 columns would not, but the accumulators would need 512 or 768 columns of tensor
@@ -603,17 +603,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane < 4 && (now.box >> (8 * lane) & 1u))
                     tma_load_3d(rows + lane * kGroupBytes, &tm_rows, 0, y >= 0 ? y : A.total_rows, 0, full, pol);
                 if (now.box != 0x01010101u) {
+                    // eight lanes take 128 columns of a row, four rows an instruction (a row an
+                    // instruction, 128 contexts in pages of two rows: 28.6 us instead of 27.7)
 #pragma unroll 1
                     for (int x = 0; x < 4; ++x) {
                         if (now.box >> (8 * x) & 1u) continue;
                         const uint8_t *const from =
-                            (now.ring >> (8 * x) & 1u ? static_cast<const uint8_t *>(A.L.swa_kv) : A.codes) + lane * 16;
-                        uint8_t *const to = rows + x * kGroupBytes + (lane >> 3) * 1024;
+                            (now.ring >> (8 * x) & 1u ? static_cast<const uint8_t *>(A.L.swa_kv) : A.codes) + (lane & 7) * 16;
+                        uint8_t *const to = rows + x * kGroupBytes;
 #pragma unroll
-                        for (int rr = 0; rr < 8; ++rr) {
+                        for (int h = 0; h < 8; h += 4) {
+                            const int rr = h + (lane >> 3);
                             const int32_t row = __shfl_sync(0xffffffffu, now.row, 8 * x + rr);
-                            cp_async16(to + rr * 128 + (((lane & 7) ^ rr) << 4), from + static_cast<int64_t>(max(row, 0)) * kHD,
-                                       row >= 0);
+                            const uint8_t *const src = from + static_cast<int64_t>(max(row, 0)) * kHD;
+                            uint8_t *const dst = to + rr * 128 + (((lane & 7) ^ rr) << 4);
+#pragma unroll
+                            for (int cg = 0; cg < 4; ++cg) cp_async16(dst + cg * 1024, src + cg * 128, row >= 0);
                         }
                     }
                     // (the stage is full when they have landed; nobody waits for them here)
@@ -670,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n_sm > 0) wait_for(&S.sfull[(n_sm - 1) % kSB], ((n_sm - 1) / kSB) & 1u, A.status);
                 __syncwarp();
                 tc_fence_after();
-                // Eight heads a warp, each split in its place (a lane has 16 columns; a
+                // Eight heads a warp, each split in its place (a lane has 2 x 8 columns; a
                 // head's 512 codes hi, then lo, in pieces of 16 whose order depends on the
                 // head); then half a row of codes a lane into tensor memory.
                 {
@@ -685,12 +690,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 8 * g; x < 8 * g + 8; ++x) {
                         uint8_t *const at = qs + x * 1024;
                         const bool real = h0 + q * 16 + x < H;
-                        const uint4 v0 = real ? reinterpret_cast<const uint4 *>(at)[2 * lane] : zero;
-                        const uint4 v1 = real ? reinterpret_cast<const uint4 *>(at)[2 * lane + 1] : zero;
+                        const uint4 v0 = real ? reinterpret_cast<const uint4 *>(at)[lane] : zero;
+                        const uint4 v1 = real ? reinterpret_cast<const uint4 *>(at)[32 + lane] : zero;
                         uint4 hi, lo;
                         const float f = split_query(v0, v1, hi, lo);
-                        reinterpret_cast<uint4 *>(at)[lane ^ (x & 7)] = hi;
-                        reinterpret_cast<uint4 *>(at + 512)[lane ^ (x & 7)] = lo;
+                        uint2 *const to = reinterpret_cast<uint2 *>(at) + (lane ^ (x & 7) << 1);
+                        to[0] = make_uint2(hi.x, hi.y);
+                        to[32] = make_uint2(hi.z, hi.w);
+                        to[64] = make_uint2(lo.x, lo.y);
+                        to[96] = make_uint2(lo.z, lo.w);
                         if (lane == 0) S.q_scale[q * 16 + x] = f * A.scale_log2;
                     }
                     __syncwarp();
