@@ -39,7 +39,7 @@
 // cycles.  (The products alone: 16 x 32 cycles for S, A in tensor memory, and 24 x 48 for
 // O^T, 1,670.)  The loop takes 1,900; for an f32 output 352 KB, 2,750, and 3,050.
 // 540,000 rows of 32 contexts 75.4 us (3.7 TB/s; the bytes alone 40.8), a million tokens
-// at ratio 4 (262,144 rows) 44.6 us (20.0).
+// at ratio 4 (262,144 rows) 44.8 us (20.0).
 // Three terms of 64 columns read a tile of O^T's A three times; one product of 128
 // or 192 columns would not, but the accumulators would need 512 or 768 columns of tensor
 // memory.  What a call begins and ends with, one long context on all SMs: 3,000 cycles
@@ -88,11 +88,12 @@ constexpr int kOCol = 64 * kSBufs<kTerms>;
 constexpr int kQCol = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxRec = 32;                     // segments a CTA lists at a time
-// A segment's epilogue, in chunks: 2, 3 and 4 are 31.2, 32.5 and 33.9 us with 128 contexts
-// at ratio 128, 85.0, 85.1 and 83.8 us with 32 long ones.
-constexpr int kSegCost = 2;
-// Chunks a token may exceed the mean before tokens are cut: with 6 a token of 5 chunks by
-// itself takes 15.3 us instead of 9.8; 3 and 4 are alike.
+// A segment's beginning and end, in chunks: 1, 2, 3 and 4 are 29.9, 27.6, 27.5 and 27.7 us
+// with 128 contexts at ratio 128, 76.9, 76.0, 75.6 and 75.8 with 32 long ones, 82.7, 78.4,
+// 78.2 and 79.6 with 128-head drafts.
+constexpr int kSegCost = 3;
+// Chunks a token may exceed the mean before tokens are cut: with 6 a token of 6 chunks by
+// itself takes 14.6 us instead of 9.7; 2, 3 and 4 are alike.
 constexpr int kCutAbove = 4;
 // Chunks between roundings of the accumulator, at most: what the tensor cores drop grows
 // with the products that are added in a row (six or three terms, 64 rows).
