@@ -56,7 +56,6 @@ namespace csa {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kBarQ = 2;                        // 2 .. 5: the two warps of a quarter of the softmax
 constexpr int kSmThreads = 256;                 // warps 0..7, half of them for each 32 rows of a chunk
 constexpr int kSmGroup = kSmThreads / 2;        // that half
 constexpr int kChunk = 64;
@@ -676,37 +675,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n_sm > 0) wait_for(&S.sfull[(n_sm - 1) % kSB], ((n_sm - 1) / kSB) & 1u, A.status);
                 __syncwarp();
                 tc_fence_after();
-                // Eight heads a warp, each split in its place (a lane has 2 x 8 columns; a
-                // head's 512 codes hi, then lo, in pieces of 16 whose order depends on the
-                // head); then half a row of codes a lane into tensor memory.
+                // The heads that there are, by turns among the warps, each split in its place
+                // (a lane has 2 x 8 columns; a head's 512 codes hi, then lo, in pieces of 16
+                // whose order depends on the head); then half a row of codes a lane into
+                // tensor memory.  (Rows of absent heads hold anything: no other row's sums
+                // see them, and their own are left where they are.)
                 {
                     const uint32_t slot = n_sm + 2 * n_ql;
                     const int st0 = slot % kSt, st1 = (slot + 1) % kSt;
                     wait_for(&S.full[st0], (slot / kSt) & 1u, A.status);
                     wait_for(&S.full[st1], ((slot + 1) / kSt) & 1u, A.status);
                     __syncwarp();
-                    uint8_t *const qs = sRows + (q < 2 ? st0 : st1) * kStageBytes + (q & 1) * (16 * 1024);
-                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    const int heads = min(kHG, H - h0);
 #pragma unroll 2
-                    for (int x = 8 * g; x < 8 * g + 8; ++x) {
-                        uint8_t *const at = qs + x * 1024;
-                        const bool real = h0 + q * 16 + x < H;
-                        const uint4 v0 = real ? reinterpret_cast<const uint4 *>(at)[lane] : zero;
-                        const uint4 v1 = real ? reinterpret_cast<const uint4 *>(at)[32 + lane] : zero;
+                    for (int h = warp; h < heads; h += kSmThreads / 32) {
+                        uint8_t *const at = sRows + (h < 32 ? st0 : st1) * kStageBytes + (h & 31) * 1024;
+                        const uint4 v0 = reinterpret_cast<const uint4 *>(at)[lane];
+                        const uint4 v1 = reinterpret_cast<const uint4 *>(at)[32 + lane];
                         uint4 hi, lo;
                         const float f = split_query(v0, v1, hi, lo);
-                        uint2 *const to = reinterpret_cast<uint2 *>(at) + (lane ^ (x & 7) << 1);
+                        __syncwarp();
+                        uint2 *const to = reinterpret_cast<uint2 *>(at) + (lane ^ (h & 7) << 1);
                         to[0] = make_uint2(hi.x, hi.y);
                         to[32] = make_uint2(hi.z, hi.w);
                         to[64] = make_uint2(lo.x, lo.y);
                         to[96] = make_uint2(lo.z, lo.w);
-                        if (lane == 0) S.q_scale[q * 16 + x] = f * A.scale_log2;
+                        if (lane == 0) S.q_scale[h] = f * A.scale_log2;
                     }
                     __syncwarp();
-                    named_bar_sync(kBarQ + q, 64);
-                    const uint4 *const get = reinterpret_cast<const uint4 *>(qs + (lane & 15) * 1024 + (lane >> 4) * 512) + 16 * g;
+                    named_bar_sync(kBarSm, kSmThreads);
+                    const uint4 *const get = reinterpret_cast<const uint4 *>(
+                        sRows + (q < 2 ? st0 : st1) * kStageBytes + ((q & 1) * 16 + (lane & 15)) * 1024 + (lane >> 4) * 512) + 16 * g;
 #pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
+                        if (16 * q >= heads) break;
                         uint32_t o[32];
 #pragma unroll
                         for (int x = 0; x < 8; ++x) {
