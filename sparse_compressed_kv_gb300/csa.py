@@ -417,7 +417,7 @@ def _device_stream(fn: str, index: int, stream=None) -> int:
 
 
 def _ptr(t, index: int, contiguous=True) -> int:
-    if not t.is_cuda or t.get_device() != index:
+    if t.get_device() != index or index < 0:         # (a host tensor's is -1)
         raise ValueError(f"tensor must live on cuda:{index}")
     if contiguous and not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
@@ -429,21 +429,22 @@ def _page_stride(cache, page_rows: int) -> int:
     is a whole pool or one layer's part of a pool that several share
     (pool[:, first:first + page_rows]): the rows of a page are dense, the pages
     any whole number of rows apart."""
-    rows = int(cache.shape[1])
+    shape = cache.shape
+    rows = shape[1]
     if rows < page_rows:
         raise ValueError(f"a page of cache holds {rows} rows, not {page_rows}")
     if cache.is_contiguous():
         return rows
     want, width = [], 1
-    for n in reversed(cache.shape[1:]):
+    for n in reversed(shape[1:]):
         want.insert(0, width)
-        width *= int(n)
+        width *= n
     row = width // max(rows, 1)
-    dense = all(n == 1 or s == w for n, s, w in zip(cache.shape[1:], cache.stride()[1:], want))
-    apart = cache.stride(0) if cache.shape[0] > 1 else width
+    dense = all(n == 1 or s == w for n, s, w in zip(shape[1:], cache.stride()[1:], want))
+    apart = cache.stride(0) if shape[0] > 1 else width
     if not dense or row == 0 or apart % row or apart < width:
         raise ValueError("cache must have dense pages, a whole number of rows apart, got shape "
-                         f"{tuple(cache.shape)} and stride {cache.stride()}")
+                         f"{tuple(shape)} and stride {cache.stride()}")
     return apart // row
 
 
