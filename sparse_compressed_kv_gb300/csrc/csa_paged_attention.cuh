@@ -376,8 +376,9 @@ __device__ __forceinline__ uint64_t atom_desc(uint32_t saddr, uint32_t lbo, uint
 __device__ __forceinline__ constexpr uint64_t off(uint32_t bytes) { return bytes >> 4; }
 
 // O^T of a stretch into the partial, or the output, by the epilogue's warps: tile by
-// tile, each handed back to the products once it is in registers.  A warp has the
-// columns of its quarter and the heads hb0 .. hb1 - 1 (multiples of 32) below hmax.
+// tile, each handed back to the products (by `ofree`, if any) once it is in registers.
+// A warp has the columns of its quarter and the heads hb0 .. hb1 - 1 (multiples of 32)
+// below hmax.
 //   o_tmem  the first tile's first column, in this warp's lanes; each tile has 64
 //           columns (heads), the first kWide ones 64 more that are added to them
 //   add     the partial holds earlier stretches, to be scaled by `flush`
@@ -398,7 +399,7 @@ __device__ __forceinline__ void drain_stretch(const PagedArgs &A, uint32_t o_tme
 #pragma unroll 1
         for (int hb = hb0; hb < hb1; hb += 32) {
             if (hb >= hmax) {                    // (hb0: nothing to do)
-                if (hb == hb0) mbar_arrive(&ofree[dd]);
+                if (ofree && hb == hb0) mbar_arrive(&ofree[dd]);
                 break;
             }
             uint32_t o[32];
@@ -434,7 +435,7 @@ __device__ __forceinline__ void drain_stretch(const PagedArgs &A, uint32_t o_tme
             tmem_wait_ld();
             if (hb + 32 >= min(hb1, hmax)) { // the tile is in registers
                 tc_fence_before();
-                mbar_arrive(&ofree[dd]);
+                if (ofree) mbar_arrive(&ofree[dd]);
             }
             if (part) {
 #pragma unroll

@@ -121,7 +121,6 @@ struct Smem {
     uint64_t full[kMaxStages], empty[kMaxStages][kSteps];    // a stage is released 32 rows at a time
     uint64_t sfull[2], sfree[2];
     uint64_t pfull[2][kSteps], pfree[2];
-    uint64_t ofree[4];           // a tile of O^T is drained
     uint32_t tmem_holder;
     uint32_t maskw[kMaxStages][kSteps];
     uint32_t risen[4];           // heads to be rescaled, 16 a word
@@ -341,7 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < kSteps; ++k) mbar_init(&S.pfull[i][k], kSmGroup);
             mbar_init(&S.pfree[i], 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&S.ofree[i], kSmThreads);
         mbar_fence_init();
         tma_prefetch_desc(&tm_rows);
     }
@@ -367,7 +365,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // chunk n of segment m is number n + 2 m + 2 of what the stages hold)
     uint32_t n_ql = 0;                   // segments begun
     uint32_t n_sm = 0;                   // chunks through the softmax
-    uint32_t n_st = 0;                   // stretches begun by the products
 
     for (;;) {
         __syncthreads();
@@ -438,34 +435,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t ad = a_desc + off(st * kStageBytes + ks * 4 * kGroupBytes);
                         const uint64_t pd = p_desc + off((pb * (kChunk / 16) + 2 * ks) * kPiece);
                         wait_for(&S.pfull[pb][ks], (np / kPB) & 1u, A.status);
-                        if (z == 0 && ks == 0) {
-                            // a stretch's first product: tile by tile, as the stretch before it
-                            // leaves them
-#pragma unroll 1
-                            for (int dd = 0; dd < ndt; ++dd) {
-                                if (n_st > 0) wait_for(&S.ofree[dd], (n_st - 1) & 1u, A.status);
-                                __syncwarp();
-                                tc_fence_after();
-                                if (elect_one()) product(dd, ad, pd, 0u);
-                                __syncwarp();
-                            }
-                            ++n_st;
-                        } else {
-                            __syncwarp();
-                            tc_fence_after();
-                            if (elect_one()) {
-                                // (all columns, unrolled: the loop's issue alone held the tensor
-                                // cores up, 32 contexts 82.3 us instead of 76.1)
-                                if (ndt == 4) {
+                        // (a stretch's first product: the one before it has been drained by the
+                        // warps that made these weights)
+                        const uint32_t acc = z > 0 || ks > 0;
+                        __syncwarp();
+                        tc_fence_after();
+                        if (elect_one()) {
+                            // (all columns, unrolled: the loop's issue alone held the tensor
+                            // cores up, 32 contexts 82.3 us instead of 76.1)
+                            if (ndt == 4) {
 #pragma unroll
-                                    for (int dd = 0; dd < 4; ++dd) product(dd, ad, pd, 1u);
-                                } else {
-                                    product(0, ad, pd, 1u);
-                                    if (ndt == 2) product(1, ad, pd, 1u);
-                                }
+                                for (int dd = 0; dd < 4; ++dd) product(dd, ad, pd, acc);
+                            } else {
+#pragma unroll 1
+                                for (int dd = 0; dd < ndt; ++dd) product(dd, ad, pd, acc);
                             }
-                            __syncwarp();
                         }
+                        __syncwarp();
                         if (elect_one()) {
                             umma_commit(&S.empty[st][ks]);
                             if (ks + 1 == kSteps) umma_commit(&S.pfree[pb]);
@@ -650,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 named_bar_sync(kBarSm, kSmThreads);      // (the factors are written)
                 tc_fence_after();
                 drain_stretch<kBf16, kWd, kStagedHeads>(
-                    A, tmem + lane_off + kO, S.fin, S.flush, S.ofree, sP + warp * staged_bytes(kStagedHeads), dt0, ndt,
+                    A, tmem + lane_off + kO, S.fin, S.flush, nullptr, sP + warp * staged_bytes(kStagedHeads), dt0, ndt,
                     32 * g, 32 * g + 32, min(kHG, H - h0), (static_cast<int64_t>(r.t) * H + h0) * kHD,
                     static_cast<int64_t>(r.slot) * gridDim.y + hg, add, part);
                 __syncwarp();
