@@ -5,8 +5,8 @@
 // The division of the work, the segments, the partials and the joins are those
 // of the bf16 rows' kernel (csa_paged_attention.cuh); a chunk is 64 row slots, and
 // the codes are the tensor cores' operands as they lie in memory:
-//   warps 0..7    the query, 8 heads each, split in two e4m3 terms where a segment
-//                 begins; softmax with a lazily raised maximum, warps 0..3 of the
+//   warps 0..7    where a segment begins, its query's heads by turns, split in two e4m3
+//                 terms; softmax with a lazily raised maximum, warps 0..3 of the
 //                 chunk's rows 0..31, warps 4..7 of the others;
 //                 and a segment's epilogue, under the next segment's first logits
 //   warp 8        S = Q . rows^T (M = 64 heads x 2 terms from tensor memory, N = 64
@@ -22,9 +22,9 @@
 // two; hi is the nearest e4m3 value, lo the nearest to what is left.  A bf16
 // number has 8 bits and each term takes 4, so the two are exact down to 2^-10 of
 // 2^8 (lo's last place is 2^-9; below that a value is off by up to 2^-10, 2^-17 of its
-// head's largest).  Rows 32 q + i and 32 q + 16 + i of the
-// operand are the terms of head 16 q + i, so that both sums lie in the same warp's
-// quarter of tensor memory, and the softmax adds them.
+// head's largest).  Rows 32 q + i and 32 q + 16 + i of the operand are the terms of head
+// 16 q + i, so that both sums lie in the same warp's quarter of tensor memory, and the
+// softmax adds them.
 //
 // P = 2^(l_j - m) s_j as e5m2 terms of 3 bits: what f16 rounds it to, cut into
 // bytes (e5m2 is f16's upper byte), three terms for a bf16 output (2^-9), six for
@@ -38,8 +38,8 @@
 // O^T, the weights once a tile), 32 KB of rows and 12 KB of weights are written: 1,720
 // cycles.  (The products alone: 16 x 32 cycles for S, A in tensor memory, and 24 x 48 for
 // O^T, 1,670.)  The loop takes 1,900; for an f32 output 352 KB, 2,750, and 3,050.
-// 540,000 rows of 32 contexts 75.4 us (3.7 TB/s; the bytes alone 40.8), a million tokens
-// at ratio 4 (262,144 rows) 44.8 us (20.0).
+// 540,000 rows of 32 contexts 75.7 us (3.7 TB/s; the bytes alone 40.8), a million tokens
+// at ratio 4 (262,144 rows) 45.0 us (20.0).
 // Three terms of 64 columns read a tile of O^T's A three times; one product of 128
 // or 192 columns would not, but the accumulators would need 512 or 768 columns of tensor
 // memory.  What a call begins and ends with, one long context on all SMs: 3,000 cycles
