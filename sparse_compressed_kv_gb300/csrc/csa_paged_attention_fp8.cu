@@ -774,58 +774,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, 16));
                     // a head whose maximum rises by more than kRescaleAbove (the first one
                     // does) rescales what has been accumulated
-                    if (any_of(hv && mc > m_ref + kRescaleAbove)) {
+                    const bool risen = any_of(hv && mc > m_ref + kRescaleAbove);
+                    float alpha = 1.f;
+                    if (risen) {
                         if (!upper) S.rise[g][hl] = mc;
                         __syncwarp();
                         named_bar_sync(kBarSm, kSmThreads);
                         mc = fmaxf(S.rise[0][hl], S.rise[1][hl]);
-                        float alpha = 1.f;
                         if (hv && mc > m_ref + kRescaleAbove) {
                             if (m_ref != -INFINITY) alpha = exp2f(m_ref - mc);
                             m_ref = mc;
                             l *= alpha;
-                        }
-                        if (z != 0) {
-                            const uint32_t mine = __ballot_sync(0xffffffffu, alpha != 1.f) & 0xFFFFu;
-                            if (g == 0 && !upper) S.alpha[hl] = alpha;
-                            if (g == 0 && lane == 0) S.risen[q] = mine;
-                            // the product before this one (and the one before that: a wait
-                            // tells a phase from the next, but not from the one after)
-                            wait_for(&S.pfree[n_sm % kPB], ((n_sm / kPB) & 1u) ^ 1u, A.status);
-                            wait_for(&S.pfree[(n_sm - 1) % kPB], ((n_sm - 1) / kPB) & 1u, A.status);
-                            __syncwarp();
-                            named_bar_sync(kBarSm, kSmThreads);
-                            tc_fence_after();
-                            // head by head (seldom more than a few), a tile or two a half of
-                            // the warps
-                            uint64_t heads = S.risen[0] | static_cast<uint64_t>(S.risen[1]) << 16 |
-                                             static_cast<uint64_t>(S.risen[2]) << 32 | static_cast<uint64_t>(S.risen[3]) << 48;
-                            while (heads) {
-                                const int h = __ffsll(heads) - 1;
-                                heads &= heads - 1;
-                                const uint32_t o = tmem + lane_off + h;
-                                const float f = S.alpha[h];
-                                const int dd = ndt == 4 ? 2 * g : g;
-                                const uint32_t a = o + o_col(dd), b = o + o_col(dd + 1);
-                                if (dd < kWd) {                    // (its second half)
-                                    const float x = tmem_ld1(a + kHG);
-                                    tmem_wait_ld();
-                                    tmem_st1(a + kHG, x * f);
-                                }
-                                if (ndt == 4) {
-                                    const float x0 = tmem_ld1(a), x1 = tmem_ld1(b);
-                                    tmem_wait_ld();
-                                    tmem_st1(a, x0 * f);
-                                    tmem_st1(b, x1 * f);
-                                } else if (dd < ndt) {
-                                    const float x0 = tmem_ld1(a);
-                                    tmem_wait_ld();
-                                    tmem_st1(a, x0 * f);
-                                }
-                            }
-                            tmem_wait_st();
-                            tc_fence_before();
-                            named_bar_sync(kBarSm, kSmThreads);
                         }
                     }
                     const float mr = m_ref == -INFINITY ? 0.f : m_ref - kTop;
@@ -853,6 +812,46 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int t = 0; t < kTerms; ++t)
                         *reinterpret_cast<uint4 *>(at + t * kTermBytes) = make_uint4(w[0][t], w[1][t], w[2][t], w[3][t]);
+                    if (risen && z != 0) {
+                        const uint32_t mine = __ballot_sync(0xffffffffu, alpha != 1.f) & 0xFFFFu;
+                        if (g == 0 && !upper) S.alpha[hl] = alpha;
+                        if (g == 0 && lane == 0) S.risen[q] = mine;
+                        // (the weights are made meanwhile; the product before this one)
+                        wait_for(&S.pfree[(n_sm - 1) % kPB], ((n_sm - 1) / kPB) & 1u, A.status);
+                        __syncwarp();
+                        named_bar_sync(kBarSm, kSmThreads);
+                        tc_fence_after();
+                        // head by head (seldom more than a few), a tile or two a half of
+                        // the warps
+                        uint64_t heads = S.risen[0] | static_cast<uint64_t>(S.risen[1]) << 16 |
+                                         static_cast<uint64_t>(S.risen[2]) << 32 | static_cast<uint64_t>(S.risen[3]) << 48;
+                        while (heads) {
+                            const int h = __ffsll(heads) - 1;
+                            heads &= heads - 1;
+                            const uint32_t o = tmem + lane_off + h;
+                            const float f = S.alpha[h];
+                            const int dd = ndt == 4 ? 2 * g : g;
+                            const uint32_t a = o + o_col(dd), b = o + o_col(dd + 1);
+                            if (dd < kWd) {                    // (its second half)
+                                const float x = tmem_ld1(a + kHG);
+                                tmem_wait_ld();
+                                tmem_st1(a + kHG, x * f);
+                            }
+                            if (ndt == 4) {
+                                const float x0 = tmem_ld1(a), x1 = tmem_ld1(b);
+                                tmem_wait_ld();
+                                tmem_st1(a, x0 * f);
+                                tmem_st1(b, x1 * f);
+                            } else if (dd < ndt) {
+                                const float x0 = tmem_ld1(a);
+                                tmem_wait_ld();
+                                tmem_st1(a, x0 * f);
+                            }
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
+                        named_bar_sync(kBarSm, kSmThreads);
+                    }
                     fence_proxy_async_smem();
                     mbar_arrive(&S.pfull[pb][g]);
 
