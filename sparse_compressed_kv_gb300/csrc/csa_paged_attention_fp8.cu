@@ -37,9 +37,9 @@
 // bf16 output a chunk's products read 176 KB (the rows once for S and once a term for
 // O^T, the weights once a tile), 32 KB of rows and 12 KB of weights are written: 1,720
 // cycles.  (The products alone: 16 x 32 cycles for S, A in tensor memory, and 24 x 48 for
-// O^T, 1,670.)  The loop takes 1,900; for an f32 output 352 KB, 2,750, and 3,050.
-// 540,000 rows of 32 contexts 73.8 us (3.7 TB/s; the bytes alone 40.8), a million tokens
-// at ratio 4 (262,144 rows) 43.2 us (20.0).
+// O^T, 1,670.)  The loop takes 1,900; for an f32 output 352 KB, 2,750, and 2,900.
+// 540,000 rows of 32 contexts 73.6 us (3.8 TB/s; the bytes alone 40.8), a million tokens
+// at ratio 4 (262,144 rows) 43.3 us (20.0).
 // Three terms of 64 columns read a tile of O^T's A three times; one product of 128
 // or 192 columns would not, but the accumulators would need 512 or 768 columns of tensor
 // memory.  What a call begins and ends with, one long context on all SMs: 3,000 cycles
