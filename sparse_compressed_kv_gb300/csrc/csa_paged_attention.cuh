@@ -134,8 +134,9 @@ struct Work {
 
     __device__ __forceinline__ Work(const PagedArgs &args, WorkSmem<kMaxRec> &smem) : A(args), S(smem) {}
 
+    // (a token's slots may end 57 below 2^31: rounded up they pass 31 bits)
     static __device__ __forceinline__ int chunks(const Rec &r) {
-        return r.b < 0 ? 0 : (rec_slots(r) + kChunk - 1) / kChunk;
+        return r.b < 0 ? 0 : static_cast<int>((static_cast<uint32_t>(rec_slots(r)) + kChunk - 1u) / kChunk);
     }
     static __device__ __forceinline__ int cost_of(int c) { return c > 0 ? c + kSegCost : 1; }
 
