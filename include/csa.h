@@ -646,9 +646,12 @@ csa_status_t csa_paged_read_fp8(const csa_read_fp8_t *read /* (host) */, int32_t
  *   q bf16; a head whose query holds an infinity or NaN gives NaN.  A query
  *     value enters exactly where it is at least 2^-9 of its head's largest, else
  *     off by at most 2^-17 of that.
- * For a bf16 output the weights enter with a relative error of at most 2^-9,
- * for an f32 output 2^-18, each off by at most 2^-24 of the largest besides (in
- * units of scale times weight).
+ * For a bf16 output the weights enter with a relative error of at most 2^-9 +
+ * 2^-11, for an f32 output 2^-18.  Besides, each is off by at most 2^-23 of the
+ * largest that is summed with it (in units of scale times weight; all rows of a
+ * token, or the part of them that one CTA has).  What one is off by there the next
+ * ones make up for: their sum is off by no more than 2^-20 of the largest, and by
+ * 2^-32 of it a row.
  * out, the workspace and the status word share memory with nothing else the
  * call takes (the cache and its scales are not checked). */
 csa_status_t csa_paged_attention_fp8(const csa_paged_layout_t *layout, const csa_params_t *params,

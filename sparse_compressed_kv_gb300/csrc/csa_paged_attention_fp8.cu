@@ -26,12 +26,13 @@
 // 16 q + i, so that both sums lie in the same warp's quarter of tensor memory, and the
 // softmax adds them.
 //
-// P = 2^(l_j - m) s_j as e5m2 terms of 3 bits: what f16 rounds it to, cut into
+// P = 2^(l_j - m) s_j as e5m2 terms of 3 bits: what f16 rounds it to (2^-11), cut into
 // bytes (e5m2 is f16's upper byte), three terms for a bf16 output (2^-9), six for
-// f32 (2^-18).  e4m3 would hold 4 bits a term, but 18 powers of two; e5m2 holds 32:
+// f32 (2^-18 in all).  e4m3 would hold 4 bits a term, but 18 powers of two; e5m2 holds 32:
 // with the maximum m of l_j + log2 s_j brought to 2^7 (and up to 2^15 before it is
-// raised) a weight is cut off below 2^-24 of the largest, so that ten thousands of
-// small weights keep their sum.
+// raised) its last place is 2^-23 of the largest weight, however many terms there are.
+// What a weight is off by there goes into the next one (last_bytes), so that small weights
+// keep their sum.
 //
 // What bounds it, with 64 heads: shared memory, which passes 128 bytes a cycle.  For a
 // bf16 output a chunk's products read 176 KB (the rows once for S and once a term for
@@ -188,6 +189,19 @@ __device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t f16x2_add(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// to magnitudes of at most `most`
+__device__ __forceinline__ uint32_t f16x2_clamp(uint32_t a, uint32_t most) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 t;\n\tmin.f16x2 t, %1, %2;\n\tmax.f16x2 %0, t, %3;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(most), "r"(most | 0x80008000u));
+    return r;
+}
 // the nearest e4m3 values of two f16, the first in the low byte
 __device__ __forceinline__ uint32_t f16x2_e4m3x2(uint32_t h) {
     uint16_t r;
@@ -204,19 +218,41 @@ __device__ __forceinline__ uint32_t upper_bytes(uint32_t &a, uint32_t &b) {
     return t;
 }
 // The last term: rounded, by half of the byte's last place (an addition; the
-// conversion instructions run at a quarter of its rate).
-__device__ __forceinline__ uint32_t last_bytes(uint32_t a, uint32_t b) {
-    return __byte_perm(a + 0x00800080u, b + 0x00800080u, 0x7531);
+// conversion instructions run at a quarter of its rate).  What that adds to or drops
+// from a weight at e5m2's last place, 2^-16, enters the same thread's weight four rows
+// on (`carry`): a sum of small weights is off by half a last place a sequence of rows,
+// not one a row, which equal weights would add up: one row and 60,000 others of 2^-12 to
+// 2^-22 of its weight, f32 output off by up to 4e-5 instead of 2.5e-3.  Above it
+// the rounding is the weight's own, 2^-9 or 2^-18 of it, and kCarry bounds what is handed
+// on.  32 contexts take 73.9 us instead of 73.5, 128-head drafts 75.2 instead of 74.5.  (The
+// maximum brought to 2^10 and rescaled above 2^5.75, 2^13 and 2^2.75: a last place 2^-3 or
+// 2^-6 of this one, 32 contexts 77.4 and 89.0 us, drafts 77.7 and 85.7.)
+constexpr uint32_t kCarry = 0x00800080u;          // 2^-17, twice
+__device__ __forceinline__ uint32_t last_bytes(uint32_t a, uint32_t b, uint32_t (&carry)[2]) {
+    a = f16x2_add(a, carry[0]);
+    b = f16x2_add(b, carry[1]);
+    const uint32_t ta = (a + 0x00800080u) & 0xFF00FF00u, tb = (b + 0x00800080u) & 0xFF00FF00u;
+    carry[0] = f16x2_clamp(f16x2_sub(a, ta), kCarry);
+    carry[1] = f16x2_clamp(f16x2_sub(b, tb), kCarry);
+    return __byte_perm(ta, tb, 0x7531);
+}
+
+// What a head's 16 sequences (four of each thread) begin with, from -120/256 to 120/256
+// of a last place: equal weights are not rounded alike in all of them, and what is
+// left over at their ends cancels.
+__device__ __forceinline__ uint32_t first_carry(int at) {
+    const int v = 8 * (2 * at - 15);
+    return v < 0 ? 0x8000u | -v : v;
 }
 
 // Four weights as kTerms words of four e5m2 values each.
 template <int kTerms>
-__device__ __forceinline__ void split_weights(const float (&p)[4], uint32_t (&t)[kTerms]) {
+__device__ __forceinline__ void split_weights(const float (&p)[4], uint32_t (&t)[kTerms], uint32_t (&carry)[2]) {
     uint32_t a = f16x2(p[0], p[1]), b = f16x2(p[2], p[3]);
     if constexpr (kTerms == 3) {
         t[0] = upper_bytes(a, b);
         t[1] = upper_bytes(a, b);
-        t[2] = last_bytes(a, b);
+        t[2] = last_bytes(a, b, carry);
     } else {
         // four terms hold f16's 11 bits (but for what is below e5m2's last place),
         // the rest of the f32 number makes two more
@@ -227,7 +263,7 @@ __device__ __forceinline__ void split_weights(const float (&p)[4], uint32_t (&t)
         a = f16x2(p[0] - ha.x, p[1] - ha.y);
         b = f16x2(p[2] - hb.x, p[3] - hb.y);
         t[4] = upper_bytes(a, b);
-        t[5] = last_bytes(a, b);
+        t[5] = last_bytes(a, b, carry);
     }
 }
 
@@ -731,6 +767,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
                 const bool cut = rec[i].flags & kRecPart;
                 float m_ref = -INFINITY, l = 0.f, m_flush = -INFINITY;
+                const int sq = 4 * (2 * g + (upper ? 1 : 0));
+                uint32_t carry[2] = {first_carry(sq) | first_carry(sq + 1) << 16,
+                                     first_carry(sq + 2) | first_carry(sq + 3) << 16};
                 const int every = flush_every<kFlush>(nch);
                 const float2 c2 = make_float2(c, c);
                 for (int k = 0, z = 0; k < nch; ++k, ++n_sm, z = z + 1 == every ? 0 : z + 1) {
@@ -819,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             p[2 * e] = v.x;
                             p[2 * e + 1] = v.y;
                         }
-                        split_weights<kTerms>(p, w[u]);
+                        split_weights<kTerms>(p, w[u], carry);
                     }
                     l += sum.x + sum.y;
                     const int pb = n_sm % kPB;
