@@ -222,7 +222,7 @@ __device__ __forceinline__ uint32_t upper_bytes(uint32_t &a, uint32_t &b) {
 // from a weight at e5m2's last place, 2^-16, enters the same thread's weight four rows
 // on (`carry`): a sum of small weights is off by half a last place a sequence of rows,
 // not one a row, which equal weights would add up: one row and 60,000 others of 2^-12 to
-// 2^-22 of its weight, f32 output off by up to 4e-5 instead of 2.5e-3.  Above it
+// 2^-22 of its weight, f32 output off by up to 2.5e-5 instead of 2.5e-3.  Above it
 // the rounding is the weight's own, 2^-9 or 2^-18 of it, and kCarry bounds what is handed
 // on.  32 contexts take 73.9 us instead of 73.5, 128-head drafts 75.2 instead of 74.5.  (The
 // maximum brought to 2^10 and rescaled above 2^5.75, 2^13 and 2^2.75: a last place 2^-3 or
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float c = S.q_scale[hl];
 
                 const bool cut = rec[i].flags & kRecPart;
-                float m_ref = -INFINITY, l = 0.f, m_flush = -INFINITY;
+                float m_ref = -INFINITY, l = 0.f, l_all = 0.f, m_flush = -INFINITY;
                 const int sq = 4 * (2 * g + (upper ? 1 : 0));
                 uint32_t carry[2] = {first_carry(sq) | first_carry(sq + 1) << 16,
                                      first_carry(sq + 2) | first_carry(sq + 3) << 16};
@@ -840,6 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (m_ref != -INFINITY) alpha = exp2f(m_ref - mc);
                             m_ref = mc;
                             l *= alpha;
+                            l_all *= alpha;
                         }
                     }
                     const float mr = m_ref == -INFINITY ? 0.f : m_ref - kTop;
@@ -912,7 +913,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
                     const bool last = k + 1 == nch;
                     if (!last && z + 1 != every) continue;
-                    if (last) {                          // the weights' sum
+                    // the weights' sum, as their products with the rows: every stretch is a
+                    // sum of its own (equal weights beside a large one are rounded alike:
+                    // added chunk by chunk, 262,144 rows left an f32 output off by 1.5e-4
+                    // instead of 4.3e-5)
+                    l_all += l;
+                    l = 0.f;
+                    if (last) {
+                        l = l_all;
                         __syncwarp();
                         l += __shfl_xor_sync(0xffffffffu, l, 16);
                         if (g == 1 && !upper) S.part_l[hl] = l;

@@ -49,7 +49,7 @@ def test_attention_of_as_many_rows_as_a_call_allows(cuda_device, dtype):
 # ---------------------------------------------------------------- small weights
 
 @BOTH
-@pytest.mark.parametrize("T,n", [(1, 60000), (4, 20000), (160, 3500), (160, 20000), (160, 60000)], ids=str)
+@pytest.mark.parametrize("T,n", [(1, 60000), (4, 20000), (160, 3500), (160, 20000), (160, 60000), (153, 262144)], ids=str)
 def test_attention_sums_of_small_weights(cuda_device, T, n, dtype):
     # one row whose weight is 2^12 to 2^22 times that of each of the others, which are all
     # equal, so that whatever rounds their weights rounds them alike
