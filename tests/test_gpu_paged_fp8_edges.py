@@ -49,7 +49,8 @@ def test_attention_of_as_many_rows_as_a_call_allows(cuda_device, dtype):
 # ---------------------------------------------------------------- small weights
 
 @BOTH
-@pytest.mark.parametrize("T,n", [(1, 60000), (4, 20000), (160, 3500), (160, 20000), (160, 60000), (153, 262144)], ids=str)
+@pytest.mark.parametrize("T,n", [(1, 60000), (4, 20000), (160, 3500), (160, 20000), (160, 60000),
+                                 (153, 262144)], ids=str)
 def test_attention_sums_of_small_weights(cuda_device, T, n, dtype):
     # one row whose weight is 2^12 to 2^22 times that of each of the others, which are all
     # equal, so that whatever rounds their weights rounds them alike
@@ -94,3 +95,81 @@ def test_attention_sums_of_small_weights(cuda_device, T, n, dtype):
         tol = F.REL[dtype] + floor + (2 ** -9 + 2 ** -11 if dtype == BF16 else 2 ** -18)
         err = (out[t].double() - ref).norm(dim=1) / ref.norm(dim=1)
         assert float(err.max()) <= tol, f"token {t}: off by {float(err.max()):.3e}, not {tol:.3e}"
+
+
+# ---------------------------------------------------------------- as exact as an f32 output is said to be
+
+# Relative 2-norm errors of a token's output of 64 heads, for the random rows of PagedFp8
+# (emulated: weights in six terms 1.0e-6 at most, the query in two 1.5e-6):
+#   logits: 16 instructions into a truncating accumulator, half a last place (0.36 2^-23 on
+#     average over a binade) of a running sum of two thirds of the final one: 4.6e-7 of
+#     a logit of 2 (root mean square, in powers of two): 1.0e-6;
+#   output: 12 instructions a chunk of 64 rows, likewise: 3.5e-7 a chunk.
+# With the sixth term left out it would be 1.4e-5, with five rounded ones 7e-6 (64 heads).
+def f32_bound(chunks):
+    return 1.0e-6 + 1.5e-6 + 1.0e-6 + 3.5e-7 * chunks
+
+
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("rows,window,chunks", [(64, 0, 1), (150, 40, 3), (256, 128, 6)], ids=str)
+def test_attention_f32_keeps_all_terms(cuda_device, rows, window, chunks, seed):
+    p = F.PagedFp8(100 + seed, row_len=[rows] * 5, tokens=[(b, 4 * rows) for b in range(5)], heads=64, window=window,
+                   page_rows=[16, 64, 3, 8][seed], sinks=seed % 2 == 1)
+    got, status = p.run(cuda_device, F32)
+    assert status == 0
+    F.check(got, p.reference(), F32, rel=f32_bound(chunks))
+
+
+def test_attention_f32_of_peaked_logits(cuda_device):
+    # logits of several hundred: a weight's relative error is its logit's absolute one.
+    # The accumulators': 4.6e-7 of the logit alike for rows whose logits are alike, and
+    # 4 x 0.14 2^-23 x 700 at random, 5e-5; the query's small values: two of 512 off by 0.6
+    # of 2^-17 of 14 at random, times rows of 17 and the scale: 7e-5; together 9e-5 (root mean
+    # square), times weight and what it is taken from, at most half the output: six times that.
+    # (A bf16 output's weights alone are off by up to 2^-9 + 2^-11, 2.4e-3.)
+    p = F.PagedFp8(5, row_len=[640], tokens=[(0, 2560)], heads=64, page_rows=64, window=0, spread=0)
+    j = torch.arange(640)
+    at = (p.table[0, j // 64].long(), j % 64)
+    codes, k = F.quantise((p.cache[at] * (1 + j[:, None] / 40)).numpy())
+    p.codes[at], p.scales[at] = torch.from_numpy(codes), torch.from_numpy(k).float()
+    p.requantised()
+    p.q *= 4
+    ref = p.reference()
+    got, status = p.run(cuda_device, F32)
+    assert status == 0
+    err = (got.double().cpu() - ref).norm(dim=2) / ref.norm(dim=2)
+    assert float(err.max()) <= 6 * 9e-5
+
+
+# ---------------------------------------------------------------- long sums of a bf16 output
+
+def test_attention_bf16_sums_in_several_stretches(cuda_device):
+    # 45,000 rows in one CTA are three stretches between which the sums go to the
+    # partial and back; the second stretch's rows raise the maximum by more than 2^8, and the
+    # first one's still weigh a tenth
+    dev, n, T = cuda_device, 45056, 320
+    g = torch.Generator(device=dev).manual_seed(31)
+    rows = torch.randn(n, H.HD, device=dev, generator=g)
+    rows *= torch.tensor([1.0, 2.4, 1.5], device=dev)[torch.arange(n, device=dev) * 3 // n][:, None]
+    cache, scales = torch.zeros(n // 32, 32, H.HD, device=dev).to(F8), torch.zeros(n // 32, 32, device=dev)
+    table = torch.randperm(n // 32, device=dev, generator=g).int()[None]
+    j = torch.arange(n, device=dev)
+    status = status_word(dev)
+    csa.csa_paged_append_fp8(csa.AppendJobsFp8([csa.AppendJobFp8(rows, table[0, j // 32].long() * 32 + j % 32, cache,
+                                                                 scales, 32)]), status)
+    q = torch.randn(T, 64, H.HD, device=dev, generator=g).to(BF16)
+    pos = 4 * (n - torch.arange(T, device=dev) * 7)
+    layout = csa.PagedLayoutFp8(torch.zeros(T, dtype=torch.int32, device=dev), pos, torch.tensor([n], device=dev),
+                                table, 32)
+    prm = csa.params(64, 1, 0, 4)
+    out = torch.empty(T, 64, H.HD, device=dev, dtype=BF16)
+    csa.csa_paged_attention_fp8(layout, prm, cache, scales, q, out, status, csa.paged_workspace(layout, prm))
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    vals = F.values(*F.quantise(rows.double().cpu().numpy())).to(dev)
+    for t in range(0, T, 53):
+        v = vals[:int(pos[t]) // 4]
+        w = torch.softmax(prm.scale * q[t].double() @ v.T, 1)
+        assert 0.01 < float(w[:, :n // 3].sum(1).mean()) < 0.5
+        ref = w @ v
+        assert (out[t].double() - ref).norm() <= F.REL[BF16] * ref.norm()
