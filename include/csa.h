@@ -573,7 +573,8 @@ csa_status_t csa_paged_attention(const csa_paged_layout_t *layout, const csa_par
  * scale for each block of tokens and head.  Row r of page p has its codes at
  * (p * page_stride + r) * width and its scale at p * scale_stride + r
  * (page_stride, scale_stride >= page_rows: several layers may share either
- * pool).  csa_page_plan serves these caches as it does the others. */
+ * pool; scales need 4-byte alignment only, slots 8).  csa_page_plan serves these
+ * caches as it does the others. */
 
 /* csa_paged_append_fp8: quantises row i of `rows` (bf16 or f32) into slot
  * slots[i], for up to four (rows, cache) pairs in one launch.  The scale is
@@ -640,18 +641,23 @@ csa_status_t csa_paged_read_fp8(const csa_read_fp8_t *read /* (host) */, int32_t
  * status bits, limits and the workspace (csa_paged_workspace_size) are
  * csa_paged_attention's, with layout->swa_kv the ring's codes [B, swa_cap, hd] and
  * swa_scales [B, swa_cap] beside it (both may be NULL without a window).
- *   cache, scales: width hd; only rows named by the table are read into the
+ *   cache, scales: width hd (scales and swa_scales: 4-byte aligned); only rows
+ *     named by the table are read into the
  *     result, the rest may hold anything.  Scales may be any f32 numbers of
  *     magnitude 2^-60 to 2^60 (or 0); a NaN in a row that is seen gives NaN.
  *   q bf16; a head whose query holds an infinity or NaN gives NaN.  A query
  *     value enters exactly where it is at least 2^-9 of its head's largest, else
- *     off by at most 2^-17 of that.
+ *     off by at most 2^-17 of that (of 2^-119 where the largest is below that).
  * For a bf16 output the weights enter with a relative error of at most 2^-9 +
  * 2^-11, for an f32 output 2^-18.  Besides, each is off by at most 2^-23 of the
  * largest that is summed with it (in units of scale times weight; all rows of a
  * token, or the part of them that one CTA has).  What one is off by there the next
  * ones make up for: their sum is off by no more than 2^-20 of the largest, and by
- * 2^-32 of it a row.
+ * 2^-32 of it a row.  The sums are the tensor cores', which drop what lies below
+ * the last place of the running sum; every 1,728 rows at most (f32 output; 21,824
+ * for bf16) they are added, rounded, to a sum in f32.  For random rows an f32 output
+ * is off by 0.8e-6 to 3.5e-6 from float64 (relative, 2-norm), a bf16 output by 1.6e-3
+ * to 1.8e-3 (rounding the exact value to bf16: 1.6e-3 to 1.7e-3).
  * out, the workspace and the status word share memory with nothing else the
  * call takes (the cache and its scales are not checked). */
 csa_status_t csa_paged_attention_fp8(const csa_paged_layout_t *layout, const csa_params_t *params,

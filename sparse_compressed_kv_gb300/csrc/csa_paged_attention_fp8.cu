@@ -38,9 +38,11 @@
 // bf16 output a chunk's products read 176 KB (the rows once for S and once a term for
 // O^T, the weights once a tile), 32 KB of rows and 12 KB of weights are written: 1,720
 // cycles.  (The products alone: 16 x 32 cycles for S, A in tensor memory, and 24 x 48 for
-// O^T, 1,670.)  The loop takes 1,900; for an f32 output 352 KB, 2,750, and 2,900.
-// 540,000 rows of 32 contexts 73.6 us (3.8 TB/s; the bytes alone 40.8), a million tokens
-// at ratio 4 (262,144 rows) 43.3 us (20.0).
+// O^T, 1,670.)  The loop takes 1,920; for an f32 output 352 KB, 2,750, and 2,960 (3,200
+// where a segment goes through the partial every 27 chunks).  540,000 rows of 32 contexts
+// 74.2 us (3.7 TB/s; the bytes alone 40.8), a million tokens at ratio 4 (262,144 rows) 43.6
+// us (20.0).  Beside a rule below stand its two sides in this build, replayed from a graph;
+// where the other side's code is gone, in the build that chose.
 // Three terms of 64 columns read a tile of O^T's A three times; one product of 128
 // or 192 columns would not, but the accumulators would need 512 or 768 columns of tensor
 // memory.  What a call begins and ends with, one long context on all SMs: 3,000 cycles
@@ -77,7 +79,8 @@ constexpr int kPieceBytes = kTerms * kTermBytes;
 // Tensor memory: S in buffers of 64 columns; O^T, 4 tiles of 64 columns (heads); the
 // query, 128 rows x 512 codes.  With an f32 output's six terms the columns of a second S
 // buffer go to the first tile, which takes two terms from one reading of its rows into 64
-// columns each (128-head drafts 81.0 -> 78.6 us; a bf16 output's three: 0 to 2% slower).
+// columns each (128-head drafts 75.5 us, with two buffers instead 78.7; a bf16 output's
+// three: 32 contexts 73.8 us and 74.2, one of 8,192 rows 14.2 either way).
 template <int kTerms>
 constexpr int kSBufs = kTerms == 3 ? 2 : 1;
 template <int kTerms>
@@ -88,12 +91,13 @@ constexpr int kOCol = 64 * kSBufs<kTerms>;
 constexpr int kQCol = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxRec = 32;                     // segments a CTA lists at a time
-// A segment's beginning and end, in chunks: 1, 2, 3 and 4 are 29.9, 27.6, 27.5 and 27.7 us
-// with 128 contexts at ratio 128, 76.9, 76.0, 75.6 and 75.8 with 32 long ones, 82.7, 78.4,
-// 78.2 and 79.6 with 128-head drafts.
+// A segment's beginning and end, in chunks: 1, 2, 3 and 4 are 29.9, 27.7, 27.1 and 27.3 us
+// with 128 contexts at ratio 128, 75.6, 74.5, 74.2 and 73.6 with 32 long ones, 80.0, 76.7,
+// 75.5 and 77.2 with 128-head drafts.
 constexpr int kSegCost = 3;
 // Chunks a token may exceed the mean before tokens are cut: with 6 a token of 6 chunks by
-// itself takes 14.6 us instead of 9.7; 2, 3 and 4 are alike.
+// itself takes 13.4 us instead of 9.7 (16 heads, f32 output: 14.6 and 8.9); 2, 3 and 4 are
+// alike.
 constexpr int kCutAbove = 4;
 // Chunks between roundings of the accumulator, at most: what the tensor cores drop grows
 // with the products that are added in a row (six or three terms, 64 rows).
@@ -102,7 +106,7 @@ constexpr float kTop = 7.f;                     // log2 of the weight that the m
 
 // mbar_wait whose loop is a call: the first try is nearly all that stays in line (what
 // the roles run together is more than the instruction caches next to the schedulers
-// hold; 32 contexts 95.6 -> 92.6 us).
+// hold; 32 contexts 74.2 us, with the loop in line 75.5).
 __device__ __noinline__ void wait_slowly(uint64_t *bar, uint32_t parity, int32_t *status) {
     mbar_wait(bar, parity, status);
 }
@@ -270,7 +274,7 @@ __device__ __forceinline__ void split_weights(const float (&p)[4], uint32_t (&t)
 // 16 columns of a head of the query as codes hi and lo.  Returns the factor that takes
 // sums of codes back to the query's units (NaN where the query is not finite).  (Two
 // numbers at a time by conversions; by integer operations on their bits, 12 instead of 10
-// instructions, the 64 heads take 5,000 cycles instead of 4,000.)
+// instructions, the 64 heads took 5,000 cycles instead of 4,000.)
 __device__ __forceinline__ float split_query(const uint4 &v0, const uint4 &v1, uint4 &hi, uint4 &lo) {
     const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
     uint32_t top = 0;
@@ -278,7 +282,7 @@ __device__ __forceinline__ float split_query(const uint4 &v0, const uint4 &v1, u
     for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
     top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
     // 1.m 2^(e - 127) to 2^7 (f16 holds what e4m3's terms need: down to 2^-14, and
-    // 8 bits); by halves, since the factor may be out of range
+    // 8 bits), as far as a factor of 2^126 does it: below 2^-119 a head keeps fewer bits
     const int k = min(134 - static_cast<int>(top >> 7), 126);
     const float f = exponent_f32(k);
     const float2 s1 = make_float2(f, f);
@@ -478,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         tc_fence_after();
                         if (elect_one()) {
-                            // (all columns, unrolled: the loop's issue alone held the tensor
-                            // cores up, 32 contexts 82.3 us instead of 76.1)
+                            // (all columns, unrolled: the loop's issue alone holds the tensor
+                            // cores up, 32 contexts 74.9 us instead of 74.2, drafts 76.7 and 75.5)
                             if (ndt == 4) {
 #pragma unroll
                                 for (int dd = 0; dd < 4; ++dd) product(dd, ad, pd, acc);
@@ -501,8 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------- row fetch
             // The warp walks the list's chunks, a row of each a lane: two chunks before it
             // is copied its page number is on its way from the table, one before it its
-            // scale.  (Whole chunks by turns, two rows a lane, take as long in the loop, but a
-            // call's first rows start later: 256 rows 10.7 us instead of 9.6.)
+            // scale.  (Whole chunks by turns, two rows a lane, took as long in the loop, but a
+            // call's first rows started later: 256 rows 10.7 us instead of 9.6.)
             const int li = warp - 10;
             int bad = 0;
             struct Cursor {
@@ -624,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d(rows + lane * kGroupBytes, &tm_rows, 0, y >= 0 ? y : A.total_rows, 0, full, pol);
                 if (now.box != 0x01010101u) {
                     // eight lanes take 128 columns of a row, four rows an instruction (a row an
-                    // instruction, 128 contexts in pages of two rows: 28.6 us instead of 27.7)
+                    // instruction, 128 contexts in pages of two rows, were 28.6 us instead of 27.7)
 #pragma unroll 1
                     for (int x = 0; x < 4; ++x) {
                         if (now.box >> (8 * x) & 1u) continue;
@@ -768,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool cut = rec[i].flags & kRecPart;
                 float m_ref = -INFINITY, l = 0.f, l_all = 0.f, m_flush = -INFINITY;
                 const int sq = 4 * (2 * g + (upper ? 1 : 0));
+                // (kept where a maximum rises: at most half a last place)
                 uint32_t carry[2] = {first_carry(sq) | first_carry(sq + 1) << 16,
                                      first_carry(sq + 2) | first_carry(sq + 3) << 16};
                 const int every = flush_every<kFlush>(nch);
@@ -813,8 +818,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // maximum rises by more than kRescaleAbove (the first one does) rescales
                     // what has been accumulated.  The largest logit plus the largest logarithm
                     // of the 32 rows tells nearly always that none does.  (With every row's
-                    // logarithm read in every chunk one million tokens take 44.0 us instead of
-                    // 43.2, 32 contexts 74.6 instead of 73.8, but 8,192 rows 13.8 instead of 14.0.)
+                    // logarithm read in every chunk one million tokens take 44.9 us instead of
+                    // 43.6, 32 contexts 77.2 instead of 74.2, but 8,192 rows 14.1 instead of 14.2.)
                     float mc = fmaxf(x[0].x, x[0].y);
 #pragma unroll
                     for (int j = 1; j < 8; ++j) mc = fmaxf(mc, fmaxf(x[j].x, x[j].y));

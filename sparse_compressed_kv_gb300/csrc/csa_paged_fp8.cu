@@ -50,13 +50,16 @@ struct Values {
 };
 
 // One warp a row: its values stay in registers between the maximum and the
-// codes, so a row is read once; a lane has up to kUnits runs of 8 values.  Bound by the
-// bytes: kRows rows at a time, and the slots of the next ones on their way, keep enough
-// of them in flight, and CTAs that stay (8 per SM) walk on without a start of their own.
-// 163,840 bf16 rows of 512 values and two caches take 41.2 us, 6.2 TB/s (the copy's rate:
-// 37.4 us); one row at a time 50.6, three 54.8 (fewer CTAs fit), two with 4 and 16 CTAs
-// per SM 42.3 and 41.4.  32 rows: 2.05 us, a launch and two trips to memory.  Rows above
-// 512 values take one at a time (twice the registers).
+// codes, so a row is read once; a lane has up to kUnits runs of 8 values.  kRows rows at a
+// time, and the slots of the next ones on their way, keep bytes in flight, and CTAs that
+// stay (8 per SM) walk on without a start of their own.  Two caches, 163,840 bf16 rows of
+// 512 values of which 120,136 have a slot (the rings keep the newest ones): 41.4 us, 4.5
+// TB/s of the 186 MB that move (the copy's rate: 27.4 us); rows without a slot take their
+// turns all the same.  120,136 rows that all have one, at random: 37.8 us, 4.9 TB/s, from
+// f32 56.3 us, 5.5.  So DRAM is not what bounds it; what does was not found out.  One row
+// at a time took 50.6, three 54.8 (fewer CTAs fit), two with 4 and 16 CTAs per SM 42.3 and
+// 41.4.  40 rows: 1.9 us, a launch and two trips to memory.  Rows above 512 values take one
+// at a time (twice the registers).
 template <int kUnits, int kRows>
 __global__ void __launch_bounds__(kFp8Threads) append_fp8_kernel(const AppendFp8Args A, int32_t *status) {
     pdl_wait();
@@ -180,7 +183,7 @@ struct ReadFp8Args {
 
 // One warp a row, 16 bytes of the output a lane at a time, two ahead of the first
 // store, and the slot of the next row.  Bound by the bytes: 131,072 rows of 512 values to
-// f32 take 54.3 us, 6.2 TB/s (the copy's rate: 49.7 us), with up to 64 CTAs' worth of rows
+// f32 take 54.9 us, 6.1 TB/s (the copy's rate: 49.7 us), with up to 64 CTAs' worth of rows
 // per SM; 16: 55.3; a thread for 16 bytes, without the slots ahead: 65.6.
 template <bool kF32>
 __global__ void __launch_bounds__(kFp8Threads) read_fp8_kernel(const ReadFp8Args A, int32_t *status) {
