@@ -173,3 +173,67 @@ def test_attention_bf16_sums_in_several_stretches(cuda_device):
         assert 0.01 < float(w[:, :n // 3].sum(1).mean()) < 0.5
         ref = w @ v
         assert (out[t].double() - ref).norm() <= F.REL[BF16] * ref.norm()
+
+
+# ---------------------------------------------------------------- sizes and orders
+
+def test_append_and_read_rows_past_32_bit_offsets(cuda_device):
+    # 4.3 GiB of rows in, and of rows out; the cache's codes pass 2^31 bytes
+    dev, n, P = cuda_device, (1 << 22) + 77, 64
+    g = torch.Generator(device=dev).manual_seed(41)
+    rows = torch.empty(n, 512, dtype=BF16, device=dev)
+    for a in range(0, n, 1 << 20):
+        rows[a:a + (1 << 20)] = torch.randn(min(1 << 20, n - a), 512, device=dev, generator=g)
+    pages = -(-n // P)
+    slots = torch.arange(n, device=dev).flip(0)
+    cache, scales = torch.zeros(pages, P, 512, dtype=torch.uint8, device=dev), torch.zeros(pages, P, device=dev)
+    out, status = torch.zeros(n, 512, dtype=BF16, device=dev), status_word(dev)
+    csa.csa_paged_append_fp8(csa.AppendJobsFp8([csa.AppendJobFp8(rows, slots, cache.view(F8), scales, P)]), status)
+    csa.csa_paged_read_fp8(cache.view(F8), scales, slots, out, status, P)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for a in range(0, n, 1 << 18):
+        x, y = rows[a:a + (1 << 18)].float(), out[a:a + (1 << 18)].float()
+        assert bool(((x - y).abs() <= torch.maximum(x.abs() * 2 ** -4, x.abs().amax(1, keepdim=True) * 2 ** -17)).all())
+    at = torch.tensor([0, 1, n // 2, n - 2, n - 1], device=dev)
+    assert torch.equal(out[at].double().cpu(), F.values(*F.quantise(rows[at].double().cpu().numpy())))
+
+
+@BOTH
+def test_attention_of_tokens_in_any_order(cuda_device, dtype):
+    # sequences and positions out of order, padding between, a position twice (with two queries)
+    tokens = [(2, 900), (0, 40), (-1, -1), (1, 1300), (2, 901), (0, 400), (1, 1300), (2, 10), (-1, -1), (0, 399)]
+    p = F.PagedFp8(71, row_len=[100, 325, 225], tokens=tokens, heads=24, sinks=True, swa_cap=1500)
+    got, status = p.run(cuda_device, dtype)
+    assert status == 0
+    F.check(got, p.reference(), dtype, [t for t, (b, _) in enumerate(tokens) if b >= 0])
+    assert bool((got[[2, 8]] == 7).all())
+
+
+@BOTH
+@pytest.mark.parametrize("row_len,pos,window", [([0], 9000, 7000), ([37], 5151, 5000), ([2500], 10003, 3001)],
+                         ids=str)
+def test_attention_of_wide_windows(cuda_device, row_len, pos, window, dtype):
+    p = F.PagedFp8(72, row_len=row_len, tokens=[(0, pos), (0, pos - 2)], heads=40, window=window, swa_cap=window + 9,
+                   page_rows=5)
+    got, status = p.run(cuda_device, dtype)
+    assert status == 0
+    F.check(got, p.reference(), dtype)
+
+
+def test_attention_of_the_most_tokens_and_heads(cuda_device):
+    tokens = [(t % 3, 200 + t % 57) for t in range(8192)]
+    p = F.PagedFp8(73, row_len=[64, 50, 3], tokens=tokens, heads=128, window=30, swa_cap=100)
+    some = list(range(0, 8192, 431)) + [8191]
+    got, status = p.run(cuda_device, F32)
+    assert status == 0
+    F.check(got, p.reference(tokens=some), F32, some)
+
+
+@BOTH
+def test_attention_of_one_page_of_many_rows(cuda_device, dtype):
+    p = F.PagedFp8(74, row_len=[70001, 3], tokens=[(0, 4 * 69000 + 2), (1, 14)], heads=16, page_rows=1 << 17, window=0,
+                   spare_pages=0)
+    got, status = p.run(cuda_device, dtype)
+    assert status == 0
+    F.check(got, p.reference(), dtype)
