@@ -652,8 +652,8 @@ csa_status_t csa_paged_read_fp8(const csa_read_fp8_t *read /* (host) */, int32_t
  * 2^-11, for an f32 output 2^-18.  Besides, each is off by at most 2^-23 of the
  * largest that is summed with it (in units of scale times weight; all rows of a
  * token, or the part of them that one CTA has).  What one is off by there the next
- * ones make up for: their sum is off by no more than 2^-20 of the largest, and by
- * 2^-32 of it a row.  The sums are the tensor cores', which drop what lies below
+ * ones make up for: their sum is off by no more than 2^-19 of the largest, and by
+ * 2^-31 of it a row.  The sums are the tensor cores', which drop what lies below
  * the last place of the running sum; every 1,728 rows at most (f32 output; 21,824
  * for bf16) they are added, rounded, to a sum in f32.  For random rows an f32 output
  * is off by 0.8e-6 to 3.5e-6 from float64 (relative, 2-norm), a bf16 output by 1.6e-3

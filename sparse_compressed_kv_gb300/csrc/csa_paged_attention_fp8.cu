@@ -231,7 +231,10 @@ __device__ __forceinline__ uint32_t upper_bytes(uint32_t &a, uint32_t &b) {
 // on.  32 contexts take 73.9 us instead of 73.5, 128-head drafts 75.2 instead of 74.5.  (The
 // maximum brought to 2^10 and rescaled above 2^5.75, 2^13 and 2^2.75: a last place 2^-3 or
 // 2^-6 of this one, 32 contexts 77.4 and 89.0 us, drafts 77.7 and 85.7.)
-constexpr uint32_t kCarry = 0x00800080u;          // 2^-17, twice
+// (A little less than half a last place: with all of it, which a large weight's rounding
+// leaves, rows without weight get 2^-16 and -2^-16 by turns; 131,008 of them beside 64
+// others, f32 output off by 7.5e-6 instead of 1.1e-6.)
+constexpr uint32_t kCarry = 0x007F007Fu;          // 127/128 of 2^-17, twice
 __device__ __forceinline__ uint32_t last_bytes(uint32_t a, uint32_t b, uint32_t (&carry)[2]) {
     a = f16x2_add(a, carry[0]);
     b = f16x2_add(b, carry[1]);

@@ -237,3 +237,40 @@ def test_attention_of_one_page_of_many_rows(cuda_device, dtype):
     got, status = p.run(cuda_device, dtype)
     assert status == 0
     F.check(got, p.reference(), dtype)
+
+
+def test_attention_rows_without_weight_add_nothing(cuda_device):
+    # 64 rows that hold all the weight, then 131,008 whose weights are below 2^-50 of theirs:
+    # what the last of the first rounds away must not go on through the others.  A weight
+    # of the 64 is off at random by 2.9e-6 (logits of 63 powers of two in 16 truncated steps,
+    # 4 x 0.14 2^-23 of them), 1.0e-6 (six terms) and 4e-6 (the query's small values, two of
+    # 512 off by 0.6 of 2^-17 of 14); times a row's part that is not in all of them, 22.6, and
+    # the weights' 2-norm, at most 0.25, over an output of 11.3: half of each
+    dev, T, n, live, heads = cuda_device, 153, 1 << 17, 64, 64
+    g = torch.Generator(device=dev).manual_seed(51)
+    randn = lambda *shape: torch.randn(*shape, device=dev, generator=g)
+    u = randn(H.HD)
+    rows = randn(n, H.HD)
+    rows -= (rows @ u)[:, None] * u / (u @ u)                # nothing along u
+    rows[:live] += 0.5 * u
+    q = randn(T, heads, H.HD) + 40 * H.HD ** 0.5 / (0.5 * float(u @ u)) * u
+    cache, scales = torch.zeros(n // 16, 16, H.HD, device=dev).to(F8), torch.zeros(n // 16, 16, device=dev)
+    status = status_word(dev)
+    csa.csa_paged_append_fp8(csa.AppendJobsFp8([csa.AppendJobFp8(rows, torch.arange(n, device=dev), cache, scales,
+                                                                 16)]), status)
+    layout = csa.PagedLayoutFp8(torch.zeros(T, dtype=torch.int32, device=dev),
+                                torch.full((T,), 4 * n, dtype=torch.int64, device=dev), torch.tensor([n], device=dev),
+                                torch.arange(n // 16, device=dev).int()[None], 16)
+    prm = csa.params(heads, 1, 0, 4)
+    q, out = q.to(BF16), torch.empty(T, heads, H.HD, device=dev)
+    csa.csa_paged_attention_fp8(layout, prm, cache, scales, q, out, status, csa.paged_workspace(layout, prm))
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    vals = F.values(*F.quantise(rows.double().cpu().numpy())).to(dev)
+    for t in range(0, T, 38):
+        l = prm.scale * q[t].double() @ vals.T
+        assert 25 < float(l[:, :live].amax(1).min()) and float(l.max()) < 55
+        assert float((l[:, live:].amax(1) - l[:, :live].amax(1)).max()) < -34.7
+        ref = torch.softmax(l, 1) @ vals
+        err = (out[t].double() - ref).norm() / ref.norm()
+        assert err <= (2.9e-6 + 1.0e-6 + 4e-6) / 2
